@@ -294,6 +294,121 @@ m3_status m3_siso_chunked_fwd_noalloc(const void *x, const float *dt, const floa
 enum { M3_WS_SISO = 0, M3_WS_MIMO = 1, M3_WS_BWD_SISO = 2, M3_WS_BWD_MIMO = 3 };
 size_t m3_workspace_bytes(int which, m3_dims d, m3_dtype dtype);
 
+/* ---- Linear attention with a decay for each head ------------------------
+ * The layer's other mixer beside the scan: no rotation, no trapezoid, one
+ * fixed decay g_h = exp(log_decay[h]) for each head (for learned or per-token
+ * decays use the scan with lam = 1 and theta = 0).  The pages have no
+ * counterpart to these entry points.
+ *
+ *   S_t = g S_{t-1} + k_t v_t^T      (dstate x headdim, fp32)
+ *   y_t = scale S_t^T q_t
+ *
+ *   q, k       (batch, seqlen, ngroups, dstate)   M3_F32 or M3_BF16; head h
+ *              reads group h / (nheads / ngroups); 0 groups = nheads
+ *   v, y       (batch, seqlen, nheads, headdim)   same dtype
+ *   log_decay  (nheads) fp32, natural logarithm, <= 0 (-inf: no memory; values
+ *              above 0 grow, unchecked)
+ *   s          (batch, nheads, dstate, headdim)   fp32
+ *   lengths    (batch) int32 on the device, or NULL for seqlen everywhere:
+ *              sequence b has lengths[b] tokens (taken into [0, seqlen]); the
+ *              tokens behind them are not read into any result, their rows of
+ *              y and of the gradients are written as zeros, and s_final is the
+ *              state after the last real token (s0 itself when there is none).
+ *
+ * ld_q, ld_k, ld_v: elements between the rows of consecutive tokens (of
+ * consecutive sequences for the step), 0 for contiguous: q, k and v may be
+ * slices of one fused projection, or single tokens of a longer tensor.  Rows
+ * of one token stay contiguous, the batch stride is seqlen * ld, and the
+ * bases of q, k and v need only the alignment of their type; everything else
+ * is contiguous and 16-byte aligned.
+ *
+ * bf16 inputs with dstate and headdim <= 128 and multiples of 8 (row strides
+ * too), at 16-byte aligned bases, run on the tensor cores; everything else in
+ * fp32 arithmetic.  A
+ * non-finite q, k or v reaches the rows that depend on it, and may reach
+ * earlier rows of its own 64-token chunk; one behind a sequence's length
+ * reaches nothing. */
+typedef struct {
+    int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
+    int64_t ld_q, ld_k, ld_v;
+} m3_linattn_dims;
+
+/* Prompts: y and, when s_final is not NULL, the final state, from s0 (NULL
+ * for zero).  scale multiplies the answers (dstate^-1/2 is usual).
+ * workspace: m3_linattn_workspace_bytes(M3_WS_LINATTN_FWD, d, dtype) bytes.
+ * Limits: dstate, headdim <= 256, dstate * headdim <= 16384, and those of
+ * m3_limits on the other sizes. */
+m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3_dtype dtype,
+                                 const float *log_decay, float scale, const float *s0,
+                                 const int32_t *lengths, m3_linattn_dims d, void *y, float *s_final,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of every (batch, head) lane: q_t, k_t (batch, ngroups, dstate),
+ * v_t, y_t (batch, nheads, headdim); s is updated in place.  d.seqlen is
+ * ignored. */
+m3_status m3_linattn_step_decode(const void *q_t, const void *k_t, const void *v_t, m3_dtype dtype,
+                                 const float *log_decay, float scale, m3_linattn_dims d, float *s,
+                                 void *y_t, void *stream);
+
+/* Gradients, contiguous, in the shapes and the dtype of their inputs (ds0 in
+ * fp32), each rounded once from an fp32 sum; NULL = not wanted.  log_decay is
+ * a constant: it has no gradient. */
+typedef struct {
+    void *dq, *dk, *dv;
+    float *ds0;
+} m3_linattn_grads;
+
+/* Backward of m3_linattn_chunked_fwd for the loss <dy, y> + <ds_final,
+ * s_final>: dy (batch, seqlen, nheads, headdim) contiguous, ds_final fp32 or
+ * NULL for zero.  Gradients of shared q and k heads are summed over the heads
+ * that share them in a fixed order: repeated calls give identical bits.
+ * workspace: m3_linattn_workspace_bytes(M3_WS_LINATTN_BWD, d, dtype) bytes. */
+m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3_dtype dtype,
+                                 const float *log_decay, float scale, const float *s0,
+                                 const int32_t *lengths, m3_linattn_dims d, const void *dy,
+                                 const float *ds_final, const m3_linattn_grads *grads, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+enum { M3_WS_LINATTN_FWD = 0, M3_WS_LINATTN_BWD = 1 };
+size_t m3_linattn_workspace_bytes(int which, m3_linattn_dims d, m3_dtype dtype);
+
+/* ---- Group norm with an activation, channels last ------------------------
+ * What follows either mixer in a block: the norm of each head's channels
+ * (batch * seqlen tokens as batch, seqlen 1, ngroups = heads) or of whole
+ * sequences, and the activation or the gate.
+ *
+ *   x, y, gate  (batch, seqlen, channels)   M3_F32 or M3_BF16
+ *   weight, bias (channels) fp32, NULL for ones / zeros
+ *   mean, rstd  (batch, ngroups) fp32, over the seqlen tokens and the
+ *               channels / ngroups channels of a group: rstd =
+ *               1 / sqrt(biased variance + eps)
+ *   u = (x - mean) rstd weight + bias
+ *   y = act(u) without a gate, u act(gate) with one
+ * channels <= 16384 and a multiple of ngroups. */
+typedef enum { M3_ACT_NONE = 0, M3_ACT_SILU = 1, M3_ACT_GELU = 2, M3_ACT_RELU = 3 } m3_act; /* GELU: the erf form */
+
+typedef struct {
+    int64_t batch, seqlen, channels, ngroups;
+} m3_norm_dims;
+
+/* mean and rstd may be NULL when they are not wanted.
+ * workspace: m3_group_norm_workspace_bytes(M3_WS_NORM_FWD, d, dtype) bytes. */
+m3_status m3_group_norm_fwd(const void *x, m3_dtype dtype, const float *weight, const float *bias,
+                            const void *gate, m3_act act, float eps, m3_norm_dims d, void *y, float *mean,
+                            float *rstd, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients from dy and the forward's mean and rstd: dx and dgate in the
+ * dtype of x, dweight and dbias (channels) fp32, each NULL when not wanted.
+ * Sums run in a fixed order: repeated calls give identical bits.
+ * workspace: m3_group_norm_workspace_bytes(M3_WS_NORM_BWD, d, dtype) bytes. */
+m3_status m3_group_norm_bwd(const void *x, const void *dy, m3_dtype dtype, const float *weight,
+                            const float *bias, const void *gate, m3_act act, const float *mean,
+                            const float *rstd, m3_norm_dims d, void *dx, float *dweight, float *dbias,
+                            void *dgate, void *workspace, size_t workspace_bytes, void *stream);
+
+enum { M3_WS_NORM_FWD = 0, M3_WS_NORM_BWD = 1 };
+size_t m3_group_norm_workspace_bytes(int which, m3_norm_dims d, m3_dtype dtype);
+
 /* Static description of a status code (never NULL). */
 const char *m3_status_string(m3_status s);
 

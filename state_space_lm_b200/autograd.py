@@ -1,9 +1,9 @@
-"""Differentiable Mamba-3 scan for PyTorch: the chunked forward and
-m3_chunked_bwd behind one torch.autograd.Function.
+"""Differentiable Mamba-3 scan, linear attention and group norm for PyTorch:
+each forward and its backward behind one torch.autograd.Function.
 
 Argument marshalling only: the forward calls m3_siso_chunked_fwd or
-m3_mimo_chunked_fwd, the backward calls m3_chunked_bwd, and every gradient
-comes from the CUDA library (there is no other implementation behind these
+m3_mimo_chunked_fwd, the backward calls m3_chunked_bwd (m3_linattn_* and
+m3_group_norm_* for the other two), and every gradient comes from the CUDA library (there is no other implementation behind these
 names).  The initial states and the final states take part in autograd too,
 so a sequence can be split into pieces whose states are chained.
 """
@@ -62,3 +62,59 @@ def mamba3_scan(x, dt, A, lam, theta, B, C, D, chunk=64, W_x=None, W_y=None, h0=
     """Differentiable scan: returns y, h_final, prevBx_final, angle_final.
     Shapes and dtypes as in include/m3.h (x, B, C bf16 or fp32; the rest fp32)."""
     return Mamba3Scan.apply(x, dt, A, lam, theta, B, C, D, W_x, W_y, h0, prevBx0, angle0, chunk)
+
+
+class LinearAttention(torch.autograd.Function):
+    """Returns (y, s_final); gradients of q, k, v and s0."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, scale, s0, lengths):
+        if ctx.needs_input_grad[3]:
+            raise ValueError("log_decay is a constant of linear_attention: it has no gradient (mamba3_scan with "
+                             "lam = 1 and theta = 0 learns its decays)")
+        y, sf = m3.linattn_chunked_fwd(q, k, v, log_decay, scale=scale, s0=s0, lengths=lengths)
+        ctx.save_for_backward(q, k, v, log_decay, s0, lengths)
+        ctx.scale = scale
+        return y, sf
+
+    @staticmethod
+    def backward(ctx, dy, ds):
+        q, k, v, log_decay, s0, lengths = ctx.saved_tensors
+        need = dict(zip(("dq", "dk", "dv"), ctx.needs_input_grad[:3]), ds0=ctx.needs_input_grad[5])
+        want = tuple(n for n, on in need.items() if on)
+        dy = torch.zeros_like(v, memory_format=torch.contiguous_format) if dy is None else dy.to(v.dtype).contiguous()
+        g = m3.linattn_chunked_bwd(q, k, v, log_decay, dy, scale=ctx.scale, s0=s0,
+                                   ds_final=None if ds is None else ds.contiguous(), lengths=lengths, want=want)
+        return g.get("dq"), g.get("dk"), g.get("dv"), None, None, g.get("ds0"), None
+
+
+def linear_attention(q, k, v, log_decay, scale=None, s0=None, lengths=None):
+    """Differentiable linear attention with a decay for each head: returns y
+    and s_final (m3.linattn_chunked_fwd).  log_decay is a constant."""
+    return LinearAttention.apply(q, k, v, log_decay, scale, s0, lengths)
+
+
+class GroupNorm(torch.autograd.Function):
+    """Returns y; gradients of x, weight, bias and gate."""
+
+    @staticmethod
+    def forward(ctx, x, groups, weight, bias, gate, act, eps):
+        y, mean, rstd = m3.group_norm_fwd(x, groups, weight, bias, gate=gate, act=act, eps=eps)
+        ctx.save_for_backward(x, weight, bias, gate, mean, rstd)
+        ctx.groups, ctx.act = groups, act
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, gate, mean, rstd = ctx.saved_tensors
+        n = ctx.needs_input_grad
+        want = tuple(k for k, on in (("dx", n[0]), ("dweight", n[2]), ("dbias", n[3]), ("dgate", n[4])) if on)
+        g = m3.group_norm_bwd(x, dy.to(x.dtype).contiguous(), mean, rstd, ctx.groups, weight, bias, gate=gate,
+                              act=ctx.act, want=want)
+        return g.get("dx"), None, g.get("dweight"), g.get("dbias"), g.get("dgate"), None, None
+
+
+def group_norm(x, groups, weight=None, bias=None, gate=None, act="none", eps=1e-5):
+    """Differentiable group norm with an activation or a gate, channels last
+    (m3.group_norm_fwd)."""
+    return GroupNorm.apply(x, groups, weight, bias, gate, act, eps)

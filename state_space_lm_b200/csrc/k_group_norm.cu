@@ -1,0 +1,792 @@
+// k_group_norm.cu -- group norm with an activation, channels last, forward
+// and backward.  Per (sequence, group) with xh = (x - mean) rstd,
+// u = xh w + b:
+//   y = act(u), or u act(gate) with a gate
+//   du = dy act'(u), or dy act(gate);   dgate = dy u act'(gate)
+//   dw = sum du xh,  db = sum du,  dn = du w
+//   dx = rstd (dn - mean(dn) - xh mean(dn xh))
+// Two plans.  `row` (one token a sequence, groups that fit a team of lanes):
+// the group stays in registers, one pass over the data.  `seq` (statistics
+// over many tokens, or wide groups): a pass for the sums, a pass that applies
+// them; the second read of x comes from L2 while the tensors fit there.
+#include "group_norm.cuh"
+
+namespace m3 {
+namespace {
+
+enum { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2, ACT_RELU = 3, ACT_ANY = -1 };
+
+// act(u) and act'(u); ACT_ANY takes the activation at run time (the variants
+// without vectors).  FAST: the exponentials of 16-bit outputs use the
+// hardware approximation (2^-21 relative, against a rounding of 2^-8).
+template <int ACT, bool FAST>
+__device__ __forceinline__ void act_both(float u, int act, float &f, float &df) {
+    const int A = ACT == ACT_ANY ? act : ACT;
+    if (A == ACT_SILU) {
+        const float e = FAST ? __expf(-u) : expf(-u);
+        const float s = FAST ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+        f = u * s;
+        df = fmaf(f, 1.f - s, s);
+    } else if (A == ACT_GELU) {
+        const float p = 0.5f * (1.f + erff(u * 0.70710678118654752f));
+        f = u * p;
+        df = fmaf(u * 0.39894228040143268f, FAST ? __expf(-0.5f * u * u) : expf(-0.5f * u * u), p);
+    } else if (A == ACT_RELU) {
+        f = u > 0.f ? u : (u == u ? 0.f : u);            // a NaN stays a NaN
+        df = u > 0.f ? 1.f : 0.f;
+    } else {
+        f = u;
+        df = 1.f;
+    }
+}
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_only(float u, int act) {
+    float f, df;
+    act_both<ACT, FAST>(u, act, f, df);
+    return f;
+}
+
+// VEC consecutive elements
+template <int VEC>
+__device__ __forceinline__ void ldv(const float *p, float *v) {
+    if (VEC == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
+    else
+#pragma unroll
+        for (int i = 0; i < VEC; i++) v[i] = p[i];
+}
+template <int VEC>
+__device__ __forceinline__ void ldv(const __nv_bfloat16 *p, float *v) {
+    if (VEC == 8) {
+        const uint4 r = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else
+#pragma unroll
+        for (int i = 0; i < VEC; i++) v[i] = __bfloat162float(p[i]);
+}
+template <int VEC>
+__device__ __forceinline__ void stv(float *p, const float *v) {
+    if (VEC == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+#pragma unroll
+        for (int i = 0; i < VEC; i++) p[i] = v[i];
+}
+template <int VEC>
+__device__ __forceinline__ void stv(__nv_bfloat16 *p, const float *v) {
+    if (VEC == 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&t);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else
+#pragma unroll
+        for (int i = 0; i < VEC; i++) p[i] = __float2bfloat16_rn(v[i]);
+}
+
+// Sum over a team of tw lanes (a power of two, 32 at most), every lane
+// receives it.
+__device__ __forceinline__ float team_sum(float v, int tw) {
+    for (int o = tw >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// The same for a team of up to 256 lanes: the warps of a wider team meet in
+// shared memory (the whole block takes part; `sh` holds a value per warp).
+__device__ __forceinline__ float2 row_sum2(float2 v, int tw, float2 *sh) {
+    const int in = tw < 32 ? tw : 32;
+    for (int o = in >> 1; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    if (tw > 32) {
+        const int w = threadIdx.x >> 5, nw = tw >> 5, w0 = w / nw * nw;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) sh[w] = v;
+        __syncthreads();
+        v = make_float2(0.f, 0.f);
+        for (int i = 0; i < nw; i++) {
+            v.x += sh[w0 + i].x;
+            v.y += sh[w0 + i].y;
+        }
+    }
+    return v;
+}
+__device__ __forceinline__ float row_sum(float v, int tw, float2 *sh) { return row_sum2(make_float2(v, 0.f), tw, sh).x; }
+
+// ------------------------------------------------------------------- row plan
+// A team of tw lanes (8 for 64 bf16 channels, a whole block for 4096) owns one
+// group's channels and walks rows with w and b in registers; neighbouring
+// teams own neighbouring groups, so a row is read as one contiguous piece.
+// Bound by the bytes.  Idle lanes (past the last whole set of G teams) take
+// part in the shuffles only.
+constexpr int RT = 256;
+
+struct RowGeo {
+    int64_t team, slot, g;
+    int lane_in;
+    bool on;
+    int64_t nslots;
+};
+__device__ __forceinline__ RowGeo row_geo(const GnArgs &a, int tw) {
+    RowGeo r;
+    const int64_t t = (int64_t)blockIdx.x * RT + threadIdx.x;
+    r.team = t / tw;
+    r.lane_in = (int)(t % tw);
+    r.nslots = (int64_t)gridDim.x * (RT / tw) / a.G;
+    r.slot = r.team / a.G;
+    r.g = r.team % a.G;
+    r.on = r.slot < r.nslots;
+    return r;
+}
+
+template <typename T, int VEC, int NV, int ACT, bool GATE>
+__global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
+    constexpr bool FAST = sizeof(T) == 2;
+    __shared__ float2 sh[RT / 32];
+    const RowGeo r = row_geo(a, tw);
+    const int D = (int)(a.C / a.G), nvec = D / VEC;
+    const float invD = 1.f / (float)D;
+    float w[NV][VEC], b[NV][VEC];
+#pragma unroll
+    for (int m = 0; m < NV; m++)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            const int c = (m * tw + r.lane_in) * VEC + e;
+            const bool in = r.on && c < D;
+            w[m][e] = (in && a.w) ? a.w[r.g * D + c] : 1.f;
+            b[m][e] = (in && a.b) ? a.b[r.g * D + c] : 0.f;
+        }
+    const int64_t turns = (a.Bt + r.nslots - 1) / r.nslots;    // the same for every lane: the shuffles need them all
+    for (int64_t k = 0; k < turns; k++) {
+        const int64_t row = r.slot + k * r.nslots;
+        const bool on = r.on && row < a.Bt;
+        const int64_t base = row * a.C + r.g * D;
+        float x[NV][VEC], z[NV][VEC];
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < NV; m++) {
+            const int v = m * tw + r.lane_in;
+            const bool in = on && v < nvec;
+#pragma unroll
+            for (int e = 0; e < VEC; e++) x[m][e] = 0.f;
+            if (in) {
+                ldv<VEC>(static_cast<const T *>(a.x) + base + v * VEC, x[m]);
+                if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + base + v * VEC, z[m]);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; e++) s += x[m][e];
+        }
+        const float mean = row_sum(s, tw, sh) * invD;
+        float q = 0.f;
+#pragma unroll
+        for (int m = 0; m < NV; m++) {
+            const bool in = on && m * tw + r.lane_in < nvec;
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                x[m][e] -= mean;
+                if (in) q = fmaf(x[m][e], x[m][e], q);
+            }
+        }
+        const float rstd = rsqrtf(fmaf(row_sum(q, tw, sh), invD, a.eps));
+        if (on && r.lane_in == 0) {
+            if (a.mean) a.mean[row * a.G + r.g] = mean;
+            if (a.rstd) a.rstd[row * a.G + r.g] = rstd;
+        }
+#pragma unroll
+        for (int m = 0; m < NV; m++) {
+            const int v = m * tw + r.lane_in;
+            if (on && v < nvec) {
+                float y[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    const float u = fmaf(x[m][e] * rstd, w[m][e], b[m][e]);
+                    y[e] = GATE ? u * act_only<ACT, FAST>(z[m][e], a.act) : act_only<ACT, FAST>(u, a.act);
+                }
+                stv<VEC>(static_cast<T *>(a.y) + base + v * VEC, y);
+            }
+        }
+    }
+}
+
+// The gradients of w and b are summed in registers over a team's rows and
+// left as one row of partial sums per slot, (slot, 2, C); k_gn_reduce adds the
+// slots up in their order.
+template <typename T, int VEC, int NV, int ACT, bool GATE>
+__global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw) {
+    constexpr bool FAST = sizeof(T) == 2;
+    __shared__ float2 sh[RT / 32];
+    const RowGeo r = row_geo(a, tw);
+    const int D = (int)(a.C / a.G), nvec = D / VEC;
+    const float invD = 1.f / (float)D;
+    float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int m = 0; m < NV; m++)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            const int c = (m * tw + r.lane_in) * VEC + e;
+            const bool in = r.on && c < D;
+            w[m][e] = (in && a.w) ? a.w[r.g * D + c] : 1.f;
+            b[m][e] = (in && a.b) ? a.b[r.g * D + c] : 0.f;
+            dw[m][e] = db[m][e] = 0.f;
+        }
+    const int64_t turns = (a.Bt + r.nslots - 1) / r.nslots;
+    for (int64_t k = 0; k < turns; k++) {
+        const int64_t row = r.slot + k * r.nslots;
+        const bool on = r.on && row < a.Bt;
+        const int64_t base = row * a.C + r.g * D;
+        const float mean = on ? a.mean_in[row * a.G + r.g] : 0.f;
+        const float rstd = on ? a.rstd_in[row * a.G + r.g] : 0.f;
+        float xh[NV][VEC], dn[NV][VEC];
+        float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+        for (int m = 0; m < NV; m++) {
+            const int v = m * tw + r.lane_in;
+            const bool in = on && v < nvec;
+            float dy[VEC], z[VEC], dz[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; e++) xh[m][e] = dy[e] = z[e] = 0.f;
+            if (in) {
+                ldv<VEC>(static_cast<const T *>(a.x) + base + v * VEC, xh[m]);
+                ldv<VEC>(static_cast<const T *>(a.dy) + base + v * VEC, dy);
+                if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + base + v * VEC, z);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                float f, df, du;
+                if (in) {
+                    xh[m][e] = (xh[m][e] - mean) * rstd;
+                    const float u = fmaf(xh[m][e], w[m][e], b[m][e]);
+                    if (GATE) {
+                        act_both<ACT, FAST>(z[e], a.act, f, df);
+                        du = dy[e] * f;
+                        dz[e] = dy[e] * u * df;
+                    } else {
+                        act_both<ACT, FAST>(u, a.act, f, df);
+                        du = dy[e] * df;
+                    }
+                    dw[m][e] = fmaf(du, xh[m][e], dw[m][e]);
+                    db[m][e] += du;
+                } else {
+                    du = 0.f;
+                }
+                dn[m][e] = du * w[m][e];
+                m1 += dn[m][e];
+                m2 = fmaf(dn[m][e], xh[m][e], m2);
+            }
+            if (GATE && in && a.dgate) stv<VEC>(static_cast<T *>(a.dgate) + base + v * VEC, dz);
+        }
+        const float2 mm = row_sum2(make_float2(m1, m2), tw, sh);
+        m1 = mm.x * invD;
+        m2 = mm.y * invD;
+        if (a.dx) {
+#pragma unroll
+            for (int m = 0; m < NV; m++) {
+                const int v = m * tw + r.lane_in;
+                if (on && v < nvec) {
+                    float dx[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; e++) dx[e] = (dn[m][e] - m1 - xh[m][e] * m2) * rstd;
+                    stv<VEC>(static_cast<T *>(a.dx) + base + v * VEC, dx);
+                }
+            }
+        }
+    }
+    if (r.on) {
+        float *pw = a.ws + (size_t)r.slot * 2 * a.C + r.g * D, *pb = pw + a.C;
+#pragma unroll
+        for (int m = 0; m < NV; m++)
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                const int c = (m * tw + r.lane_in) * VEC + e;
+                if (c < D) {
+                    pw[c] = dw[m][e];
+                    pb[c] = db[m][e];
+                }
+            }
+    }
+}
+
+// dw, db from partial sums (n rows of 2 C): one block per 32 channels, its 8
+// warps take rows in turn, then add up in a fixed order.
+__global__ void __launch_bounds__(256) k_gn_reduce(const float *part, int64_t n, int64_t C, float *dw, float *db) {
+    __shared__ float sh[8][32];
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+    const int64_t c = (int64_t)blockIdx.x * 32 + l;       // of 2 C
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    if (c < 2 * C) {
+        int64_t r = w;
+        for (; r + 24 < n; r += 32) {
+            s0 += part[r * 2 * C + c];
+            s1 += part[(r + 8) * 2 * C + c];
+            s2 += part[(r + 16) * 2 * C + c];
+            s3 += part[(r + 24) * 2 * C + c];
+        }
+        for (; r < n; r += 8) s0 += part[r * 2 * C + c];
+    }
+    sh[w][l] = (s0 + s1) + (s2 + s3);
+    __syncthreads();
+    if (w == 0 && c < 2 * C) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) t += sh[i][l];
+        if (c < C) {
+            if (dw) dw[c] = t;
+        } else if (db) {
+            db[c - C] = t;
+        }
+    }
+}
+
+// ------------------------------------------------------------------- seq plan
+// The L tokens of a sequence are cut into chunks of `rows` tokens, one CTA
+// each, all channels of a token read as one contiguous piece.
+constexpr int SQT = 256;
+
+// Per (sequence, chunk, group): count is known, (mean, M2) are written.  A
+// thread sums a vector of channels over the chunk's tokens as differences
+// from its first value (so a large mean cancels nothing), the vectors of a
+// group are merged by the pairwise update of means.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int64_t rows, int64_t nch) {
+    extern __shared__ float2 vstat[];                     // C / VEC pairs (mean, M2)
+    const int64_t bi = blockIdx.x / nch, ch = blockIdx.x % nch;
+    const int64_t t0 = ch * rows, t1 = t0 + rows < a.L ? t0 + rows : a.L;
+    const int nvec = (int)(a.C / VEC), D = (int)(a.C / a.G), dvec = D / VEC;
+    const T *x = static_cast<const T *>(a.x) + bi * a.L * a.C;
+    const float n1 = (float)((t1 - t0) * VEC);
+    for (int v = threadIdx.x; v < nvec; v += SQT) {
+        float k0[VEC], s[VEC], q[VEC];
+        ldv<VEC>(x + t0 * a.C + (int64_t)v * VEC, k0);
+        const float K = k0[0];
+#pragma unroll
+        for (int e = 0; e < VEC; e++) s[e] = q[e] = 0.f;
+#pragma unroll 4
+        for (int64_t t = t0; t < t1; t++) {
+            float y[VEC];
+            ldv<VEC>(x + t * a.C + (int64_t)v * VEC, y);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                const float d = y[e] - K;
+                s[e] += d;
+                q[e] = fmaf(d, d, q[e]);
+            }
+        }
+        float S = 0.f, Q = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            S += s[e];
+            Q += q[e];
+        }
+        const float m = S / n1;
+        vstat[v] = make_float2(K + m, fmaxf(Q - S * m, 0.f));
+    }
+    __syncthreads();
+    // one warp per group: mean of the vectors' means, then their spread
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+    float2 *out = reinterpret_cast<float2 *>(a.ws) + (bi * nch + ch) * a.G;
+    for (int g = w; g < a.G; g += SQT / 32) {
+        float m = 0.f;
+        for (int v = l; v < dvec; v += 32) m += vstat[g * dvec + v].x;
+        m = team_sum(m, 32) / (float)dvec;
+        float M2 = 0.f;
+        for (int v = l; v < dvec; v += 32) {
+            const float2 p = vstat[g * dvec + v];
+            const float d = p.x - m;
+            M2 += fmaf(n1 * d, d, p.y);
+        }
+        M2 = team_sum(M2, 32);
+        if (l == 0) out[g] = make_float2(m, M2);
+    }
+}
+
+// (mean, rstd) of every (sequence, group) from its chunks: a warp each.
+__global__ void __launch_bounds__(256) k_gn_seq_final(GnArgs a, int64_t rows, int64_t nch, float2 *stat) {
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int l = threadIdx.x & 31;
+    if (i >= a.Bt * a.G) return;
+    const int64_t bi = i / a.G, g = i % a.G;
+    const float2 *p = reinterpret_cast<const float2 *>(a.ws) + bi * nch * a.G + g;
+    const float D = (float)(a.C / a.G), n = (float)a.L * D;
+    float m = 0.f;
+    for (int64_t c = l; c < nch; c += 32) {
+        const float nc = (float)((c + 1) * rows < a.L ? rows : a.L - c * rows) * D;
+        m = fmaf(p[c * a.G].x, nc / n, m);
+    }
+    m = team_sum(m, 32);
+    float M2 = 0.f;
+    for (int64_t c = l; c < nch; c += 32) {
+        const float nc = (float)((c + 1) * rows < a.L ? rows : a.L - c * rows) * D;
+        const float2 s = p[c * a.G];
+        const float d = s.x - m;
+        M2 += fmaf(nc * d, d, s.y);
+    }
+    M2 = team_sum(M2, 32);
+    if (l == 0) {
+        const float rstd = rsqrtf(M2 / n + a.eps);
+        stat[i] = make_float2(m, rstd);
+        if (a.mean) a.mean[i] = m;
+        if (a.rstd) a.rstd[i] = rstd;
+    }
+}
+
+template <typename T, int VEC, int ACT, bool GATE>
+__global__ void __launch_bounds__(SQT) k_gn_seq_apply(GnArgs a, int64_t rows, int64_t nch, const float2 *stat) {
+    constexpr bool FAST = sizeof(T) == 2;
+    const int64_t bi = blockIdx.x / nch, ch = blockIdx.x % nch;
+    const int64_t t0 = ch * rows, t1 = t0 + rows < a.L ? t0 + rows : a.L;
+    const int nvec = (int)(a.C / VEC), dvec = (int)(a.C / a.G) / VEC;
+    const int64_t base = bi * a.L * a.C;
+    for (int v = threadIdx.x; v < nvec; v += SQT) {
+        const float2 st = stat[bi * a.G + v / dvec];
+        float w[VEC], b[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            w[e] = a.w ? a.w[v * VEC + e] : 1.f;
+            b[e] = a.b ? a.b[v * VEC + e] : 0.f;
+        }
+#pragma unroll 4
+        for (int64_t t = t0; t < t1; t++) {
+            const int64_t o = base + t * a.C + (int64_t)v * VEC;
+            float x[VEC], z[VEC];
+            ldv<VEC>(static_cast<const T *>(a.x) + o, x);
+            if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + o, z);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                const float u = fmaf((x[e] - st.x) * st.y, w[e], b[e]);
+                x[e] = GATE ? u * act_only<ACT, FAST>(z[e], a.act) : act_only<ACT, FAST>(u, a.act);
+            }
+            stv<VEC>(static_cast<T *>(a.y) + o, x);
+        }
+    }
+}
+
+// du of one element, and xh; dz where there is a gate
+template <int ACT, bool GATE, bool FAST>
+__device__ __forceinline__ float gn_du(float x, float dy, float z, float2 st, float w, float b, int act, float &xh,
+                                       float &dz) {
+    float f, df;
+    xh = (x - st.x) * st.y;
+    const float u = fmaf(xh, w, b);
+    if (GATE) {
+        act_both<ACT, FAST>(z, act, f, df);
+        dz = dy * u * df;
+        return dy * f;
+    }
+    act_both<ACT, FAST>(u, act, f, df);
+    return dy * df;
+}
+
+// Per (sequence, chunk, channel): sums of du xh and du over the chunk's
+// tokens, (sequence, chunk, 2, C); the gate's gradient is written on the way.
+template <typename T, int VEC, int ACT, bool GATE>
+__global__ void __launch_bounds__(SQT) k_gn_seq_bsums(GnArgs a, int64_t rows, int64_t nch) {
+    constexpr bool FAST = sizeof(T) == 2;
+    const int64_t bi = blockIdx.x / nch, ch = blockIdx.x % nch;
+    const int64_t t0 = ch * rows, t1 = t0 + rows < a.L ? t0 + rows : a.L;
+    const int nvec = (int)(a.C / VEC), dvec = (int)(a.C / a.G) / VEC;
+    const int64_t base = bi * a.L * a.C;
+    float *out = a.ws + (size_t)blockIdx.x * 2 * a.C;
+    for (int v = threadIdx.x; v < nvec; v += SQT) {
+        const int64_t gi = bi * a.G + v / dvec;
+        const float2 st = make_float2(a.mean_in[gi], a.rstd_in[gi]);
+        float w[VEC], b[VEC], s1[VEC], s2[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            w[e] = a.w ? a.w[v * VEC + e] : 1.f;
+            b[e] = a.b ? a.b[v * VEC + e] : 0.f;
+            s1[e] = s2[e] = 0.f;
+        }
+#pragma unroll 2
+        for (int64_t t = t0; t < t1; t++) {
+            const int64_t o = base + t * a.C + (int64_t)v * VEC;
+            float x[VEC], dy[VEC], z[VEC], dz[VEC];
+            ldv<VEC>(static_cast<const T *>(a.x) + o, x);
+            ldv<VEC>(static_cast<const T *>(a.dy) + o, dy);
+            if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + o, z);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                float xh;
+                const float du = gn_du<ACT, GATE, FAST>(x[e], dy[e], z[e], st, w[e], b[e], a.act, xh, dz[e]);
+                s1[e] = fmaf(du, xh, s1[e]);
+                s2[e] += du;
+            }
+            if (GATE && a.dgate) stv<VEC>(static_cast<T *>(a.dgate) + o, dz);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            out[v * VEC + e] = s1[e];
+            out[a.C + v * VEC + e] = s2[e];
+        }
+    }
+}
+
+// Per sequence: the chunks' sums added up into (sequence, 2, C), 32 channels a
+// block, eight warps over the chunks.
+__global__ void __launch_bounds__(256) k_gn_seq_fold(const float *part, int64_t nch, int64_t C, int cb, float *sums) {
+    __shared__ float sh[8][32];
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+    const int64_t bi = blockIdx.x / cb, c = (int64_t)(blockIdx.x % cb) * 32 + l;
+    float s = 0.f;
+    if (c < 2 * C)
+        for (int64_t k = w; k < nch; k += 8) s += part[(bi * nch + k) * 2 * C + c];
+    sh[w][l] = s;
+    __syncthreads();
+    if (w == 0 && c < 2 * C) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) t += sh[i][l];
+        sums[bi * 2 * C + c] = t;
+    }
+}
+
+// Per (sequence, group): mean(dn xh) and mean(dn) from the channels' sums.
+__global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, const float *sums, float2 *mom) {
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int l = threadIdx.x & 31;
+    if (i >= a.Bt * a.G) return;
+    const int64_t bi = i / a.G, g = i % a.G;
+    const int D = (int)(a.C / a.G);
+    const float *p = sums + bi * 2 * a.C + g * D;
+    float m2 = 0.f, m1 = 0.f;
+    for (int c = l; c < D; c += 32) {
+        const float w = a.w ? a.w[g * D + c] : 1.f;
+        m2 = fmaf(p[c], w, m2);
+        m1 = fmaf(p[a.C + c], w, m1);
+    }
+    const float n = (float)a.L * (float)D;
+    m2 = team_sum(m2, 32) / n;
+    m1 = team_sum(m1, 32) / n;
+    if (l == 0) mom[i] = make_float2(m2, m1);
+}
+
+template <typename T, int VEC, int ACT, bool GATE>
+__global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int64_t rows, int64_t nch, const float2 *mom) {
+    constexpr bool FAST = sizeof(T) == 2;
+    const int64_t bi = blockIdx.x / nch, ch = blockIdx.x % nch;
+    const int64_t t0 = ch * rows, t1 = t0 + rows < a.L ? t0 + rows : a.L;
+    const int nvec = (int)(a.C / VEC), dvec = (int)(a.C / a.G) / VEC;
+    const int64_t base = bi * a.L * a.C;
+    for (int v = threadIdx.x; v < nvec; v += SQT) {
+        const int64_t gi = bi * a.G + v / dvec;
+        const float2 st = make_float2(a.mean_in[gi], a.rstd_in[gi]), mm = mom[gi];
+        float w[VEC], b[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            w[e] = a.w ? a.w[v * VEC + e] : 1.f;
+            b[e] = a.b ? a.b[v * VEC + e] : 0.f;
+        }
+#pragma unroll 2
+        for (int64_t t = t0; t < t1; t++) {
+            const int64_t o = base + t * a.C + (int64_t)v * VEC;
+            float x[VEC], dy[VEC], z[VEC];
+            ldv<VEC>(static_cast<const T *>(a.x) + o, x);
+            ldv<VEC>(static_cast<const T *>(a.dy) + o, dy);
+            if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + o, z);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                float xh, dz;
+                const float du = gn_du<ACT, GATE, FAST>(x[e], dy[e], z[e], st, w[e], b[e], a.act, xh, dz);
+                x[e] = (fmaf(du, w[e], -mm.y) - xh * mm.x) * st.y;
+            }
+            stv<VEC>(static_cast<T *>(a.dx) + o, x);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+struct Plan {
+    bool row;
+    int vec, nv, tw;           // row plan: vector width, vectors a lane, lanes a team
+    unsigned blocks;
+    int64_t nslots;            // row plan: rows in flight (rows of partial sums)
+    int64_t rows, nch;         // seq plan: tokens a chunk, chunks a sequence
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Row plan: groups of one token that a block can hold in registers (4096
+// bf16, 8192 fp32 channels, 2048 without vectors).  Otherwise the seq plan.  Vectors of 16 bytes where the group is a whole
+// number of them (every base address is 16-byte aligned), else single
+// elements.
+Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd) {
+    Plan p{};
+    if (L == 0) {
+        p.rows = p.nch = 1;
+        return p;
+    }
+    const int64_t D = C / G;
+    const int wide = dt == M3_BF16 ? 8 : 4;
+    p.vec = D % wide == 0 ? wide : 1;
+    const int64_t nvec = D / p.vec;
+    const int most = p.vec == 8 ? 2 : 8;                  // vectors a lane: 16 bf16, 32 fp32 or 8 single values
+    if (L == 1 && nvec <= RT * most) {
+        p.row = true;
+        p.tw = 1;
+        while (p.tw < 32 && p.tw < nvec) p.tw *= 2;       // a warp first, then more values a lane, then more warps
+        while (p.tw < RT && nvec > p.tw * (p.vec > 1 ? most / 2 : 4)) p.tw *= 2;
+        const int64_t nv = ceil_div(nvec, p.tw);
+        p.nv = 1;
+        while (p.nv < nv) p.nv *= 2;
+        // about six CTAs per SM, at least two rows a team (weights are read
+        // once a team); always enough teams for one of each group
+        const int64_t teams_cta = RT / p.tw, need = ceil_div(G, teams_cta);
+        int64_t blocks = ceil_div(Bt * G, teams_cta * 2);
+        const int64_t cap = 148 * (bwd ? 3 : 6);
+        if (blocks > cap) blocks = cap;
+        if (blocks < need) blocks = need;
+        p.blocks = (unsigned)blocks;
+        p.nslots = blocks * teams_cta / G;
+        return p;
+    }
+    // chunks of tokens: about four CTAs per SM, at least 4 tokens each
+    int64_t nch = ceil_div(148 * 4, Bt > 0 ? Bt : 1);
+    if (nch > ceil_div(L, 4)) nch = ceil_div(L, 4);
+    if (nch < 1) nch = 1;
+    p.rows = ceil_div(L, nch);
+    p.nch = ceil_div(L, p.rows);
+    return p;
+}
+
+// the (activation, gate) variant of a kernel template: without vectors the
+// activation is a run-time choice (a quarter of the variants)
+#define GN_ACTS(K, T, VEC, NV, ...)                                                   \
+    if constexpr (VEC == 1) {                                                                 \
+        if (a.gate) K<T, 1 NV, ACT_ANY, true> __VA_ARGS__;                            \
+        else K<T, 1 NV, ACT_ANY, false> __VA_ARGS__;                                  \
+    } else {                                                                          \
+        constexpr int V = VEC == 1 ? (sizeof(T) == 2 ? 8 : 4) : VEC;                  \
+        switch (a.act * 2 + (a.gate ? 1 : 0)) {                                       \
+            case 0: K<T, V NV, ACT_NONE, false> __VA_ARGS__; break;                   \
+            case 1: K<T, V NV, ACT_NONE, true> __VA_ARGS__; break;                    \
+            case 2: K<T, V NV, ACT_SILU, false> __VA_ARGS__; break;                   \
+            case 3: K<T, V NV, ACT_SILU, true> __VA_ARGS__; break;                    \
+            case 4: K<T, V NV, ACT_GELU, false> __VA_ARGS__; break;                   \
+            case 5: K<T, V NV, ACT_GELU, true> __VA_ARGS__; break;                    \
+            case 6: K<T, V NV, ACT_RELU, false> __VA_ARGS__; break;                   \
+            default: K<T, V NV, ACT_RELU, true> __VA_ARGS__; break;                   \
+        }                                                                             \
+    }
+#define GN_COMMA_NV(n) , n
+
+template <typename T, int VEC, int NV>
+cudaError_t row_launch(const GnArgs &a, const Plan &p, bool bwd, cudaStream_t s) {
+    if (bwd) {
+        GN_ACTS(k_gn_row_bwd, T, VEC, GN_COMMA_NV(NV), <<<p.blocks, RT, 0, s>>>(a, p.tw))
+    } else {
+        GN_ACTS(k_gn_row_fwd, T, VEC, GN_COMMA_NV(NV), <<<p.blocks, RT, 0, s>>>(a, p.tw))
+    }
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T, int WIDE>
+cudaError_t row_dispatch(const GnArgs &a, const Plan &p, bool bwd, cudaStream_t s) {
+    if (p.vec == WIDE) {
+        if (p.nv == 1) return row_launch<T, WIDE, 1>(a, p, bwd, s);
+        if (p.nv == 2) return row_launch<T, WIDE, 2>(a, p, bwd, s);
+        if (WIDE == 4) {
+            if (p.nv == 4) return row_launch<T, 4, 4>(a, p, bwd, s);
+            return row_launch<T, 4, 8>(a, p, bwd, s);
+        }
+        return cudaErrorInvalidValue;
+    }
+    if (p.nv == 1) return row_launch<T, 1, 1>(a, p, bwd, s);
+    if (p.nv == 2) return row_launch<T, 1, 2>(a, p, bwd, s);
+    if (p.nv == 4) return row_launch<T, 1, 4>(a, p, bwd, s);
+    return row_launch<T, 1, 8>(a, p, bwd, s);
+}
+
+template <typename T, int VEC>
+cudaError_t seq_fwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
+    const unsigned blocks = (unsigned)(a.Bt * p.nch);
+    const int smem = (int)(a.C / VEC * sizeof(float2));
+    cudaError_t e;
+    if (smem > 48 * 1024 &&
+        (e = cudaFuncSetAttribute(k_gn_seq_stats<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        return e;
+    k_gn_seq_stats<T, VEC><<<blocks, SQT, smem, s>>>(a, p.rows, p.nch);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    float2 *stat = reinterpret_cast<float2 *>(a.ws) + a.Bt * p.nch * a.G;
+    k_gn_seq_final<<<(unsigned)ceil_div(a.Bt * a.G, 8), 256, 0, s>>>(a, p.rows, p.nch, stat);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    GN_ACTS(k_gn_seq_apply, T, VEC, , <<<blocks, SQT, 0, s>>>(a, p.rows, p.nch, stat))
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t seq_bwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
+    const unsigned blocks = (unsigned)(a.Bt * p.nch);
+    cudaError_t e;
+    GN_ACTS(k_gn_seq_bsums, T, VEC, , <<<blocks, SQT, 0, s>>>(a, p.rows, p.nch))
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    float *sums = a.ws + (size_t)a.Bt * p.nch * 2 * a.C;
+    float2 *mom = reinterpret_cast<float2 *>(sums + (size_t)a.Bt * 2 * a.C);
+    const unsigned cb = (unsigned)ceil_div(2 * a.C, 32);
+    k_gn_seq_fold<<<cb * (unsigned)a.Bt, 256, 0, s>>>(a.ws, p.nch, a.C, (int)cb, sums);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (a.dw || a.db) {
+        k_gn_reduce<<<cb, 256, 0, s>>>(sums, a.Bt, a.C, a.dw, a.db);
+        count_launch();
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (!a.dx) return cudaSuccess;
+    k_gn_seq_moments<<<(unsigned)ceil_div(a.Bt * a.G, 8), 256, 0, s>>>(a, sums, mom);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    GN_ACTS(k_gn_seq_dx, T, VEC, , <<<blocks, SQT, 0, s>>>(a, p.rows, p.nch, mom))
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t gn_fwd_workspace_floats(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt) {
+    const Plan p = plan_of(Bt, L, C, G, dt, false);
+    return p.row ? 0 : (size_t)(Bt * p.nch * G + Bt * G) * 2;
+}
+
+size_t gn_bwd_workspace_floats(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt) {
+    const Plan p = plan_of(Bt, L, C, G, dt, true);
+    return p.row ? (size_t)p.nslots * 2 * C : (size_t)Bt * (p.nch + 1) * 2 * C + (size_t)Bt * G * 2;
+}
+
+cudaError_t launch_gn_fwd(const GnArgs &a, m3_dtype dt, cudaStream_t s) {
+    const Plan p = plan_of(a.Bt, a.L, a.C, a.G, dt, false);
+    if (p.row)
+        return dt == M3_BF16 ? row_dispatch<__nv_bfloat16, 8>(a, p, false, s) : row_dispatch<float, 4>(a, p, false, s);
+    if (dt == M3_BF16) return p.vec == 8 ? seq_fwd<__nv_bfloat16, 8>(a, p, s) : seq_fwd<__nv_bfloat16, 1>(a, p, s);
+    return p.vec == 4 ? seq_fwd<float, 4>(a, p, s) : seq_fwd<float, 1>(a, p, s);
+}
+
+cudaError_t launch_gn_bwd(const GnArgs &a, m3_dtype dt, cudaStream_t s) {
+    if (a.Bt == 0 || a.L == 0) {                          // nothing was summed: zeros
+        if (!(a.dw || a.db)) return cudaSuccess;
+        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 256, 0, s>>>(nullptr, 0, a.C, a.dw, a.db);
+        count_launch();
+        return cudaGetLastError();
+    }
+    const Plan p = plan_of(a.Bt, a.L, a.C, a.G, dt, true);
+    if (p.row) {
+        cudaError_t e =
+            dt == M3_BF16 ? row_dispatch<__nv_bfloat16, 8>(a, p, true, s) : row_dispatch<float, 4>(a, p, true, s);
+        if (e != cudaSuccess || !(a.dw || a.db)) return e;
+        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 256, 0, s>>>(a.ws, p.nslots, a.C, a.dw, a.db);
+        count_launch();
+        return cudaGetLastError();
+    }
+    if (dt == M3_BF16) return p.vec == 8 ? seq_bwd<__nv_bfloat16, 8>(a, p, s) : seq_bwd<__nv_bfloat16, 1>(a, p, s);
+    return p.vec == 4 ? seq_bwd<float, 4>(a, p, s) : seq_bwd<float, 1>(a, p, s);
+}
+
+}  // namespace m3

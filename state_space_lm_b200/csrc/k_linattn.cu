@@ -1,0 +1,390 @@
+// k_linattn.cu -- linear attention with a decay for each head: the fp32
+// kernel for every size and type, the combine of a split time axis, the sum
+// of per-head gradients over shared heads, and the single-token step.
+#include "linattn.cuh"
+
+namespace m3 {
+namespace {
+
+// ---------------------------------------------------------------- k_mix_simt
+// One CTA owns one lane (or one segment of it) and 32 columns of c, and walks
+// the tokens in blocks of 16.  With M the state entering a block, j the place
+// in it and L its tokens:
+//   y_j = scale_i g^(j+1) M^T a_j + sum_{i <= j} P_ji c_i,  P_ji = scale_p g^(j-i) (a_j . b_i)
+//   M  <- M + M (g^L - 1) + sum_i b_i (scale_w g^(L-1-i) c_i)^T
+// (walking backwards g^j and g^(L-i)).  A thread holds one column and RS rows
+// of M in registers (warp = row slice, lane = column), so a and b rows are
+// read from shared memory as broadcasts and the block's own part of M is
+// summed before it meets M: a long sum loses no more than one rounding a
+// block.  This is the path of fp32 inputs, whose products the tensor cores
+// would round, and of sizes that TMA cannot address.
+constexpr int SC = 16, SP = 32, ST = 256;
+
+template <int RS>
+struct SimtSmem {
+    static constexpr int DA = 8 * RS, LDA = DA + 4;     // row padding: conflict-free 16-byte reads down a column
+    float a[SC][LDA], b[SC][LDA], c[SC][SP], p[SC][SC + 1], part[8][SC][SP];
+    float pw[SC + 1], pm1[SC + 1];
+};
+
+template <typename T, int RS, bool SO>
+__global__ void __launch_bounds__(ST) k_mix_simt(MixArgs g) {
+    using Sm = SimtSmem<RS>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
+    const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
+    const int nsb = SO ? g.nseg - 1 : g.nseg;
+    const int64_t lane = blockIdx.x / nsb, bi = lane / g.H, h = lane % g.H;
+    const int seg = (int)(blockIdx.x % nsb);
+    const int p0 = blockIdx.y * SP, pc = p0 + l;
+    const bool col = pc < g.dc;
+    const int64_t len = lane_length(g.lengths, bi, g.T);
+    const int64_t t0 = seg_begin(seg, g.nseg, g.seg_len, g.reverse);
+    const int64_t n = seg_tokens(seg, g.nseg, g.seg_len, g.reverse, len);
+    const double lg = (double)g.log_decay[h];
+    if (tid <= SC) {
+        sm.pw[tid] = decay_pow(lg, tid);
+        sm.pm1[tid] = decay_pow_m1(lg, tid);
+    }
+    const int64_t row0 = bi * g.T;
+    const T *A = static_cast<const T *>(g.a) + (int64_t)(h / g.ra) * g.da;
+    const T *B = static_cast<const T *>(g.b) + (int64_t)(h / g.rb) * g.da;
+    const T *C = static_cast<const T *>(g.c) + (int64_t)(h / g.rc) * g.dc;
+    const size_t elems = (size_t)g.da * g.dc;
+    float *slots = g.ws + (size_t)lane * (g.nseg - 1) * elems;
+
+    // the state: rows w*RS .. +RS of column pc
+    float M[RS];
+    {
+        const float *src = (SO || (seg == 0 && !g.m0)) ? nullptr : (seg == 0 ? g.m0 + lane * elems : slots + (seg - 1) * elems);
+        const bool tr = seg == 0 && g.m_trans;
+#pragma unroll
+        for (int i = 0; i < RS; i++) {
+            const int r = w * RS + i;
+            M[i] = (src && col && r < g.da) ? src[tr ? (size_t)pc * g.da + r : (size_t)r * g.dc + pc] : 0.f;
+        }
+    }
+
+    // a block's rows travel through registers one block ahead: warp w takes
+    // its places 2w and 2w+1
+    constexpr int NV = RS / 4;                           // 32-wide pieces of a row
+    float ra[2][NV], rb[2][NV], rc[2];
+    auto fetch = [&](int64_t j0) {
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const int64_t j = j0 + 2 * w + u;
+            const bool on = j < n;
+            const int64_t t = row0 + (g.reverse ? t0 + n - 1 - j : t0 + j);
+#pragma unroll
+            for (int m = 0; m < NV; m++) {
+                const int i = l + 32 * m;
+                const bool in = on && i < g.da;
+                if (!SO) ra[u][m] = in ? ldf(A, t * g.lda + i) : 0.f;
+                rb[u][m] = in ? ldf(B, t * g.ldb + i) : 0.f;
+            }
+            rc[u] = (on && col) ? ldf(C, t * g.ldc + pc) : 0.f;
+        }
+    };
+    if (n > 0) fetch(0);
+    for (int64_t j0 = 0; j0 < n; j0 += SC) {
+        const int L = (int)(n - j0 < SC ? n - j0 : SC);
+        __syncthreads();                                 // the block before is read
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+#pragma unroll
+            for (int m = 0; m < NV; m++) {
+                const int i = l + 32 * m;                // rows are 8 RS = 32 NV wide
+                if (!SO) sm.a[2 * w + u][i] = ra[u][m];
+                sm.b[2 * w + u][i] = rb[u][m];
+            }
+            sm.c[2 * w + u][l] = rc[u];
+        }
+        __syncthreads();
+        if (j0 + SC < n) fetch(j0 + SC);
+        if (!SO) {
+            {
+                const int j = tid >> 4, i = tid & 15;
+                if (i <= j) {
+                    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll 4
+                    for (int k = 0; k < Sm::DA; k += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(&sm.a[j][k]);
+                        const float4 z = *reinterpret_cast<const float4 *>(&sm.b[i][k]);
+                        s0 = fmaf(x.x, z.x, s0);
+                        s1 = fmaf(x.y, z.y, s1);
+                        s2 = fmaf(x.z, z.z, s2);
+                        s3 = fmaf(x.w, z.w, s3);
+                    }
+                    sm.p[j][i] = ((s0 + s1) + (s2 + s3)) * (sm.pw[j - i] * g.scale_p);
+                }
+            }
+#pragma unroll 4
+            for (int j = 0; j < SC; j++) {
+                float acc = 0.f;
+#pragma unroll
+                for (int i = 0; i < RS; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.a[j][w * RS + i]);
+                    acc = fmaf(x.x, M[i], acc);
+                    acc = fmaf(x.y, M[i + 1], acc);
+                    acc = fmaf(x.z, M[i + 2], acc);
+                    acc = fmaf(x.w, M[i + 3], acc);
+                }
+                sm.part[w][j][l] = acc;
+            }
+        }
+        {
+            float own[RS];
+#pragma unroll
+            for (int i = 0; i < RS; i++) own[i] = 0.f;
+            for (int j = 0; j < L; j++) {
+                const float cw = sm.c[j][l] * (sm.pw[g.reverse ? L - j : L - 1 - j] * g.scale_w);
+#pragma unroll
+                for (int i = 0; i < RS; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.b[j][w * RS + i]);
+                    own[i] = fmaf(x.x, cw, own[i]);
+                    own[i + 1] = fmaf(x.y, cw, own[i + 1]);
+                    own[i + 2] = fmaf(x.z, cw, own[i + 2]);
+                    own[i + 3] = fmaf(x.w, cw, own[i + 3]);
+                }
+            }
+            const float dm1 = sm.pm1[L];
+#pragma unroll
+            for (int i = 0; i < RS; i++) M[i] = fmaf(M[i], dm1, M[i]) + own[i];
+        }
+        if (!SO) {
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                const int j = w + 8 * u;
+                if (j < L && col && g.y) {
+                    float inter = 0.f, intra = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 8; k++) inter += sm.part[k][j][l];
+                    for (int i = 0; i <= j; i++) intra = fmaf(sm.p[j][i], sm.c[i][l], intra);
+                    const float y = fmaf(inter, sm.pw[g.reverse ? j : j + 1] * g.scale_i, intra);
+                    const int64_t t = row0 + (g.reverse ? t0 + n - 1 - (j0 + j) : t0 + j0 + j);
+                    const int64_t o = (t * g.H + h) * g.dc + pc;
+                    if (g.y_f32) stf(static_cast<float *>(g.y), o, y);
+                    else stf(static_cast<T *>(g.y), o, y);
+                }
+            }
+        }
+    }
+    float *dst = SO ? slots + seg * elems : (seg == g.nseg - 1 && g.m_out ? g.m_out + lane * elems : nullptr);
+    if (dst && col) {
+        const bool tr = !SO && g.m_trans;
+#pragma unroll
+        for (int i = 0; i < RS; i++) {
+            const int r = w * RS + i;
+            if (r < g.da) dst[tr ? (size_t)pc * g.da + r : (size_t)r * g.dc + pc] = M[i];
+        }
+    }
+    if (!SO && col && g.y) {
+        // rows behind the sequence, inside this segment: zeros
+        const int64_t e = t0 + g.seg_len < g.T ? t0 + g.seg_len : g.T;
+        for (int64_t t = t0 + n + w; t < e; t += 8) {
+            const int64_t o = ((row0 + t) * g.H + h) * g.dc + pc;
+            if (g.y_f32) stf(static_cast<float *>(g.y), o, 0.f);
+            else stf(static_cast<T *>(g.y), o, 0.f);
+        }
+    }
+}
+
+// Between the two passes of a split time axis: slot j holds segment j's own
+// state (from zero) and receives the state entering segment j + 1,
+//   M_(j+1) = g^n_j M_j + own_j.
+// One thread per state element; bound by the slots' bytes, read and written
+// once each.
+__global__ void __launch_bounds__(256) k_mix_combine(MixArgs g) {
+    __shared__ float dm1[256];
+    const int64_t lane = blockIdx.x, bi = lane / g.H, h = lane % g.H;
+    const int64_t len = lane_length(g.lengths, bi, g.T);
+    const double lg = (double)g.log_decay[h];
+    for (int j = threadIdx.x; j < g.nseg - 1; j += 256)
+        dm1[j] = decay_pow_m1(lg, seg_tokens(j, g.nseg, g.seg_len, g.reverse, len));
+    __syncthreads();
+    const size_t elems = (size_t)g.da * g.dc, i = (size_t)blockIdx.y * 256 + threadIdx.x;
+    if (i >= elems) return;
+    float M = 0.f;
+    if (g.m0) {
+        const size_t r = i / g.dc, p = i % g.dc;
+        M = g.m0[lane * elems + (g.m_trans ? p * g.da + r : i)];
+    }
+    float *sl = g.ws + (size_t)lane * (g.nseg - 1) * elems + i;
+    for (int j = 0; j < g.nseg - 1; j++) {
+        M = fmaf(M, dm1[j], M) + sl[j * elems];
+        sl[j * elems] = M;
+    }
+}
+
+// out[row, group, :] = sum over the group's heads of in[row, head, :], in
+// fp32 and a fixed order, rounded once.  Bound by reading `in`.
+template <typename T>
+__global__ void __launch_bounds__(256) k_head_sum(const float *in, T *out, int64_t n, int rep, int64_t d) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t e = i % d, rg = i / d;
+    const float *p = in + rg * rep * d + e;
+    float s = 0.f;
+    for (int r = 0; r < rep; r++) s += p[r * d];
+    stf(out, i, s);
+}
+
+// -------------------------------------------------------------- k_lin_step
+// One token of every lane: S <- S + (S (g - 1) + k v^T), y = scale S^T q.
+// One CTA per lane.  The state is read once and written once in VEC-wide
+// pieces: thread = (row of R, piece of a row), so a warp's accesses are
+// contiguous; the y sums over rows meet in shared memory.  Bound by the
+// state's bytes.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) k_lin_step(LinStepArgs a) {
+    __shared__ float qs[256], ks[256], vs[256];
+    __shared__ float red[256 * VEC];
+    const int tid = threadIdx.x;
+    const int64_t lane = blockIdx.x, b = lane / a.H, h = lane % a.H, hg = h / (a.H / a.G);
+    const int dk = (int)a.dk, dv = (int)a.dv;
+    const T *q = static_cast<const T *>(a.q) + b * a.ldq + hg * dk;
+    const T *k = static_cast<const T *>(a.k) + b * a.ldk + hg * dk;
+    const T *v = static_cast<const T *>(a.v) + b * a.ldv + h * dv;
+    if (tid < dk) {
+        qs[tid] = ldf(q, tid) * a.scale;
+        ks[tid] = ldf(k, tid);
+    }
+    if (tid < dv) vs[tid] = ldf(v, tid);
+    const float gm1 = expm1f(a.log_decay[h]);
+    const int cols = dv / VEC, R = 256 / cols;            // pieces of a row, rows at a time
+    const int c = tid % cols, r0 = tid / cols;
+    float *S = a.s + (size_t)lane * dk * dv;
+    float acc[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; e++) acc[e] = 0.f;
+    __syncthreads();
+    if (r0 < R) {
+        constexpr int U = 8;
+        for (int rr = r0; rr < dk; rr += U * R) {
+            float x[U][VEC];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int r = rr + u * R;
+                if (r < dk) {
+                    if (VEC == 4) *reinterpret_cast<float4 *>(x[u]) = *reinterpret_cast<const float4 *>(S + r * dv + 4 * c);
+                    else x[u][0] = S[r * dv + c];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int r = rr + u * R;
+                if (r < dk) {
+#pragma unroll
+                    for (int e = 0; e < VEC; e++) {
+                        x[u][e] += fmaf(x[u][e], gm1, ks[r] * vs[VEC * c + e]);
+                        acc[e] = fmaf(qs[r], x[u][e], acc[e]);
+                    }
+                    if (VEC == 4) *reinterpret_cast<float4 *>(S + r * dv + 4 * c) = *reinterpret_cast<float4 *>(x[u]);
+                    else S[r * dv + c] = x[u][0];
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; e++) red[(r0 * cols + c) * VEC + e] = acc[e];
+    }
+    __syncthreads();
+    if (tid < dv) {
+        float s = 0.f;
+        for (int r = 0; r < R; r++) s += red[r * dv + tid];
+        stf(static_cast<T *>(a.y), lane * dv + tid, s);
+    }
+}
+
+template <typename T, int RS>
+cudaError_t launch_mix_simt_t(const MixArgs &a, cudaStream_t s) {
+    constexpr int smem = (int)sizeof(SimtSmem<RS>);
+    const int64_t lanes = a.Bt * a.H;
+    const unsigned tiles = (unsigned)((a.dc + SP - 1) / SP);
+    cudaError_t e;
+    if (a.nseg > 1) {
+        if ((e = cudaFuncSetAttribute(k_mix_simt<T, RS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
+            cudaSuccess)
+            return e;
+        k_mix_simt<T, RS, true><<<dim3((unsigned)(lanes * (a.nseg - 1)), tiles), ST, smem, s>>>(a);
+        count_launch();
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_mix_combine(a, s)) != cudaSuccess) return e;
+    }
+    if ((e = cudaFuncSetAttribute(k_mix_simt<T, RS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
+        cudaSuccess)
+        return e;
+    k_mix_simt<T, RS, false><<<dim3((unsigned)(lanes * a.nseg), tiles), ST, smem, s>>>(a);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_mix_simt_d(const MixArgs &a, cudaStream_t s) {
+    if (a.da <= 32) return launch_mix_simt_t<T, 4>(a, s);
+    if (a.da <= 64) return launch_mix_simt_t<T, 8>(a, s);
+    if (a.da <= 128) return launch_mix_simt_t<T, 16>(a, s);
+    return launch_mix_simt_t<T, 32>(a, s);
+}
+
+}  // namespace
+
+// Split the time axis when the lanes' column tiles leave SMs idle: enough
+// segments for about four CTAs per SM, at least 128 tokens each (a segment
+// costs a state written and read, and its tokens' b and c twice), at most 64
+// segments and 64 MB of states.
+void mix_simt_plan(int64_t Bt, int64_t H, int64_t T, int da, int dc, int *nseg, int64_t *seg_len) {
+    *nseg = 1;
+    *seg_len = T > 0 ? T : 1;
+    const int64_t lanes = Bt * H, ctas = lanes * ((dc + SP - 1) / SP);
+    if (lanes == 0 || ctas >= 296 || T < 512) return;
+    int64_t ns = 592 / ctas;
+    if (ns > T / 128) ns = T / 128;
+    if (ns > 64) ns = 64;
+    const int64_t most = ((int64_t)64 << 20) / (lanes * da * dc * 4) + 1;
+    if (ns > most) ns = most;
+    if (ns < 2) return;
+    int64_t len = (T + ns - 1) / ns;
+    len = (len + SC - 1) / SC * SC;
+    *nseg = (int)((T + len - 1) / len);
+    *seg_len = len;
+}
+
+cudaError_t launch_mix_simt(const MixArgs &a, m3_dtype dt, cudaStream_t s) {
+    return dt == M3_BF16 ? launch_mix_simt_d<__nv_bfloat16>(a, s) : launch_mix_simt_d<float>(a, s);
+}
+
+cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s) {
+    k_mix_combine<<<dim3((unsigned)(a.Bt * a.H), (unsigned)((a.da * a.dc + 255) / 256)), 256, 0, s>>>(a);
+    count_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_head_sum(const float *in, void *out, m3_dtype dt, int64_t rows, int64_t H, int64_t G, int64_t d,
+                            cudaStream_t s) {
+    const int64_t n = rows * G * d;
+    if (n == 0) return cudaSuccess;
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+    if (dt == M3_BF16)
+        k_head_sum<__nv_bfloat16><<<blocks, 256, 0, s>>>(in, static_cast<__nv_bfloat16 *>(out), n, (int)(H / G), d);
+    else
+        k_head_sum<float><<<blocks, 256, 0, s>>>(in, static_cast<float *>(out), n, (int)(H / G), d);
+    count_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linattn_step(const LinStepArgs &a, m3_dtype dt, cudaStream_t s) {
+    const unsigned lanes = (unsigned)(a.Bt * a.H);
+    const bool v4 = a.dv % 4 == 0;
+    if (dt == M3_BF16) {
+        if (v4) k_lin_step<__nv_bfloat16, 4><<<lanes, 256, 0, s>>>(a);
+        else k_lin_step<__nv_bfloat16, 1><<<lanes, 256, 0, s>>>(a);
+    } else {
+        if (v4) k_lin_step<float, 4><<<lanes, 256, 0, s>>>(a);
+        else k_lin_step<float, 1><<<lanes, 256, 0, s>>>(a);
+    }
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace m3

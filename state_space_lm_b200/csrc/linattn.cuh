@@ -1,0 +1,89 @@
+// linattn.cuh -- shared declarations of the linear-attention kernels (not
+// part of the ABI).
+//
+// Forward and backward are one operation, a causal mix of three row
+// sequences a_t (width da), b_t (width da), c_t (width dc) of one lane:
+//
+//   y_t = scale_p sum_{s <= t} g^(t-s) (a_t . b_s) c_s + scale_i g^(t+1) M0^T a_t
+//
+// with the state M_t = g M_{t-1} + scale_w b_t c_t^T carried along (g the
+// lane's decay, t counted in walking order).  The three uses:
+//   y  = mix(q, k, v)   forwards,  M = S
+//   dq = mix(dy, v, k)  forwards,  M = S^T          (dq_t = scale S_t dy_t)
+//   dk = mix(v, dy, q)  backwards, M = Z^T          (dk_t = Z_t v_t)
+//   dv = mix(k, q, dy)  backwards, M = Z            (dv_t = Z_t^T k_t)
+// where Z_t = scale q_t dy_t^T + g Z_{t+1} is the adjoint of S_t.  Walking
+// backwards the carried state is g Z, the adjoint before the walk's next
+// token, so its powers are one lower in the answers and one higher in the
+// state (`reverse` below).
+#pragma once
+#include "m3_internal.cuh"
+
+namespace m3 {
+
+struct MixArgs {
+    const void *a, *b, *c;
+    int64_t lda, ldb, ldc;       // elements between the rows of consecutive tokens
+    int ra, rb, rc;              // lanes' heads that share one head of a, b, c
+    int da, dc;                  // width of a and b rows, of c rows
+    const float *log_decay;      // (H), natural logarithm
+    const int32_t *lengths;      // (Bt) tokens of each sequence, or NULL for T
+    const float *m0;             // state the walk starts from, or NULL for zero
+    float *m_out;                // state after the walk, or NULL
+    int m_trans;                 // m0, m_out hold the state transposed, (dc, da) instead of (da, dc)
+    void *y;                     // (Bt, T, H, dc), or NULL when only m_out is wanted
+    int y_f32;                   // y in fp32 (else the input type)
+    int64_t Bt, T, H;
+    int reverse;
+    float scale_p, scale_i, scale_w;
+    int nseg;                    // segments of the time axis, in walking order
+    int64_t seg_len;             // tokens of a segment
+    float *ws;                   // (nseg - 1) states of da * dc floats for each lane
+};
+
+struct LinStepArgs {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;       // elements between the rows of consecutive sequences
+    const float *log_decay;
+    float *s;
+    void *y;
+    int64_t Bt, H, G, dk, dv;
+    float scale;
+};
+
+// Tokens of segment j (walking order) of a sequence of `len` tokens whose
+// padded length is T.  Segments are cut at multiples of seg_len from the
+// sequence's first token; walking backwards, segment 0 is the last of them.
+__host__ __device__ __forceinline__ int64_t seg_begin(int j, int nseg, int64_t seg_len, int reverse) {
+    return (int64_t)(reverse ? nseg - 1 - j : j) * seg_len;
+}
+__device__ __forceinline__ int64_t seg_tokens(int j, int nseg, int64_t seg_len, int reverse, int64_t len) {
+    const int64_t t0 = seg_begin(j, nseg, seg_len, reverse);
+    const int64_t n = len - t0;
+    return n < 0 ? 0 : (n < seg_len ? n : seg_len);
+}
+__device__ __forceinline__ int64_t lane_length(const int32_t *lengths, int64_t b, int64_t T) {
+    if (!lengths) return T;
+    const int64_t n = lengths[b];
+    return n < 0 ? 0 : (n > T ? T : n);
+}
+// g^n and g^n - 1 for whole n >= 0, from 64 bits: the powers are needed to
+// full fp32 accuracy, and a state multiplied by g^n must not inherit the
+// rounding of a g near 1 (it is updated as M + M (g^n - 1)).  g^0 is 1 for a
+// decay of zero too (log_decay = -inf).
+__device__ __forceinline__ float decay_pow(double lg, int64_t n) { return n == 0 ? 1.f : (float)exp(lg * (double)n); }
+__device__ __forceinline__ float decay_pow_m1(double lg, int64_t n) {
+    return n == 0 ? 0.f : (float)expm1(lg * (double)n);
+}
+
+// segment plan and launch of the fp32 kernel (any sizes within the limits)
+void mix_simt_plan(int64_t Bt, int64_t H, int64_t T, int da, int dc, int *nseg, int64_t *seg_len);
+cudaError_t launch_mix_simt(const MixArgs &a, m3_dtype dt, cudaStream_t s);
+// chains the segments' states between the two passes
+cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s);
+// sums an fp32 (Bt, T, H, d) tensor over the heads of each of G groups
+cudaError_t launch_head_sum(const float *in, void *out, m3_dtype dt, int64_t rows, int64_t H, int64_t G, int64_t d,
+                            cudaStream_t s);
+cudaError_t launch_linattn_step(const LinStepArgs &a, m3_dtype dt, cudaStream_t s);
+
+}  // namespace m3

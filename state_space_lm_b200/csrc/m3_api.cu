@@ -5,6 +5,8 @@
 #include <cmath>
 #include <initializer_list>
 
+#include "group_norm.cuh"
+#include "linattn.cuh"
 #include "m3_internal.cuh"
 
 namespace m3 {
@@ -399,6 +401,281 @@ m3_status m3_chunked_bwd(const void *x, const float *dt, const float *A, const f
     a.ws = static_cast<float *>(workspace);
     if (d.batch == 0) return M3_OK;
     return launch_unless_injected([&] { return launch_scan_bwd(a, dtype, (cudaStream_t)stream); });
+}
+
+// ---- linear attention ------------------------------------------------------
+namespace {
+struct LinGeo {
+    int64_t G, ldq, ldk, ldv;
+};
+// Sizes and row strides of the linear-attention entry points.
+m3_status check_linattn_dims(const m3_linattn_dims &d, bool need_seq, LinGeo &o) {
+    if (d.batch < 0 || d.nheads < 1 || d.headdim < 1 || d.dstate < 1 || d.ngroups < 0) return M3_ERR_INVALID_ARG;
+    if (need_seq && d.seqlen < 0) return M3_ERR_INVALID_ARG;
+    if (d.ld_q < 0 || d.ld_k < 0 || d.ld_v < 0) return M3_ERR_INVALID_ARG;
+    if (d.dstate > kMaxDstate || d.headdim > kMaxHeaddim || d.dstate * d.headdim > kMaxStateElems)
+        return M3_ERR_UNSUPPORTED;
+    if (d.batch > (int64_t)1 << 24 || d.nheads > 4096 || (need_seq && d.seqlen > (int64_t)1 << 30))
+        return M3_ERR_UNSUPPORTED;
+    if (d.batch * d.nheads > kMaxLanes) return M3_ERR_UNSUPPORTED;
+    o.G = d.ngroups ? d.ngroups : d.nheads;
+    if (d.nheads % o.G) return M3_ERR_INVALID_ARG;
+    o.ldq = d.ld_q ? d.ld_q : o.G * d.dstate;
+    o.ldk = d.ld_k ? d.ld_k : o.G * d.dstate;
+    o.ldv = d.ld_v ? d.ld_v : d.nheads * d.headdim;
+    if (o.ldq < o.G * d.dstate || o.ldk < o.G * d.dstate || o.ldv < d.nheads * d.headdim) return M3_ERR_INVALID_ARG;
+    const int64_t T = need_seq ? d.seqlen : 1, wide = d.nheads * (d.headdim > d.dstate ? d.headdim : d.dstate);
+    int64_t ld = o.ldq > o.ldk ? o.ldq : o.ldk;
+    if (o.ldv > ld) ld = o.ldv;
+    if (wide > ld) ld = wide;
+    if (sat_product({d.batch, T, ld}) > kMaxElems) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+// q, k, v: non-null, aligned to their elements (the tensor-core path asks for
+// 16 bytes and is chosen only there)
+inline bool elem_aligned(const void *p, m3_dtype t) { return ((uintptr_t)p & (t == M3_BF16 ? 1u : 3u)) == 0; }
+#define M3_REQ_ELEM(p)                                                          \
+    do {                                                                        \
+        if (!(p) || !elem_aligned(p, dtype)) return M3_ERR_INVALID_ARG;         \
+    } while (0)
+
+inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// One mix of the problem (see linattn.cuh), without its pointers.
+MixArgs mix_of(const m3_linattn_dims &d, int64_t da, int64_t dc) {
+    MixArgs m{};
+    m.Bt = d.batch; m.H = d.nheads; m.T = d.seqlen;
+    m.da = (int)da; m.dc = (int)dc;
+    return m;
+}
+
+// Segment plan of a mix, and the bytes of its segment states.
+size_t plan_mix(MixArgs &m, m3_dtype dtype) {
+    (void)dtype;
+    mix_simt_plan(m.Bt, m.H, m.T, m.da, m.dc, &m.nseg, &m.seg_len);
+    return align256((size_t)(m.Bt * m.H) * (size_t)(m.nseg - 1) * m.da * m.dc * sizeof(float));
+}
+
+// Workspace of the backward: the segment states of one mix at a time, then
+// the per-head gradients of shared q and k heads in fp32.
+struct LinBwdPlan {
+    MixArgs dq, dk, dv;
+    size_t states, heads;      // bytes of the segment states, of one per-head gradient
+};
+LinBwdPlan plan_linattn_bwd(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
+    LinBwdPlan p;
+    p.dq = mix_of(d, d.headdim, d.dstate);
+    p.dk = p.dq;
+    p.dk.reverse = 1;
+    p.dv = mix_of(d, d.dstate, d.headdim);
+    p.dv.reverse = 1;
+    p.states = 0;
+    for (MixArgs *m : {&p.dq, &p.dk, &p.dv}) {
+        const size_t b = plan_mix(*m, dtype);
+        if (b > p.states) p.states = b;
+    }
+    p.heads = o.G == d.nheads ? 0 : align256((size_t)d.batch * d.seqlen * d.nheads * d.dstate * sizeof(float));
+    return p;
+}
+}  // namespace
+
+size_t m3_linattn_workspace_bytes(int which, m3_linattn_dims d, m3_dtype dtype) {
+    LinGeo o;
+    if (check_dtype(dtype) != M3_OK || check_linattn_dims(d, true, o) != M3_OK) return 0;
+    if (which == M3_WS_LINATTN_FWD) {
+        MixArgs m = mix_of(d, d.dstate, d.headdim);
+        return plan_mix(m, dtype);
+    }
+    if (which == M3_WS_LINATTN_BWD) {
+        const LinBwdPlan p = plan_linattn_bwd(d, o, dtype);
+        return p.states + p.heads;
+    }
+    return 0;
+}
+
+m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3_dtype dtype, const float *log_decay,
+                                 float scale, const float *s0, const int32_t *lengths, m3_linattn_dims d, void *y,
+                                 float *s_final, void *workspace, size_t workspace_bytes, void *stream) {
+    m3_status st;
+    LinGeo o;
+    if ((st = check_dtype(dtype)) != M3_OK) return st;
+    if ((st = check_linattn_dims(d, true, o)) != M3_OK) return st;
+    if (!std::isfinite(scale)) return M3_ERR_INVALID_ARG;
+    M3_REQ(log_decay);
+    if (d.batch > 0 && d.seqlen > 0) {
+        M3_REQ_ELEM(q); M3_REQ_ELEM(k); M3_REQ_ELEM(v); M3_REQ(y);
+    }
+    M3_OPT(s0); M3_OPT(lengths); M3_OPT(s_final); M3_OPT(workspace);
+    MixArgs m = mix_of(d, d.dstate, d.headdim);
+    const size_t need = plan_mix(m, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
+    if (d.batch == 0) return M3_OK;
+    m.a = q; m.b = k; m.c = v;
+    m.lda = o.ldq; m.ldb = o.ldk; m.ldc = o.ldv;
+    m.ra = m.rb = (int)(d.nheads / o.G);
+    m.rc = 1;
+    m.log_decay = log_decay; m.lengths = lengths;
+    m.m0 = s0; m.m_out = s_final;
+    m.y = y; m.y_f32 = dtype == M3_F32;
+    m.scale_p = m.scale_i = scale;
+    m.scale_w = 1.f;
+    m.ws = static_cast<float *>(workspace);
+    return launch_unless_injected([&] { return launch_mix_simt(m, dtype, (cudaStream_t)stream); });
+}
+
+m3_status m3_linattn_step_decode(const void *q_t, const void *k_t, const void *v_t, m3_dtype dtype,
+                                 const float *log_decay, float scale, m3_linattn_dims d, float *s, void *y_t,
+                                 void *stream) {
+    m3_status st;
+    LinGeo o;
+    if ((st = check_dtype(dtype)) != M3_OK) return st;
+    if ((st = check_linattn_dims(d, false, o)) != M3_OK) return st;
+    if (!std::isfinite(scale)) return M3_ERR_INVALID_ARG;
+    M3_REQ(log_decay);
+    if (d.batch == 0) return M3_OK;
+    M3_REQ_ELEM(q_t); M3_REQ_ELEM(k_t); M3_REQ_ELEM(v_t); M3_REQ(s); M3_REQ(y_t);
+    LinStepArgs a;
+    a.q = q_t; a.k = k_t; a.v = v_t;
+    a.ldq = o.ldq; a.ldk = o.ldk; a.ldv = o.ldv;
+    a.log_decay = log_decay; a.s = s; a.y = y_t;
+    a.Bt = d.batch; a.H = d.nheads; a.G = o.G; a.dk = d.dstate; a.dv = d.headdim;
+    a.scale = scale;
+    return launch_unless_injected([&] { return launch_linattn_step(a, dtype, (cudaStream_t)stream); });
+}
+
+m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3_dtype dtype, const float *log_decay,
+                                 float scale, const float *s0, const int32_t *lengths, m3_linattn_dims d,
+                                 const void *dy, const float *ds_final, const m3_linattn_grads *grads, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+    m3_status st;
+    LinGeo o;
+    if ((st = check_dtype(dtype)) != M3_OK) return st;
+    if ((st = check_linattn_dims(d, true, o)) != M3_OK) return st;
+    if (!std::isfinite(scale) || !grads) return M3_ERR_INVALID_ARG;
+    M3_REQ(log_decay);
+    if (d.batch > 0 && d.seqlen > 0) {
+        M3_REQ_ELEM(q); M3_REQ_ELEM(k); M3_REQ_ELEM(v); M3_REQ(dy);
+    }
+    const m3_linattn_grads &g = *grads;
+    M3_OPT(s0); M3_OPT(lengths); M3_OPT(ds_final); M3_OPT(workspace);
+    M3_OPT(g.dq); M3_OPT(g.dk); M3_OPT(g.dv); M3_OPT(g.ds0);
+    LinBwdPlan p = plan_linattn_bwd(d, o, dtype);
+    const size_t need = p.states + p.heads;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
+    if (d.batch == 0) return M3_OK;
+    const int rep = (int)(d.nheads / o.G);
+    const bool shared = rep > 1;
+    float *states = static_cast<float *>(workspace);
+    float *heads = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.states);
+    for (MixArgs *m : {&p.dq, &p.dk, &p.dv}) {
+        m->log_decay = log_decay; m->lengths = lengths;
+        m->ws = states;
+        m->y_f32 = dtype == M3_F32;
+        m->scale_p = scale;
+    }
+    const int64_t ldd = d.nheads * d.headdim;
+    // dq_t = scale S_t dy_t: the forward walk with S^T as its state
+    p.dq.a = dy; p.dq.lda = ldd; p.dq.ra = 1;
+    p.dq.b = v; p.dq.ldb = o.ldv; p.dq.rb = 1;
+    p.dq.c = k; p.dq.ldc = o.ldk; p.dq.rc = rep;
+    p.dq.m0 = s0; p.dq.m_trans = 1;
+    p.dq.scale_i = scale; p.dq.scale_w = 1.f;
+    // dk_t = Z_t v_t and dv_t = Z_t^T k_t: walks from the end, scale inside Z
+    p.dk.a = v; p.dk.lda = o.ldv; p.dk.ra = 1;
+    p.dk.b = dy; p.dk.ldb = ldd; p.dk.rb = 1;
+    p.dk.c = q; p.dk.ldc = o.ldq; p.dk.rc = rep;
+    p.dk.m0 = ds_final; p.dk.m_trans = 1;
+    p.dv.a = k; p.dv.lda = o.ldk; p.dv.ra = rep;
+    p.dv.b = q; p.dv.ldb = o.ldq; p.dv.rb = rep;
+    p.dv.c = dy; p.dv.ldc = ldd; p.dv.rc = 1;
+    p.dv.m0 = ds_final; p.dv.m_out = g.ds0;
+    p.dv.y = g.dv;
+    p.dk.scale_i = p.dv.scale_i = 1.f;
+    p.dk.scale_w = p.dv.scale_w = scale;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const int64_t rows = d.batch * d.seqlen;
+    return launch_unless_injected([&]() -> cudaError_t {
+        cudaError_t e;
+        struct { MixArgs *m; void *out; } shared_out[2] = {{&p.dq, g.dq}, {&p.dk, g.dk}};
+        for (auto &x : shared_out) {
+            if (!x.out) continue;
+            x.m->y = shared ? heads : x.out;
+            if (shared) x.m->y_f32 = 1;
+            if ((e = launch_mix_simt(*x.m, dtype, s)) != cudaSuccess) return e;
+            if (shared && (e = launch_head_sum(heads, x.out, dtype, rows, d.nheads, o.G, d.dstate, s)) != cudaSuccess)
+                return e;
+        }
+        if (g.dv || g.ds0)
+            if ((e = launch_mix_simt(p.dv, dtype, s)) != cudaSuccess) return e;
+        return cudaSuccess;
+    });
+}
+
+// ---- group norm --------------------------------------------------------------
+namespace {
+m3_status check_norm(m3_dtype dtype, m3_act act, const m3_norm_dims &d) {
+    m3_status st;
+    if ((st = check_dtype(dtype)) != M3_OK) return st;
+    if (act < M3_ACT_NONE || act > M3_ACT_RELU) return M3_ERR_INVALID_ARG;
+    if (d.batch < 0 || d.seqlen < 0 || d.channels < 1 || d.ngroups < 1 || d.channels % d.ngroups)
+        return M3_ERR_INVALID_ARG;
+    if (d.channels > 16384 || d.batch > (int64_t)1 << 24 || d.seqlen > (int64_t)1 << 30) return M3_ERR_UNSUPPORTED;
+    if (sat_product({d.batch, d.seqlen, d.channels}) > kMaxElems) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+}  // namespace
+
+size_t m3_group_norm_workspace_bytes(int which, m3_norm_dims d, m3_dtype dtype) {
+    if (check_norm(dtype, M3_ACT_NONE, d) != M3_OK || d.batch == 0 || d.seqlen == 0) return 0;
+    if (which == M3_WS_NORM_FWD)
+        return gn_fwd_workspace_floats(d.batch, d.seqlen, d.channels, d.ngroups, dtype) * sizeof(float);
+    if (which == M3_WS_NORM_BWD)
+        return gn_bwd_workspace_floats(d.batch, d.seqlen, d.channels, d.ngroups, dtype) * sizeof(float);
+    return 0;
+}
+
+m3_status m3_group_norm_fwd(const void *x, m3_dtype dtype, const float *weight, const float *bias, const void *gate,
+                            m3_act act, float eps, m3_norm_dims d, void *y, float *mean, float *rstd, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    m3_status st;
+    if ((st = check_norm(dtype, act, d)) != M3_OK) return st;
+    if (!(eps >= 0.f && std::isfinite(eps))) return M3_ERR_INVALID_ARG;
+    M3_OPT(weight); M3_OPT(bias); M3_OPT(gate); M3_OPT(mean); M3_OPT(rstd); M3_OPT(workspace);
+    const size_t need = m3_group_norm_workspace_bytes(M3_WS_NORM_FWD, d, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
+    if (d.batch == 0 || d.seqlen == 0) return M3_OK;
+    M3_REQ(x); M3_REQ(y);
+    GnArgs a{};
+    a.x = x; a.gate = gate; a.w = weight; a.b = bias; a.y = y; a.mean = mean; a.rstd = rstd;
+    a.Bt = d.batch; a.L = d.seqlen; a.C = d.channels; a.G = d.ngroups;
+    a.act = act; a.eps = eps;
+    a.ws = static_cast<float *>(workspace);
+    return launch_unless_injected([&] { return launch_gn_fwd(a, dtype, (cudaStream_t)stream); });
+}
+
+m3_status m3_group_norm_bwd(const void *x, const void *dy, m3_dtype dtype, const float *weight, const float *bias,
+                            const void *gate, m3_act act, const float *mean, const float *rstd, m3_norm_dims d,
+                            void *dx, float *dweight, float *dbias, void *dgate, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    m3_status st;
+    if ((st = check_norm(dtype, act, d)) != M3_OK) return st;
+    if (dgate && !gate) return M3_ERR_INVALID_ARG;
+    M3_OPT(weight); M3_OPT(bias); M3_OPT(gate); M3_OPT(dx); M3_OPT(dweight); M3_OPT(dbias); M3_OPT(dgate);
+    M3_OPT(workspace);
+    const size_t need = m3_group_norm_workspace_bytes(M3_WS_NORM_BWD, d, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
+    if (d.batch > 0 && d.seqlen > 0) {
+        M3_REQ(x); M3_REQ(dy); M3_REQ(mean); M3_REQ(rstd);
+    }
+    GnArgs a{};
+    a.x = x; a.dy = dy; a.gate = gate; a.w = weight; a.b = bias;
+    a.mean_in = mean; a.rstd_in = rstd;
+    a.dx = dx; a.dw = dweight; a.db = dbias; a.dgate = dgate;
+    a.Bt = d.batch; a.L = d.seqlen; a.C = d.channels; a.G = d.ngroups;
+    a.act = act;
+    a.ws = static_cast<float *>(workspace);
+    return launch_unless_injected([&] { return launch_gn_bwd(a, dtype, (cudaStream_t)stream); });
 }
 
 }  // extern "C"

@@ -24,8 +24,13 @@ ABI_FUNCTIONS = (
     "m3_mimo_chunked_fwd", "m3_step_decode", "m3_workspace_bytes", "m3_status_string",
     "m3_launch_count", "m3_device_error", "m3_siso_chunked_fwd_noalloc", "m3_mimo_step_decode",
     "m3_step_decode_factored", "m3_chunked_bwd", "m3_selftest_bounded_wait", "m3_debug_fail_next_launches",
+    "m3_linattn_chunked_fwd", "m3_linattn_step_decode", "m3_linattn_chunked_bwd", "m3_linattn_workspace_bytes",
+    "m3_group_norm_fwd", "m3_group_norm_bwd", "m3_group_norm_workspace_bytes",
 )
 M3_SELFTEST_SITE = 99
+M3_WS_LINATTN_FWD, M3_WS_LINATTN_BWD = 0, 1
+M3_WS_NORM_FWD, M3_WS_NORM_BWD = 0, 1
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
 
 GRAD_FIELDS = ("dx", "ddt", "dA", "dlam", "dtheta", "dB", "dC", "dD", "dW_x", "dW_y",
                "dnormw_B", "dnormw_C", "dbias_B", "dbias_C", "dh0", "dprevBx0", "dangle0")
@@ -53,6 +58,19 @@ class BcNorm(ctypes.Structure):
 
 class Grads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in GRAD_FIELDS]
+
+
+class LinattnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "headdim", "dstate", "ngroups",
+                                              "ld_q", "ld_k", "ld_v")]
+
+
+class LinattnGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dq", "dk", "dv", "ds0")]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "channels", "ngroups")]
 
 
 class Limits(ctypes.Structure):
@@ -117,6 +135,23 @@ def lib():
     L.m3_chunked_bwd.argtypes = [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int,
                                  ctypes.POINTER(BcNorm), _VP, _VP, _VP, Dims, _VP, _VP, _VP, _VP,
                                  ctypes.POINTER(Grads), _VP, ctypes.c_size_t, _VP]
+    i, sz, fl = ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    L.m3_linattn_chunked_fwd.restype = i
+    L.m3_linattn_chunked_fwd.argtypes = [_VP, _VP, _VP, i, _VP, fl, _VP, _VP, LinattnDims, _VP, _VP, _VP, sz, _VP]
+    L.m3_linattn_step_decode.restype = i
+    L.m3_linattn_step_decode.argtypes = [_VP, _VP, _VP, i, _VP, fl, LinattnDims, _VP, _VP, _VP]
+    L.m3_linattn_chunked_bwd.restype = i
+    L.m3_linattn_chunked_bwd.argtypes = [_VP, _VP, _VP, i, _VP, fl, _VP, _VP, LinattnDims, _VP, _VP,
+                                         ctypes.POINTER(LinattnGrads), _VP, sz, _VP]
+    L.m3_linattn_workspace_bytes.restype = sz
+    L.m3_linattn_workspace_bytes.argtypes = [i, LinattnDims, i]
+    L.m3_group_norm_fwd.restype = i
+    L.m3_group_norm_fwd.argtypes = [_VP, i, _VP, _VP, _VP, i, fl, NormDims, _VP, _VP, _VP, _VP, sz, _VP]
+    L.m3_group_norm_bwd.restype = i
+    L.m3_group_norm_bwd.argtypes = [_VP, _VP, i, _VP, _VP, _VP, i, _VP, _VP, NormDims, _VP, _VP, _VP, _VP, _VP, sz,
+                                    _VP]
+    L.m3_group_norm_workspace_bytes.restype = sz
+    L.m3_group_norm_workspace_bytes.argtypes = [i, NormDims, i]
     _lib = L
     return L
 
@@ -492,4 +527,254 @@ def chunked_bwd(x, dt, A, lam, theta, B, C, D, dy, chunk, W_x=None, W_y=None, no
                                 _ptr(W_x), _ptr(W_y), dtype, nptr, _ptr(h0), _ptr(prevBx0), _ptr(angle0), d,
                                 _ptr(dy), _ptr(dh_final), _ptr(dprevBx_final), _ptr(dangle_final),
                                 ctypes.byref(g), _ptr(ws), nbytes, _stream(stream)), "m3_chunked_bwd")
+    return out
+
+
+# ---- linear attention with a decay for each head, group norm -------------------
+def _row_ptr(t):
+    """Address of a tensor whose strides the caller has checked."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
+
+
+class _Device:
+    """Makes a tensor's device the current one around a library call (the
+    library launches on the current device), and gives the stream: the
+    caller's, or that device's current one."""
+
+    def __init__(self, dev, stream):
+        self.guard = None if dev.type != "cuda" or dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        self.dev, self.stream = dev, stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return (torch.cuda.current_stream(self.dev) if self.stream is None else self.stream).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _ld(where, name, t):
+    """Elements between the rows of consecutive tokens of a (Bt,[T,]heads,d)
+    tensor whose rows are contiguous: a slice of a fused projection has more
+    than heads * d."""
+    size, stride = t.shape, t.stride()
+    heads, d = size[-2], size[-1]
+    ok = (d <= 1 or stride[-1] == 1) and (heads <= 1 or stride[-2] == d)
+    lead = [(n, s) for n, s in zip(size[:-2], stride[:-2])]
+    ld = heads * d
+    if len(lead) == 1:
+        if lead[0][0] > 1:
+            ld = lead[0][1]
+    else:
+        (B, sb), (T, st) = lead
+        if T > 1:
+            ld = st
+            ok = ok and (B <= 1 or sb == T * ld)
+        elif B > 1:
+            ld = sb
+    if not ok or ld < heads * d:
+        raise ValueError("%s: %s has strides %s; the rows of a token have to be contiguous and the batch stride "
+                         "seqlen times the token stride" % (where, name, tuple(stride)))
+    return ld
+
+
+def _linattn_dims(w, q, k, v, seq):
+    if q.dim() != 3 + seq or v.dim() != 3 + seq:
+        raise ValueError("%s: q, k, v are (Bt,%sheads,d)" % (w, "T," if seq else ""))
+    B, H, dv = v.shape[0], v.shape[-2], v.shape[-1]
+    T = v.shape[1] if seq else 1
+    G, dk = q.shape[-2], q.shape[-1]
+    if v.dtype not in _DTYPE:
+        raise ValueError("%s: q, k, v must be float32 or bfloat16, got %s" % (w, v.dtype))
+    dev = v.device
+    _expect(w, dev, "q", q, B * T * G * dk, v.dtype)
+    _expect(w, dev, "k", k, B * T * G * dk, v.dtype)
+    for name, t in (("q", q), ("k", k)):
+        if t.shape[:-2] != v.shape[:-2] or t.shape[-2:] != q.shape[-2:]:
+            raise ValueError("%s: %s is %s for v %s" % (w, name, tuple(t.shape), tuple(v.shape)))
+    if G < 1 or H % G:
+        raise ValueError("%s: %d heads over %d groups of q and k" % (w, H, G))
+    d = LinattnDims(B, T, H, dv, dk, G, _ld(w, "q", q), _ld(w, "k", k), _ld(w, "v", v))
+    return d, dev
+
+
+def _linattn_scale(scale, dk):
+    return float(dk) ** -0.5 if scale is None else float(scale)
+
+
+def _own_workspace(need, workspace, dev):
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
+    if workspace.device != dev:
+        raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def linattn_chunked_fwd(q, k, v, log_decay, scale=None, s0=None, lengths=None, workspace=None, out=None,
+                        stream=None):
+    """Linear attention with a decay for each head over a prompt:
+    S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t.
+
+    q, k (Bt,T,G,dk) with G dividing H, v (Bt,T,H,dv), bf16 or fp32 (slices of
+    a fused projection are taken as they are); log_decay (H) fp32, <= 0; scale
+    defaults to dk^-1/2; s0 (Bt,H,dk,dv) fp32 or None for zero; lengths (Bt)
+    int32 on the device or None: tokens behind a sequence's length are left
+    out and their rows of y are zeros.  Returns y (Bt,T,H,dv) and s_final
+    (Bt,H,dk,dv) fp32, the state for linattn_step_decode; ``out`` may hold
+    both (s_final None when it is not wanted)."""
+    w, f = "m3_linattn_chunked_fwd", torch.float32
+    d, dev = _linattn_dims(w, q, k, v, True)
+    ns = d.batch * d.nheads * d.dstate * d.headdim
+    _expect(w, dev, "log_decay", log_decay, d.nheads, f)
+    _expect(w, dev, "s0", s0, ns, f, required=False)
+    _expect(w, dev, "lengths", lengths, d.batch, torch.int32, required=False)
+    if out is None:
+        out = (torch.empty(v.shape, dtype=v.dtype, device=dev),
+               torch.empty((d.batch, d.nheads, d.dstate, d.headdim), dtype=f, device=dev))
+    y, sf = out
+    _expect(w, dev, "y", y, v.numel(), v.dtype)
+    _expect(w, dev, "s_final", sf, ns, f, required=False)
+    L, dt = lib(), _DTYPE[v.dtype]
+    ws, nbytes = _own_workspace(L.m3_linattn_workspace_bytes(M3_WS_LINATTN_FWD, d, dt), workspace, dev)
+    args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay), _linattn_scale(scale, d.dstate), _ptr(s0),
+            _ptr(lengths), d, _ptr(y), _ptr(sf), _ptr(ws), nbytes)
+    with _Device(dev, stream) as s:
+        _check(L.m3_linattn_chunked_fwd(*args, s), w)
+    return y, sf
+
+
+def linattn_step_decode(q_t, k_t, v_t, log_decay, s, scale=None, y_out=None, stream=None):
+    """One token of every lane: q_t, k_t (Bt,G,dk), v_t (Bt,H,dv); the state s
+    (Bt,H,dk,dv) fp32 is updated in place; returns y_t (Bt,H,dv)."""
+    w, f = "m3_linattn_step_decode", torch.float32
+    d, dev = _linattn_dims(w, q_t, k_t, v_t, False)
+    _expect(w, dev, "log_decay", log_decay, d.nheads, f)
+    _expect(w, dev, "s", s, d.batch * d.nheads * d.dstate * d.headdim, f)
+    y = torch.empty(v_t.shape, dtype=v_t.dtype, device=dev) if y_out is None else y_out
+    _expect(w, dev, "y_t", y, v_t.numel(), v_t.dtype)
+    args = (_row_ptr(q_t), _row_ptr(k_t), _row_ptr(v_t), _DTYPE[v_t.dtype], _ptr(log_decay),
+            _linattn_scale(scale, d.dstate), d, _ptr(s), _ptr(y))
+    with _Device(dev, stream) as st:
+        _check(lib().m3_linattn_step_decode(*args, st), w)
+    return y
+
+
+def linattn_chunked_bwd(q, k, v, log_decay, dy, scale=None, s0=None, ds_final=None, lengths=None, want=None,
+                        out=None, workspace=None, stream=None):
+    """Backward of linattn_chunked_fwd: a dict of the gradients named in
+    ``want`` (by default dq, dk, dv, ds0), contiguous in their inputs' shapes
+    and dtype (ds0 fp32).  dy (Bt,T,H,dv) contiguous; ds_final fp32 or None for
+    zero.  ``out`` may hold preallocated tensors by name."""
+    w, f = "m3_linattn_chunked_bwd", torch.float32
+    d, dev = _linattn_dims(w, q, k, v, True)
+    ns = d.batch * d.nheads * d.dstate * d.headdim
+    _expect(w, dev, "log_decay", log_decay, d.nheads, f)
+    _expect(w, dev, "dy", dy, v.numel(), v.dtype)
+    _expect(w, dev, "s0", s0, ns, f, required=False)
+    _expect(w, dev, "ds_final", ds_final, ns, f, required=False)
+    _expect(w, dev, "lengths", lengths, d.batch, torch.int32, required=False)
+    names = ("dq", "dk", "dv", "ds0")
+    shapes = dict(dq=q.shape, dk=k.shape, dv=v.shape, ds0=(d.batch, d.nheads, d.dstate, d.headdim))
+    want = names if want is None else want
+    pre = out or {}
+    out = {}
+    for n in want:
+        if n not in shapes:
+            raise ValueError("%s: no gradient %r" % (w, n))
+        dt = f if n == "ds0" else v.dtype
+        out[n] = pre[n] if n in pre else torch.empty(shapes[n], dtype=dt, device=dev)
+        _expect(w, dev, n, out[n], ns if n == "ds0" else {"dq": q, "dk": k, "dv": v}[n].numel(), dt)
+    L, dt = lib(), _DTYPE[v.dtype]
+    ws, nbytes = _own_workspace(L.m3_linattn_workspace_bytes(M3_WS_LINATTN_BWD, d, dt), workspace, dev)
+    g = LinattnGrads(*[_ptr(out.get(n)) for n in names])
+    args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay), _linattn_scale(scale, d.dstate), _ptr(s0),
+            _ptr(lengths), d, _ptr(dy), _ptr(ds_final), ctypes.byref(g), _ptr(ws), nbytes)
+    with _Device(dev, stream) as s:
+        _check(L.m3_linattn_chunked_bwd(*args, s), w)
+    return out
+
+
+def _norm_dims(w, x, groups, weight, bias, gate, act):
+    if x.dim() < 2:
+        raise ValueError("%s: x is (Bt,...,C)" % w)
+    if x.dtype not in _DTYPE:
+        raise ValueError("%s: x must be float32 or bfloat16, got %s" % (w, x.dtype))
+    if act not in ACTIVATIONS:
+        raise ValueError("%s: act is one of %s, got %r" % (w, ", ".join(sorted(ACTIVATIONS)), act))
+    C, B, dev = x.shape[-1], x.shape[0], x.device
+    L = 1
+    for n in x.shape[1:-1]:
+        L *= n
+    for name, t in (("weight", weight), ("bias", bias)):
+        _expect(w, dev, name, t, C, torch.float32, required=False)
+    _expect(w, dev, "gate", gate, x.numel(), x.dtype, required=False)
+    return NormDims(B, L, C, int(groups)), dev
+
+
+def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps=1e-5, workspace=None, out=None,
+                   stream=None):
+    """Group norm with an activation, channels last: u = (x - mean) rstd weight
+    + bias with the statistics of each (x[b], group) over all positions and
+    the group's channels; y = act(u), or u * act(gate) with a gate.
+
+    x and gate (Bt,...,C) bf16 or fp32, contiguous; weight, bias (C) fp32 or
+    None; act "none", "silu", "gelu" (erf) or "relu".  For the norm of each
+    head of each token pass (tokens, C) and groups = heads.  Returns y, mean
+    and rstd (Bt, groups) fp32; ``out`` may hold the three (mean, rstd None
+    when not wanted)."""
+    w, f = "m3_group_norm_fwd", torch.float32
+    d, dev = _norm_dims(w, x, groups, weight, bias, gate, act)
+    if out is None:
+        g = max(d.ngroups, 0)
+        out = (torch.empty(x.shape, dtype=x.dtype, device=dev), torch.empty((d.batch, g), dtype=f, device=dev),
+               torch.empty((d.batch, g), dtype=f, device=dev))
+    y, mean, rstd = out
+    _expect(w, dev, "y", y, x.numel(), x.dtype)
+    _expect(w, dev, "mean", mean, d.batch * d.ngroups, f, required=False)
+    _expect(w, dev, "rstd", rstd, d.batch * d.ngroups, f, required=False)
+    L, dt = lib(), _DTYPE[x.dtype]
+    ws, nbytes = _own_workspace(L.m3_group_norm_workspace_bytes(M3_WS_NORM_FWD, d, dt), workspace, dev)
+    args = (_ptr(x), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], float(eps), d, _ptr(y), _ptr(mean),
+            _ptr(rstd), _ptr(ws), nbytes)
+    with _Device(dev, stream) as s:
+        _check(L.m3_group_norm_fwd(*args, s), w)
+    return y, mean, rstd
+
+
+def group_norm_bwd(x, dy, mean, rstd, groups, weight=None, bias=None, gate=None, act="none", want=None, out=None,
+                   workspace=None, stream=None):
+    """Backward of group_norm_fwd from its mean and rstd: a dict of the
+    gradients named in ``want`` (by default dx, dweight, dbias, and dgate with
+    a gate): dx, dgate in x's shape and dtype, dweight, dbias (C) fp32."""
+    w, f = "m3_group_norm_bwd", torch.float32
+    d, dev = _norm_dims(w, x, groups, weight, bias, gate, act)
+    _expect(w, dev, "dy", dy, x.numel(), x.dtype)
+    _expect(w, dev, "mean", mean, d.batch * d.ngroups, f)
+    _expect(w, dev, "rstd", rstd, d.batch * d.ngroups, f)
+    names = ("dx", "dweight", "dbias", "dgate")
+    if want is None:
+        want = names if gate is not None else names[:3]
+    pre = out or {}
+    out = {}
+    for n in want:
+        if n not in names or (n == "dgate" and gate is None):
+            raise ValueError("%s: no gradient %r" % (w, n))
+        wide = n in ("dx", "dgate")
+        shape, dt = (x.shape, x.dtype) if wide else ((d.channels,), f)
+        out[n] = pre[n] if n in pre else torch.empty(shape, dtype=dt, device=dev)
+        _expect(w, dev, n, out[n], x.numel() if wide else d.channels, dt)
+    L, dt = lib(), _DTYPE[x.dtype]
+    ws, nbytes = _own_workspace(L.m3_group_norm_workspace_bytes(M3_WS_NORM_BWD, d, dt), workspace, dev)
+    args = (_ptr(x), _ptr(dy), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], _ptr(mean), _ptr(rstd), d,
+            _ptr(out.get("dx")), _ptr(out.get("dweight")), _ptr(out.get("dbias")), _ptr(out.get("dgate")), _ptr(ws),
+            nbytes)
+    with _Device(dev, stream) as s:
+        _check(L.m3_group_norm_bwd(*args, s), w)
     return out
