@@ -333,21 +333,21 @@ cudaError_t launch_mix_simt_d(const MixArgs &a, cudaStream_t s) {
 // segments for about four CTAs per SM, at least 128 tokens each (a segment
 // costs a state written and read, and its tokens' b and c twice), at most 64
 // segments and 64 MB of states.
-void mix_simt_plan(int64_t Bt, int64_t H, int64_t T, int da, int dc, int *nseg, int64_t *seg_len) {
-    *nseg = 1;
-    *seg_len = T > 0 ? T : 1;
-    const int64_t lanes = Bt * H, ctas = lanes * ((dc + SP - 1) / SP);
-    if (lanes == 0 || ctas >= 296 || T < 512) return;
+void mix_simt_plan(MixArgs &a) {
+    a.nseg = 1;
+    a.seg_len = a.T > 0 ? a.T : 1;
+    const int64_t lanes = a.Bt * a.H, ctas = lanes * ((a.dc + SP - 1) / SP);
+    if (lanes == 0 || ctas >= 296 || a.T < 512) return;
     int64_t ns = 592 / ctas;
-    if (ns > T / 128) ns = T / 128;
+    if (ns > a.T / 128) ns = a.T / 128;
     if (ns > 64) ns = 64;
-    const int64_t most = ((int64_t)64 << 20) / (lanes * da * dc * 4) + 1;
+    const int64_t most = ((int64_t)64 << 20) / (lanes * a.da * a.dc * 4) + 1;
     if (ns > most) ns = most;
     if (ns < 2) return;
-    int64_t len = (T + ns - 1) / ns;
+    int64_t len = (a.T + ns - 1) / ns;
     len = (len + SC - 1) / SC * SC;
-    *nseg = (int)((T + len - 1) / len);
-    *seg_len = len;
+    a.nseg = (int)((a.T + len - 1) / len);
+    a.seg_len = len;
 }
 
 cudaError_t launch_mix_simt(const MixArgs &a, m3_dtype dt, cudaStream_t s) {

@@ -1,0 +1,662 @@
+// k_mix_tc.cu -- the causal mix of linattn.cuh on the sm_100a tensor cores
+// (bf16 rows, widths up to 128): the linear-attention forward, and each of
+// the three products of its backward.
+//
+// The chunked form, chunks of 64 tokens.  With M the state entering a chunk
+// (fp32, da x 64 of the dc columns), L its tokens, i and j places in it:
+//   D1 = A B^T              scores                     M=64  N=64 K=da
+//   P_ji = scale_p g^|j-i| D1_ji  (i <= j; walking backwards i >= j), bf16
+//   D2 = P C                own chunk's answer         M=64  N=64 K=64
+//   D3 = A M                the past's answer          M=64  N=64 K=da
+//   D4 = B^T Cw             own chunk's state          M=128 N=64 K=64 (three times)
+//   y_j = D2_j + scale_i g^(j+1) D3_j                  (backwards g^(L-1-j))
+//   M  <- M + M (g^L - 1) + D4,  Cw_i = scale_w g^(L-1-i) c_i   (backwards g^(i+1))
+// The decay is a constant of the lane, so every weight is a table of the 65
+// powers g^0 .. g^64: the 64 x 64 mask lives in the score warps' registers.
+//
+// Roundings: A, B, C enter as they are.  P and the copy of M that D3 reads
+// are rounded to bf16, one rounding for each term of y, as y itself has.  The
+// state is carried in fp32 and is an output in fp32, so Cw goes in as three
+// bf16 pieces, hi + mid + lo = w c to 2^-24: two thirds of D4's work, on a
+// tensor pipe that is not the limit here.
+//
+// One CTA owns one lane, one tile of 64 columns of c and one segment of the
+// time axis, and walks its chunks.  18 warps: 0 TMA, 1 UMMA issue (and TMEM),
+// 2-5 Cw, 6-9 scores, 10-13 state, 14-17 outputs.  Every hand-over is double
+// buffered in TMEM or shared memory, so the roles work on different chunks;
+// the chain from chunk to chunk is only the state's update.  A split time
+// axis takes two passes: B and C alone for every segment's own state, the
+// combine of linattn.cuh, then all segments at once.
+//
+// The problems of a call (three in the backward) share one launch.  Every
+// wait is bounded: past ~1 s the kernel records the site, stops issuing work,
+// drains what it has in flight and returns.
+#include <initializer_list>
+
+#include "linattn.cuh"
+#include "tc_ptx.cuh"
+
+namespace m3 {
+namespace mixtc {
+using namespace ptx;
+
+constexpr int Q = 64, DC = 64, DA = 128;               // chunk, columns of a tile, widest a and b rows
+constexpr int W_TMA = 0, W_MMA = 1, W_CW = 2, W_SC = 6, W_ST = 10, W_Y = 14, NWARPS = 18, THREADS = NWARPS * 32;
+
+// ---- shared memory (bytes from a 1024-aligned base), all tiles 128B-swizzled
+constexpr int NST = 3;                                  // stages of A, B, C
+constexpr int SZ_AB = Q * DA * 2, SZ_C = Q * DC * 2, SZ_STAGE = 2 * SZ_AB + SZ_C;
+constexpr int SZ_T = Q * DC * 2;                        // one 64 x 64 bf16 tile
+constexpr int SZ_M = DA * DC * 2;
+constexpr int OFF_STAGE = 0;
+constexpr int OFF_CW = OFF_STAGE + NST * SZ_STAGE;      // 2 x 3 pieces
+constexpr int OFF_P = OFF_CW + 2 * 3 * SZ_T;            // 2
+constexpr int OFF_M = OFF_P + 2 * SZ_T;                 // 2
+constexpr int OFF_Y = OFF_M + 2 * SZ_M;                 // 1
+constexpr int OFF_PW = OFF_Y + SZ_T;                    // fp32 g^0 .. g^64, then g^n - 1
+constexpr int NPW = 72;
+constexpr int OFF_BAR = OFF_PW + 2 * NPW * 4;
+enum {
+    B_FULL = 0,                    // NST: a stage has arrived
+    B_EMPTY = B_FULL + NST,        // NST: its readers are done
+    B_CWFULL = B_EMPTY + NST,      // 2 of each from here on
+    B_CWEMPTY = B_CWFULL + 2,
+    B_SFULL = B_CWEMPTY + 2,       // scores in TMEM
+    B_SEMPTY = B_SFULL + 2,
+    B_PFULL = B_SEMPTY + 2,        // masked scores in shared memory
+    B_PEMPTY = B_PFULL + 2,
+    B_DFULL = B_PEMPTY + 2,        // a chunk's own state in TMEM
+    B_DEMPTY = B_DFULL + 2,
+    B_MFULL = B_DEMPTY + 2,        // the entering state in shared memory
+    B_MEMPTY = B_MFULL + 2,
+    B_YFULL = B_MEMPTY + 2,        // both parts of the answer in TMEM
+    B_YEMPTY = B_YFULL + 2,
+    B_DRAIN = B_YEMPTY + 2,
+    NBAR
+};
+constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+constexpr int SMEM = OFF_MISC + 16 + 1024;
+static_assert(SMEM <= 227 * 1024, "shared memory budget");
+
+constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_Y2 = 128, COL_Y3 = 256, COL_D = 384;   // each two tiles of 64
+
+constexpr int MAXP = 3;
+struct Batch {
+    CUtensorMap ma[MAXP], mb[MAXP], mc[MAXP], my[MAXP];
+    MixArgs g[MAXP];
+    unsigned first[MAXP + 1];      // first block of each problem
+    int n;
+    int *err;
+};
+
+template <bool SO>
+__global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ Batch P) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const uint32_t sbase = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, l32 = tid & 31;
+    int pi = 0;
+    while (pi + 1 < P.n && blockIdx.x >= P.first[pi + 1]) pi++;
+    const MixArgs &g = P.g[pi];
+    const unsigned bid = blockIdx.x - P.first[pi];
+    const int ntile = (g.dc + DC - 1) / DC, nsb = SO ? g.nseg - 1 : g.nseg;
+    const int tile = (int)(bid % ntile), seg = (int)(bid / ntile % nsb);
+    const int64_t lane = bid / ntile / nsb, b = lane / g.H, h = lane % g.H;
+    const int64_t len = lane_length(g.lengths, b, g.T);
+    const int64_t t_beg = seg_begin(seg, g.nseg, g.seg_len, g.reverse);
+    const int64_t ntok = seg_tokens(seg, g.nseg, g.seg_len, g.reverse, len);
+    const int nch = (int)((ntok + Q - 1) / Q);
+    const bool rev = g.reverse != 0;
+    const int p0 = tile * DC;
+    const int nk = (g.da + 15) / 16;                    // K-steps over a and b rows
+    auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + OFF_MISC + 4);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_MISC);
+    float *pw = reinterpret_cast<float *>(sm + OFF_PW), *pm1 = pw + NPW;
+    // chunk c of the walk starts at token chunk_t(c) of the segment and has chunk_n(c) tokens
+    auto chunk_t = [&](int c) { return (int64_t)(rev ? nch - 1 - c : c) * Q; };
+    auto chunk_n = [&](int c) {
+        const int64_t n = ntok - chunk_t(c);
+        return (int)(n < Q ? n : Q);
+    };
+
+    if (tid == 0) {
+        for (int i = 0; i < NST; i++) {
+            mbar_init(bar(B_FULL + i), 1);
+            mbar_init(bar(B_EMPTY + i), 5);             // the chunk's last UMMA, four Cw warps
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(bar(B_CWFULL + i), 4);
+            mbar_init(bar(B_CWEMPTY + i), 1);
+            mbar_init(bar(B_SFULL + i), 1);
+            mbar_init(bar(B_SEMPTY + i), 4);
+            mbar_init(bar(B_PFULL + i), 4);
+            mbar_init(bar(B_PEMPTY + i), 1);
+            mbar_init(bar(B_DFULL + i), 1);
+            mbar_init(bar(B_DEMPTY + i), 4);
+            mbar_init(bar(B_MFULL + i), 4);
+            mbar_init(bar(B_MEMPTY + i), 1);
+            mbar_init(bar(B_YFULL + i), 1);
+            mbar_init(bar(B_YEMPTY + i), 4);
+        }
+        mbar_init(bar(B_DRAIN), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid >= 64 && tid < 64 + Q + 1) {
+        const double lg = (double)g.log_decay[h];
+        pw[tid - 64] = decay_pow(lg, tid - 64);
+        pm1[tid - 64] = decay_pow_m1(lg, tid - 64);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](int i, uint32_t parity, int site) { return warp_wait(bar(i), parity & 1, abort_flag, P.err, site); };
+    auto arrive = [&](int i) {                          // once for a converged warp
+        __syncwarp();
+        if (l32 == 0) mbar_arrive(bar(i));
+    };
+
+    if (warp == W_TMA) {
+        const int ha = (int)(h / g.ra), hb = (int)(h / g.rb), hc = (int)(h / g.rc);
+        for (int c = 0; c < nch; c++) {
+            const int st = c % NST, k = c / NST;
+            if (k > 0 && !wait(B_EMPTY + st, k - 1, 101)) break;
+            const int t = (int)(t_beg + chunk_t(c));
+            const uint32_t s0 = sbase + OFF_STAGE + st * SZ_STAGE, fb = bar(B_FULL + st);
+            if (elect_one()) {
+                mbar_expect_tx(fb, SO ? SZ_AB + SZ_C : SZ_STAGE);
+                for (int x = 0; x < 2; x++) {
+                    if (!SO) tma_load4(s0 + x * (SZ_AB / 2), &P.ma[pi], 64 * x, ha, t, (int)b, fb);
+                    tma_load4(s0 + SZ_AB + x * (SZ_AB / 2), &P.mb[pi], 64 * x, hb, t, (int)b, fb);
+                }
+                tma_load4(s0 + 2 * SZ_AB, &P.mc[pi], p0, hc, t, (int)b, fb);
+            }
+            __syncwarp();
+        }
+        // every load issued has landed before the CTA's memory goes away: the
+        // UMMA warp waits for each stage unless it gave up
+        if (*abort_flag) {
+            const long long t0 = clock64();
+            for (int c = (nch > NST ? nch - NST : 0); c < nch; c++)
+                while (!mbar_try(bar(B_FULL + c % NST), (c / NST) & 1) && clock64() - t0 < WAIT_LIMIT_CYCLES / 16) {
+                }
+        }
+    } else if (warp == W_MMA) {
+        constexpr uint32_t id_kk = idesc(64, 64, 0, 0), id_kmn = idesc(64, 64, 0, 1), id_st = idesc(128, 64, 1, 1);
+        // K-major operand, K-step kk of 16: 32 bytes inside a 128-byte row, the
+        // second 64 columns Q rows further; MN-major: two groups of 8 rows
+        auto kstep_k = [](int kk) { return (uint64_t)(((kk >> 2) * (Q * 128) + (kk & 3) * 32) >> 4); };
+        auto kstep_mn = [](int kk) { return (uint64_t)((kk * 2048) >> 4); };
+        const uint64_t d_k0 = sdesc(sbase + OFF_STAGE, 16, 1024), d_mn0 = sdesc(sbase + OFF_STAGE, Q * 128, 1024);
+        const uint64_t d_cw0 = sdesc(sbase + OFF_CW, Q * 128, 1024), d_p0 = sdesc(sbase + OFF_P, 16, 1024);
+        const uint64_t d_m0 = sdesc(sbase + OFF_M, DA * 128, 1024);
+        constexpr uint64_t ST = SZ_STAGE >> 4, AB = SZ_AB >> 4, TT = SZ_T >> 4, MM = SZ_M >> 4;
+        auto scores = [&](int c) {                      // D1 of chunk c
+            const int st = c % NST;
+            if (!wait(B_FULL + st, c / NST, 102)) return false;
+            if (c > 1 && !wait(B_SEMPTY + (c & 1), (c >> 1) - 1, 103)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t da = d_k0 + st * ST, db = da + AB;
+#pragma unroll 1
+                for (int kk = 0; kk < nk; kk++)
+                    umma(tmem + COL_S + (c & 1) * 64, da + kstep_k(kk), db + kstep_k(kk), id_kk, kk > 0);
+                umma_commit(bar(B_SFULL + (c & 1)));
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = SO || nch == 0 || scores(0);
+        for (int c = 0; c < nch && ok; c++) {
+            const int st = c % NST, pb = c & 1, k2 = c >> 1;
+            if (!SO && c + 1 < nch && !(ok = scores(c + 1))) break;
+            // D4: the stage has arrived, since Cw was built from it
+            if (!(ok = wait(B_CWFULL + pb, k2, 104))) break;
+            if (SO && !(ok = wait(B_FULL + st, c / NST, 105))) break;
+            if (c > 1 && !(ok = wait(B_DEMPTY + pb, k2 - 1, 106))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t db = d_mn0 + st * ST + AB, dw = d_cw0 + pb * (3 * TT);
+#pragma unroll 1
+                for (int kk = 0; kk < 12; kk++)         // pieces lo, mid, hi of 4 K-steps
+                    umma(tmem + COL_D + pb * 64, db + kstep_mn(kk & 3), dw + (kk >> 2) * TT + kstep_mn(kk & 3), id_st,
+                         kk > 0);
+                umma_commit(bar(B_DFULL + pb));
+                umma_commit(bar(B_CWEMPTY + pb));
+                if (SO) umma_commit(bar(B_EMPTY + st));
+            }
+            __syncwarp();
+            if (SO) continue;
+            if (!(ok = wait(B_MFULL + pb, k2, 107))) break;
+            if (c > 1 && !(ok = wait(B_YEMPTY + pb, k2 - 1, 108))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t da = d_k0 + st * ST, dm = d_m0 + pb * MM;
+#pragma unroll 1
+                for (int kk = 0; kk < nk; kk++)
+                    umma(tmem + COL_Y3 + pb * 64, da + kstep_k(kk), dm + kstep_mn(kk), id_kmn, kk > 0);
+                umma_commit(bar(B_MEMPTY + pb));
+            }
+            __syncwarp();
+            if (!(ok = wait(B_PFULL + pb, k2, 109))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t dp = d_p0 + pb * TT, dc = d_mn0 + st * ST + 2 * AB;
+#pragma unroll 1
+                for (int kk = 0; kk < 4; kk++)
+                    umma(tmem + COL_Y2 + pb * 64, dp + (uint64_t)(kk * 2), dc + kstep_mn(kk), id_kmn, kk > 0);
+                umma_commit(bar(B_YFULL + pb));
+                umma_commit(bar(B_PEMPTY + pb));
+                umma_commit(bar(B_EMPTY + st));
+            }
+            __syncwarp();
+        }
+        // every UMMA issued has completed before TMEM is freed
+        if (elect_one()) umma_commit(bar(B_DRAIN));
+        __syncwarp();
+        const long long t0 = clock64();
+        while (!mbar_try(bar(B_DRAIN), 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+        }
+        __syncwarp();
+    } else if (warp < W_SC) {
+        // ---- Cw = w c in three bf16 pieces; rows behind the sequence zeroed in B and C
+        const int wt = tid - W_CW * 32;                 // 0..127: 16-byte piece wt & 7 of rows wt/8 + 16u
+        for (int c = 0; c < nch; c++) {
+            const int st = c % NST, pb = c & 1, L = chunk_n(c);
+            if (!wait(B_FULL + st, c / NST, 110)) break;
+            if (c > 1 && !wait(B_CWEMPTY + pb, (c >> 1) - 1, 111)) break;
+            uint8_t *ct = sm + OFF_STAGE + st * SZ_STAGE + 2 * SZ_AB;
+            uint8_t *cw = sm + OFF_CW + pb * 3 * SZ_T;
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const int row = (wt >> 3) + 16 * u, o = (wt + 128 * u) * 16;
+                uint4 x = *reinterpret_cast<const uint4 *>(ct + o), hi, mid, lo;
+                float w = 0.f;
+                if (row < L) w = pw[rev ? row + 1 : L - 1 - row] * g.scale_w;
+                else x = make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                uint32_t hs[4], ms[4], ls[4];
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    float v0 = bf16_lo(xs[q]) * w, v1 = bf16_hi(xs[q]) * w;
+                    hs[q] = pack_bf16(v0, v1);
+                    v0 -= bf16_lo(hs[q]);
+                    v1 -= bf16_hi(hs[q]);
+                    ms[q] = pack_bf16(v0, v1);
+                    ls[q] = pack_bf16(v0 - bf16_lo(ms[q]), v1 - bf16_hi(ms[q]));
+                }
+                hi = make_uint4(hs[0], hs[1], hs[2], hs[3]);
+                mid = make_uint4(ms[0], ms[1], ms[2], ms[3]);
+                lo = make_uint4(ls[0], ls[1], ls[2], ls[3]);
+                *reinterpret_cast<uint4 *>(cw + o) = lo;
+                *reinterpret_cast<uint4 *>(cw + SZ_T + o) = mid;
+                *reinterpret_cast<uint4 *>(cw + 2 * SZ_T + o) = hi;
+                if (row >= L) {
+                    // behind the sequence but inside the tensor: may hold anything
+                    *reinterpret_cast<uint4 *>(ct + o) = x;
+                    uint8_t *bt = sm + OFF_STAGE + st * SZ_STAGE + SZ_AB + o;
+                    *reinterpret_cast<uint4 *>(bt) = x;
+                    *reinterpret_cast<uint4 *>(bt + SZ_AB / 2) = x;
+                }
+            }
+            fence_async_smem();
+            arrive(B_CWFULL + pb);
+            if (l32 == 0) mbar_arrive(bar(B_EMPTY + st));
+        }
+    } else if (warp < W_ST) {
+        // ---- scores: mask, round, store
+        if (!SO) {
+            const int q = warp & 3;                     // TMEM lane quarter: rows 16q .. 16q+15
+            const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+            const int ra = 16 * q + (l32 >> 2), cq = 2 * (l32 & 3);
+            float m[2][16];                             // the mask at this thread's places
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    const int row = ra + ((e & 2) ? 8 : 0), s = 32 * hf + 8 * (e >> 2) + cq + (e & 1);
+                    const int d = rev ? s - row : row - s;
+                    m[hf][e] = d >= 0 ? pw[d] * g.scale_p : 0.f;
+                }
+            for (int c = 0; c < nch; c++) {
+                const int pb = c & 1, L = chunk_n(c);
+                uint8_t *pt = sm + OFF_P + pb * SZ_T;
+                if (!wait(B_SFULL + pb, c >> 1, 112)) break;
+                if (c > 1 && !wait(B_PEMPTY + pb, (c >> 1) - 1, 113)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    // 16 x 32 blocks wholly on the masked side are zero: written
+                    // into each buffer once
+                    const bool zero = rev ? (hf == 0 && q >= 2) : (hf == 1 && q < 2);
+                    if (zero && c > 1) continue;
+                    float v[16];
+                    if (!zero) {
+                        tmem_ld16x256b_x4(tl + COL_S + pb * 64 + 32 * hf, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; e++) v[e] *= m[hf][e];
+                        if (L < Q) {                    // columns behind the sequence may be anything: select
+#pragma unroll
+                            for (int e = 0; e < 16; e++)
+                                if (32 * hf + 8 * (e >> 2) + cq + (e & 1) >= L) v[e] = 0.f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e++) v[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int col = 32 * hf + 8 * i + cq;
+                        *reinterpret_cast<uint32_t *>(pt + sw128(ra, col)) = pack_bf16(v[4 * i], v[4 * i + 1]);
+                        *reinterpret_cast<uint32_t *>(pt + sw128(ra + 8, col)) = pack_bf16(v[4 * i + 2], v[4 * i + 3]);
+                    }
+                }
+                tc_fence_before();
+                fence_async_smem();
+                arrive(B_SEMPTY + pb);
+                if (l32 == 0) mbar_arrive(bar(B_PFULL + pb));
+            }
+        }
+    } else if (warp < W_Y) {
+        // ---- the state: this thread's row, 64 columns, fp32
+        const int q = warp & 3, n = 32 * q + l32;
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+        const size_t elems = (size_t)g.da * g.dc;
+        float *slots = g.ws + (size_t)lane * (g.nseg - 1) * elems;
+        const bool mine = n < g.da;
+        float M[DC];
+        {
+            const float *src = (SO || (seg == 0 && !g.m0)) ? nullptr
+                               : (seg == 0 ? g.m0 + lane * elems : slots + (size_t)(seg - 1) * elems);
+#pragma unroll
+            for (int p = 0; p < DC; p++) M[p] = 0.f;
+            if (src && mine) {
+                if (seg == 0 && g.m_trans) {
+#pragma unroll
+                    for (int p = 0; p < DC; p++)
+                        if (p0 + p < g.dc) M[p] = src[(size_t)(p0 + p) * g.da + n];
+                } else {
+#pragma unroll
+                    for (int p = 0; p < DC; p += 4)     // dc is a multiple of 8
+                        if (p0 + p < g.dc) {
+                            const float4 v = *reinterpret_cast<const float4 *>(src + (size_t)n * g.dc + p0 + p);
+                            M[p] = v.x; M[p + 1] = v.y; M[p + 2] = v.z; M[p + 3] = v.w;
+                        }
+                }
+            }
+        }
+        auto publish = [&](int buf) {                   // the rounded copy that D3 reads
+            uint8_t *mt = sm + OFF_M + buf * SZ_M + n * 128;
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                uint4 v;
+                v.x = pack_bf16(M[8 * k], M[8 * k + 1]);
+                v.y = pack_bf16(M[8 * k + 2], M[8 * k + 3]);
+                v.z = pack_bf16(M[8 * k + 4], M[8 * k + 5]);
+                v.w = pack_bf16(M[8 * k + 6], M[8 * k + 7]);
+                *reinterpret_cast<uint4 *>(mt + ((k ^ (n & 7)) << 4)) = v;
+            }
+            fence_async_smem();
+            arrive(B_MFULL + buf);
+        };
+        if (!SO && nch > 0) publish(0);
+        for (int c = 0; c < nch; c++) {
+            const int pb = c & 1;
+            const float dm1 = pm1[chunk_n(c)];
+            if (!wait(B_DFULL + pb, c >> 1, 114)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < DC / 16; k++) {
+                float d[16];
+                tmem_ld16(tl + COL_D + pb * 64 + 16 * k, d);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; u++) M[16 * k + u] = fmaf(M[16 * k + u], dm1, M[16 * k + u]) + d[u];
+            }
+            tc_fence_before();
+            arrive(B_DEMPTY + pb);
+            if (!SO && c + 1 < nch) {
+                // buffer (c+1) & 1 was last read by D3 of chunk c - 1
+                if (c > 0 && !wait(B_MEMPTY + (pb ^ 1), (c - 1) >> 1, 115)) break;
+                publish(pb ^ 1);
+            }
+        }
+        float *dst = SO ? slots + (size_t)seg * elems
+                        : (seg == g.nseg - 1 && g.m_out ? g.m_out + lane * elems : nullptr);
+        if (dst && mine && !*abort_flag) {
+            if (!SO && g.m_trans) {
+#pragma unroll
+                for (int p = 0; p < DC; p++)
+                    if (p0 + p < g.dc) dst[(size_t)(p0 + p) * g.da + n] = M[p];
+            } else {
+#pragma unroll
+                for (int p = 0; p < DC; p += 4)
+                    if (p0 + p < g.dc)
+                        *reinterpret_cast<float4 *>(dst + (size_t)n * g.dc + p0 + p) =
+                            make_float4(M[p], M[p + 1], M[p + 2], M[p + 3]);
+            }
+        }
+    } else if (!SO && g.y) {
+        // ---- the answers
+        const int q = warp & 3, wy = warp - W_Y;
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+        const int r0 = l32 >> 2, ra = 16 * q + r0, rb = ra + 8, cq = 2 * (l32 & 3);
+        uint8_t *yt = sm + OFF_Y + 16 * q * 128;        // this warp's 16 rows
+        float *yf = static_cast<float *>(g.y);
+        for (int c = 0; c < nch; c++) {
+            const int pb = c & 1, L = chunk_n(c);
+            const int64_t t = t_beg + chunk_t(c);
+            if (!wait(B_YFULL + pb, c >> 1, 116)) break;
+            tc_fence_after();
+            const bool la = ra < L, lb = rb < L;
+            const float fa = la ? pw[rev ? L - 1 - ra : ra + 1] * g.scale_i : 0.f;
+            const float fb = lb ? pw[rev ? L - 1 - rb : rb + 1] * g.scale_i : 0.f;
+            if (!g.y_f32) {
+                if (l32 == 0) tma_store_wait_read();    // the rows of the chunk before are on their way
+                __syncwarp();
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+                float y2[16], y3[16];
+                tmem_ld16x256b_x4(tl + COL_Y2 + pb * 64 + 32 * hf, y2);
+                tmem_ld16x256b_x4(tl + COL_Y3 + pb * 64 + 32 * hf, y3);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int col = 32 * hf + 8 * i + cq;
+                    const float a0 = la ? fmaf(fa, y3[4 * i], y2[4 * i]) : 0.f;
+                    const float a1 = la ? fmaf(fa, y3[4 * i + 1], y2[4 * i + 1]) : 0.f;
+                    const float b0 = lb ? fmaf(fb, y3[4 * i + 2], y2[4 * i + 2]) : 0.f;
+                    const float b1 = lb ? fmaf(fb, y3[4 * i + 3], y2[4 * i + 3]) : 0.f;
+                    if (!g.y_f32) {
+                        *reinterpret_cast<uint32_t *>(yt + sw128(r0, col)) = pack_bf16(a0, a1);
+                        *reinterpret_cast<uint32_t *>(yt + sw128(r0 + 8, col)) = pack_bf16(b0, b1);
+                    } else if (p0 + col < g.dc) {       // dc is a multiple of 8: pairs stay whole
+                        if (t + ra < g.T)
+                            *reinterpret_cast<float2 *>(yf + ((b * g.T + t + ra) * g.H + h) * g.dc + p0 + col) =
+                                make_float2(a0, a1);
+                        if (t + rb < g.T)
+                            *reinterpret_cast<float2 *>(yf + ((b * g.T + t + rb) * g.H + h) * g.dc + p0 + col) =
+                                make_float2(b0, b1);
+                    }
+                }
+            }
+            tc_fence_before();
+            arrive(B_YEMPTY + pb);
+            if (!g.y_f32) {
+                fence_async_smem();
+                __syncwarp();
+                if (l32 == 0 && t + 16 * q < g.T)
+                    tma_store4(&P.my[pi], p0, (int)h, (int)(t + 16 * q), (int)b, sbase + OFF_Y + 16 * q * 128);
+                __syncwarp();
+            }
+        }
+        // rows behind the sequence in the segment's chunks that were not walked: zeros
+        const int64_t e = t_beg + g.seg_len < g.T ? t_beg + g.seg_len : g.T;
+        const int cols = g.dc - p0 < DC ? g.dc - p0 : DC, es = g.y_f32 ? 4 : 2, nv = cols * es / 16;
+        for (int64_t t = t_beg + (int64_t)nch * Q + wy; t < e; t += 4) {
+            uint8_t *row = static_cast<uint8_t *>(g.y) + (((b * g.T + t) * g.H + h) * g.dc + p0) * es;
+            for (int v = l32; v < nv; v += 32) reinterpret_cast<uint4 *>(row)[v] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (l32 == 0) tma_store_wait_all();
+    } else if (!SO) {
+        // no answer is wanted, only the state: hand the accumulators back
+        for (int c = 0; c < nch; c++) {
+            if (!wait(B_YFULL + (c & 1), c >> 1, 117)) break;
+            arrive(B_YEMPTY + (c & 1));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+__device__ int g_error;
+
+// ---- host side -------------------------------------------------------------------
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// bf16 rows (Bt, T, heads, d) with ld elements from token to token: boxes of
+// 64 columns and `rows` tokens, zeros outside
+static bool rows_map(CUtensorMap *m, const void *base, int64_t d, int64_t heads, int64_t T, int64_t Bt, int64_t ld,
+                     uint32_t rows) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)Bt};
+    const cuuint64_t strides[3] = {(cuuint64_t)(d * 2), (cuuint64_t)(ld * 2), (cuuint64_t)(ld * T * 2)};
+    const cuuint32_t box[4] = {64, 1, rows, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace mixtc
+
+bool mix_tc_sizes(const MixArgs &g, m3_dtype dt) {
+    if (dt != M3_BF16 || g.da > mixtc::DA || g.dc > mixtc::DA || g.da % 8 || g.dc % 8 || g.T < 1) return false;
+    // a TMA stride is a multiple of 16 bytes below 2^40
+    for (int64_t ld : {g.lda, g.ldb, g.ldc})
+        if (ld % 8 || ld > ((int64_t)1 << 38) / g.T) return false;
+    return true;
+}
+
+// Segments of the problems of one launch (the same count for all).  A CTA
+// holds an SM, so k CTAs take ceil(k / 148) waves of (chunks of a segment);
+// the state pass over the leading segments costs about 0.6 of a full chunk per
+// chunk.  The count with the least time in those units, at least 4 chunks a
+// segment, at most 64 segments and 64 MB of states.
+void mix_tc_plan(MixArgs *g, int n) {
+    using namespace mixtc;
+    const int64_t nq = (g[0].T + Q - 1) / Q;
+    int64_t ctas = 0, state = 0;
+    for (int i = 0; i < n; i++) {
+        ctas += g[i].Bt * g[i].H * ((g[i].dc + DC - 1) / DC);
+        state += g[i].Bt * g[i].H * g[i].da * g[i].dc * 4;
+        g[i].nseg = 1;
+        g[i].seg_len = (nq > 0 ? nq : 1) * Q;
+    }
+    if (ctas == 0 || ctas >= 148 || nq < 8) return;
+    const int64_t most = ((int64_t)64 << 20) / state;
+    auto waves = [](int64_t k) { return (k + 147) / 148; };
+    double best = (double)waves(ctas) * (double)nq;
+    for (int64_t ns = 2; ns <= 64; ns++) {
+        const int64_t len = (nq + ns - 1) / ns;
+        if (len < 4) break;
+        const int64_t k = (nq + len - 1) / len;
+        if (k < 2 || k - 1 > most) continue;
+        const double cost = ((double)waves(ctas * k) + 0.6 * (double)waves(ctas * (k - 1))) * (double)len;
+        if (cost < best - 1e-9) {
+            best = cost;
+            for (int i = 0; i < n; i++) {
+                g[i].nseg = (int)k;
+                g[i].seg_len = len * Q;
+            }
+        }
+    }
+}
+
+cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
+    using namespace mixtc;
+    if (n < 1 || n > MAXP) return cudaErrorInvalidValue;
+    Batch P;
+    P.n = n;
+    cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&P.err), g_error);
+    if (e != cudaSuccess) return e;
+    bool split = false;
+    for (int i = 0; i < n; i++) {
+        const MixArgs &a = g[i];
+        if (!rows_map(&P.ma[i], a.a, a.da, a.H / a.ra, a.T, a.Bt, a.lda, Q) ||
+            !rows_map(&P.mb[i], a.b, a.da, a.H / a.rb, a.T, a.Bt, a.ldb, Q) ||
+            !rows_map(&P.mc[i], a.c, a.dc, a.H / a.rc, a.T, a.Bt, a.ldc, Q))
+            return cudaErrorInvalidValue;
+        if (a.y && !a.y_f32 && !rows_map(&P.my[i], a.y, a.dc, a.H, a.T, a.Bt, a.H * a.dc, 16)) return cudaErrorInvalidValue;
+        P.g[i] = a;
+        split |= a.nseg > 1;
+    }
+    if (split) {
+        unsigned k = 0;
+        for (int i = 0; i < n; i++) {
+            P.first[i] = k;
+            k += (unsigned)(g[i].Bt * g[i].H * (g[i].nseg - 1) * ((g[i].dc + DC - 1) / DC));
+        }
+        P.first[n] = k;
+        if ((e = cudaFuncSetAttribute(k_mix_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
+            return e;
+        k_mix_tc<true><<<k, THREADS, SMEM, s>>>(P);
+        count_launch();
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        for (int i = 0; i < n; i++)
+            if (g[i].nseg > 1 && (e = launch_mix_combine(g[i], s)) != cudaSuccess) return e;
+    }
+    unsigned k = 0;
+    for (int i = 0; i < n; i++) {
+        P.first[i] = k;
+        k += (unsigned)(g[i].Bt * g[i].H * g[i].nseg * ((g[i].dc + DC - 1) / DC));
+    }
+    P.first[n] = k;
+    if ((e = cudaFuncSetAttribute(k_mix_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
+        return e;
+    k_mix_tc<false><<<k, THREADS, SMEM, s>>>(P);
+    count_launch();
+    return cudaGetLastError();
+}
+
+int mix_tc_error_and_clear(cudaStream_t s) {
+    int *err = nullptr, v = 0;
+    const int zero = 0;
+    if (cudaGetSymbolAddress(reinterpret_cast<void **>(&err), mixtc::g_error) != cudaSuccess) return -1;
+    if (cudaMemcpyAsync(&v, err, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess) return -1;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return -1;
+    if (v) {
+        if (cudaMemcpyAsync(err, &zero, sizeof(int), cudaMemcpyHostToDevice, s) != cudaSuccess) return -1;
+        if (cudaStreamSynchronize(s) != cudaSuccess) return -1;
+    }
+    return v;
+}
+
+}  // namespace m3

@@ -76,9 +76,17 @@ __device__ __forceinline__ float decay_pow_m1(double lg, int64_t n) {
     return n == 0 ? 0.f : (float)expm1(lg * (double)n);
 }
 
-// segment plan and launch of the fp32 kernel (any sizes within the limits)
-void mix_simt_plan(int64_t Bt, int64_t H, int64_t T, int da, int dc, int *nseg, int64_t *seg_len);
+// segment plan (nseg, seg_len) and launch of the fp32 kernel: any sizes
+// within the limits
+void mix_simt_plan(MixArgs &a);
 cudaError_t launch_mix_simt(const MixArgs &a, m3_dtype dt, cudaStream_t s);
+// The tensor-core kernel: bf16, widths at most 128, widths and row strides
+// multiples of 8, 16-byte aligned bases.  Up to three problems of one batch share
+// their launches.
+bool mix_tc_sizes(const MixArgs &a, m3_dtype dt);
+void mix_tc_plan(MixArgs *a, int n);
+cudaError_t launch_mix_tc(const MixArgs *a, int n, cudaStream_t s);
+int mix_tc_error_and_clear(cudaStream_t s);
 // chains the segments' states between the two passes
 cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s);
 // sums an fp32 (Bt, T, H, d) tensor over the heads of each of G groups

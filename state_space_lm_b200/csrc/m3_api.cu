@@ -187,7 +187,12 @@ const char *m3_status_string(m3_status s) {
 }
 
 m3_status m3_device_error(void *stream, int *site) {
-    const int e = scan_tc_error_and_clear((cudaStream_t)stream);
+    // one error word for the scan's kernels, one for the mixes' (sites from 101)
+    int e = scan_tc_error_and_clear((cudaStream_t)stream);
+    if (e >= 0) {
+        const int e2 = mix_tc_error_and_clear((cudaStream_t)stream);
+        if (e2 != 0 && e == 0) e = e2;
+    }
     if (site) *site = e > 0 ? e : 0;
     if (e < 0) return M3_ERR_CUDA;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return M3_ERR_CUDA;
@@ -442,56 +447,109 @@ inline bool elem_aligned(const void *p, m3_dtype t) { return ((uintptr_t)p & (t 
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// One mix of the problem (see linattn.cuh), without its pointers.
-MixArgs mix_of(const m3_linattn_dims &d, int64_t da, int64_t dc) {
+// The mixes of a call (linattn.cuh) and the plan of their launches.
+struct LinPlan {
+    MixArgs m[3];
+    int n;
+    bool tc;                   // all of them on the tensor cores, in shared launches; else one by one
+    size_t states[3], bytes;   // offsets of their segment states, and the end of these
+};
+void plan_mixes(LinPlan &p, m3_dtype dtype, bool aligned) {
+    p.tc = aligned;
+    for (int i = 0; i < p.n; i++) p.tc = p.tc && mix_tc_sizes(p.m[i], dtype);
+    if (p.tc) mix_tc_plan(p.m, p.n);
+    p.bytes = 0;
+    for (int i = 0; i < p.n; i++) {
+        MixArgs &m = p.m[i];
+        if (!p.tc) mix_simt_plan(m);
+        p.states[i] = p.bytes;
+        p.bytes += align256((size_t)(m.Bt * m.H) * (size_t)(m.nseg - 1) * m.da * m.dc * sizeof(float));
+    }
+}
+cudaError_t launch_mixes(LinPlan &p, m3_dtype dtype, void *workspace, cudaStream_t s) {
+    for (int i = 0; i < p.n; i++)
+        p.m[i].ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.states[i]);
+    if (p.tc) return launch_mix_tc(p.m, p.n, s);
+    for (int i = 0; i < p.n; i++) {
+        const cudaError_t e = launch_mix_simt(p.m[i], dtype, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// One mix of the problem, without its pointers.
+MixArgs mix_of(const m3_linattn_dims &d, int64_t da, int64_t dc, m3_dtype dtype) {
     MixArgs m{};
     m.Bt = d.batch; m.H = d.nheads; m.T = d.seqlen;
     m.da = (int)da; m.dc = (int)dc;
+    m.ra = m.rb = m.rc = 1;
+    m.y_f32 = dtype == M3_F32;
     return m;
 }
-
-// Segment plan of a mix, and the bytes of its segment states.
-size_t plan_mix(MixArgs &m, m3_dtype dtype) {
-    (void)dtype;
-    mix_simt_plan(m.Bt, m.H, m.T, m.da, m.dc, &m.nseg, &m.seg_len);
-    return align256((size_t)(m.Bt * m.H) * (size_t)(m.nseg - 1) * m.da * m.dc * sizeof(float));
-}
-
-// Workspace of the backward: the segment states of one mix at a time, then
-// the per-head gradients of shared q and k heads in fp32.
-struct LinBwdPlan {
-    MixArgs dq, dk, dv;
-    size_t states, heads;      // bytes of the segment states, of one per-head gradient
-};
-LinBwdPlan plan_linattn_bwd(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
-    LinBwdPlan p;
-    p.dq = mix_of(d, d.headdim, d.dstate);
-    p.dk = p.dq;
-    p.dk.reverse = 1;
-    p.dv = mix_of(d, d.dstate, d.headdim);
-    p.dv.reverse = 1;
-    p.states = 0;
-    for (MixArgs *m : {&p.dq, &p.dk, &p.dv}) {
-        const size_t b = plan_mix(*m, dtype);
-        if (b > p.states) p.states = b;
-    }
-    p.heads = o.G == d.nheads ? 0 : align256((size_t)d.batch * d.seqlen * d.nheads * d.dstate * sizeof(float));
+LinPlan fwd_mix(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
+    LinPlan p;
+    p.n = 1;
+    MixArgs &m = p.m[0] = mix_of(d, d.dstate, d.headdim, dtype);
+    m.lda = o.ldq; m.ldb = o.ldk; m.ldc = o.ldv;
+    m.ra = m.rb = (int)(d.nheads / o.G);
     return p;
 }
+// dq = mix(dy, v, k) forwards, dk = mix(v, dy, q) and dv = mix(k, q, dy)
+// backwards: those that are wanted.
+LinPlan bwd_mixes(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype, bool dq, bool dk, bool dv) {
+    LinPlan p;
+    p.n = 0;
+    const int rep = (int)(d.nheads / o.G);
+    const int64_t ldd = d.nheads * d.headdim;
+    if (dq) {
+        MixArgs &m = p.m[p.n++] = mix_of(d, d.headdim, d.dstate, dtype);
+        m.lda = ldd; m.ldb = o.ldv; m.ldc = o.ldk; m.rc = rep;
+        m.m_trans = 1;
+        if (rep > 1) m.y_f32 = 1;
+    }
+    if (dk) {
+        MixArgs &m = p.m[p.n++] = mix_of(d, d.headdim, d.dstate, dtype);
+        m.lda = o.ldv; m.ldb = ldd; m.ldc = o.ldq; m.rc = rep;
+        m.m_trans = m.reverse = 1;
+        if (rep > 1) m.y_f32 = 1;
+    }
+    if (dv) {
+        MixArgs &m = p.m[p.n++] = mix_of(d, d.dstate, d.headdim, dtype);
+        m.lda = o.ldk; m.ldb = o.ldq; m.ldc = ldd;
+        m.ra = m.rb = rep;
+        m.reverse = 1;
+    }
+    return p;
+}
+// bytes of one gradient of shared heads, per head in fp32
+size_t head_bytes(const m3_linattn_dims &d, const LinGeo &o) {
+    return o.G == d.nheads ? 0 : align256((size_t)d.batch * d.seqlen * d.nheads * d.dstate * sizeof(float));
+}
+inline bool tma_aligned(const void *q, const void *k, const void *v) { return aligned16(q) && aligned16(k) && aligned16(v); }
 }  // namespace
 
+// Enough for either path (the choice depends on the bases' alignment) and for
+// any of the gradients.
 size_t m3_linattn_workspace_bytes(int which, m3_linattn_dims d, m3_dtype dtype) {
     LinGeo o;
     if (check_dtype(dtype) != M3_OK || check_linattn_dims(d, true, o) != M3_OK) return 0;
-    if (which == M3_WS_LINATTN_FWD) {
-        MixArgs m = mix_of(d, d.dstate, d.headdim);
-        return plan_mix(m, dtype);
-    }
-    if (which == M3_WS_LINATTN_BWD) {
-        const LinBwdPlan p = plan_linattn_bwd(d, o, dtype);
-        return p.states + p.heads;
-    }
-    return 0;
+    size_t most = 0;
+    for (int want = which == M3_WS_LINATTN_BWD ? 1 : 7; want < 8; want++)
+        for (bool aligned : {false, true}) {
+            LinPlan p;
+            size_t heads = 0;
+            if (which == M3_WS_LINATTN_FWD) {
+                p = fwd_mix(d, o, dtype);
+            } else if (which == M3_WS_LINATTN_BWD) {
+                p = bwd_mixes(d, o, dtype, want & 1, want & 2, want & 4);
+                heads = ((want & 1) + (want >> 1 & 1)) * head_bytes(d, o);
+            } else {
+                return 0;
+            }
+            plan_mixes(p, dtype, aligned);
+            if (p.bytes + heads > most) most = p.bytes + heads;
+        }
+    return most;
 }
 
 m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3_dtype dtype, const float *log_decay,
@@ -507,21 +565,19 @@ m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3
         M3_REQ_ELEM(q); M3_REQ_ELEM(k); M3_REQ_ELEM(v); M3_REQ(y);
     }
     M3_OPT(s0); M3_OPT(lengths); M3_OPT(s_final); M3_OPT(workspace);
-    MixArgs m = mix_of(d, d.dstate, d.headdim);
-    const size_t need = plan_mix(m, dtype);
+    const size_t need = m3_linattn_workspace_bytes(M3_WS_LINATTN_FWD, d, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
     if (d.batch == 0) return M3_OK;
+    LinPlan p = fwd_mix(d, o, dtype);
+    MixArgs &m = p.m[0];
     m.a = q; m.b = k; m.c = v;
-    m.lda = o.ldq; m.ldb = o.ldk; m.ldc = o.ldv;
-    m.ra = m.rb = (int)(d.nheads / o.G);
-    m.rc = 1;
     m.log_decay = log_decay; m.lengths = lengths;
     m.m0 = s0; m.m_out = s_final;
-    m.y = y; m.y_f32 = dtype == M3_F32;
+    m.y = y;
     m.scale_p = m.scale_i = scale;
     m.scale_w = 1.f;
-    m.ws = static_cast<float *>(workspace);
-    return launch_unless_injected([&] { return launch_mix_simt(m, dtype, (cudaStream_t)stream); });
+    plan_mixes(p, dtype, tma_aligned(q, k, v));
+    return launch_unless_injected([&] { return launch_mixes(p, dtype, workspace, (cudaStream_t)stream); });
 }
 
 m3_status m3_linattn_step_decode(const void *q_t, const void *k_t, const void *v_t, m3_dtype dtype,
@@ -560,55 +616,45 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
     const m3_linattn_grads &g = *grads;
     M3_OPT(s0); M3_OPT(lengths); M3_OPT(ds_final); M3_OPT(workspace);
     M3_OPT(g.dq); M3_OPT(g.dk); M3_OPT(g.dv); M3_OPT(g.ds0);
-    LinBwdPlan p = plan_linattn_bwd(d, o, dtype);
-    const size_t need = p.states + p.heads;
+    const size_t need = m3_linattn_workspace_bytes(M3_WS_LINATTN_BWD, d, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
-    if (d.batch == 0) return M3_OK;
-    const int rep = (int)(d.nheads / o.G);
-    const bool shared = rep > 1;
-    float *states = static_cast<float *>(workspace);
-    float *heads = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.states);
-    for (MixArgs *m : {&p.dq, &p.dk, &p.dv}) {
-        m->log_decay = log_decay; m->lengths = lengths;
-        m->ws = states;
-        m->y_f32 = dtype == M3_F32;
-        m->scale_p = scale;
-    }
-    const int64_t ldd = d.nheads * d.headdim;
-    // dq_t = scale S_t dy_t: the forward walk with S^T as its state
-    p.dq.a = dy; p.dq.lda = ldd; p.dq.ra = 1;
-    p.dq.b = v; p.dq.ldb = o.ldv; p.dq.rb = 1;
-    p.dq.c = k; p.dq.ldc = o.ldk; p.dq.rc = rep;
-    p.dq.m0 = s0; p.dq.m_trans = 1;
-    p.dq.scale_i = scale; p.dq.scale_w = 1.f;
-    // dk_t = Z_t v_t and dv_t = Z_t^T k_t: walks from the end, scale inside Z
-    p.dk.a = v; p.dk.lda = o.ldv; p.dk.ra = 1;
-    p.dk.b = dy; p.dk.ldb = ldd; p.dk.rb = 1;
-    p.dk.c = q; p.dk.ldc = o.ldq; p.dk.rc = rep;
-    p.dk.m0 = ds_final; p.dk.m_trans = 1;
-    p.dv.a = k; p.dv.lda = o.ldk; p.dv.ra = rep;
-    p.dv.b = q; p.dv.ldb = o.ldq; p.dv.rb = rep;
-    p.dv.c = dy; p.dv.ldc = ldd; p.dv.rc = 1;
-    p.dv.m0 = ds_final; p.dv.m_out = g.ds0;
-    p.dv.y = g.dv;
-    p.dk.scale_i = p.dv.scale_i = 1.f;
-    p.dk.scale_w = p.dv.scale_w = scale;
+    LinPlan p = bwd_mixes(d, o, dtype, g.dq, g.dk, g.dv || g.ds0);
+    if (d.batch == 0 || p.n == 0) return M3_OK;
+    plan_mixes(p, dtype, tma_aligned(q, k, v));
+    const size_t hb = head_bytes(d, o);
+    const bool shared = hb > 0;
+    char *heads = static_cast<char *>(workspace) + p.bytes;
+    struct { const void *in; void *out; } sums[2] = {};
+    int i = 0, ns = 0;
+    auto next = [&](const void *a, const void *b, const void *c, const float *m0, void *y) -> MixArgs & {
+        MixArgs &m = p.m[i++];
+        m.a = a; m.b = b; m.c = c;
+        m.m0 = m0;
+        m.y = y;
+        m.log_decay = log_decay; m.lengths = lengths;
+        m.scale_p = scale;
+        // the forward walk scales its answers, the walks from the end their state
+        m.scale_i = m.reverse ? 1.f : scale;
+        m.scale_w = m.reverse ? scale : 1.f;
+        return m;
+    };
+    auto summed = [&](void *out) -> void * {
+        if (!shared) return out;
+        void *in = heads + ns * hb;
+        sums[ns].in = in;
+        sums[ns++].out = out;
+        return in;
+    };
+    if (g.dq) next(dy, v, k, s0, summed(g.dq));
+    if (g.dk) next(v, dy, q, ds_final, summed(g.dk));
+    if (g.dv || g.ds0) next(k, q, dy, ds_final, g.dv).m_out = g.ds0;
     const cudaStream_t s = (cudaStream_t)stream;
-    const int64_t rows = d.batch * d.seqlen;
     return launch_unless_injected([&]() -> cudaError_t {
-        cudaError_t e;
-        struct { MixArgs *m; void *out; } shared_out[2] = {{&p.dq, g.dq}, {&p.dk, g.dk}};
-        for (auto &x : shared_out) {
-            if (!x.out) continue;
-            x.m->y = shared ? heads : x.out;
-            if (shared) x.m->y_f32 = 1;
-            if ((e = launch_mix_simt(*x.m, dtype, s)) != cudaSuccess) return e;
-            if (shared && (e = launch_head_sum(heads, x.out, dtype, rows, d.nheads, o.G, d.dstate, s)) != cudaSuccess)
-                return e;
-        }
-        if (g.dv || g.ds0)
-            if ((e = launch_mix_simt(p.dv, dtype, s)) != cudaSuccess) return e;
-        return cudaSuccess;
+        cudaError_t e = launch_mixes(p, dtype, workspace, s);
+        for (int j = 0; j < ns && e == cudaSuccess; j++)
+            e = launch_head_sum(static_cast<const float *>(sums[j].in), sums[j].out, dtype, d.batch * d.seqlen,
+                                d.nheads, o.G, d.dstate, s);
+        return e;
     });
 }
 
