@@ -17,13 +17,12 @@
 // Roundings: A, B, C enter as they are.  P and the copy of M that D3 reads
 // are rounded to bf16, one rounding for each term of y, as y itself has.  The
 // state is carried in fp32 and is an output in fp32, so Cw goes in as three
-// bf16 pieces, hi + mid + lo = w c to 2^-24: two thirds of D4's work, on a
-// tensor pipe that is not the limit here.
+// bf16 pieces, hi + mid + lo = w c exactly, summed by the tensor cores.
 //
 // One CTA owns one lane, one tile of 64 columns of c and one segment of the
 // time axis, and walks its chunks.  18 warps: 0 TMA, 1 UMMA issue (and TMEM),
-// 2-5 Cw, 6-9 scores, 10-13 state, 14-17 outputs.  Every hand-over is double
-// buffered in TMEM or shared memory, so the roles work on different chunks;
+// 2-5 Cw, 6-9 scores, 10-13 state, 14-17 outputs.  The hand-overs are buffered
+// in TMEM or shared memory, so the roles work on different chunks;
 // the chain from chunk to chunk is only the state's update.  A split time
 // axis takes two passes: B and C alone for every segment's own state, the
 // combine of linattn.cuh, then all segments at once.
@@ -89,6 +88,18 @@ struct Batch {
     int *err;
 };
 
+// the upper half of an fp32 pattern (its first 8 significant bits), and of two
+__device__ __forceinline__ float cut(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+__device__ __forceinline__ uint32_t cut2(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+// rounded to bf16, as one register
+__device__ __forceinline__ uint32_t round2(f32x2 v) {
+    float a, b;
+    unpair(v, a, b);
+    return pack_bf16(a, b);
+}
+
 template <bool SO>
 __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ Batch P) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -102,23 +113,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     const int ntile = (g.dc + DC - 1) / DC, nsb = SO ? g.nseg - 1 : g.nseg;
     const int tile = (int)(bid % ntile), seg = (int)(bid / ntile % nsb);
     const int64_t lane = bid / ntile / nsb, b = lane / g.H, h = lane % g.H;
-    const int64_t len = lane_length(g.lengths, b, g.T);
     const int64_t t_beg = seg_begin(seg, g.nseg, g.seg_len, g.reverse);
-    const int64_t ntok = seg_tokens(seg, g.nseg, g.seg_len, g.reverse, len);
-    const int nch = (int)((ntok + Q - 1) / Q);
+    const int ntok = (int)seg_tokens(seg, g.nseg, g.seg_len, g.reverse, lane_length(g.lengths, b, g.T));
+    const int nch = (ntok + Q - 1) / Q;
     const bool rev = g.reverse != 0;
     const int p0 = tile * DC;
-    const int nk = (g.da + 15) / 16;                    // K-steps over a and b rows
     auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + OFF_MISC + 4);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_MISC);
     float *pw = reinterpret_cast<float *>(sm + OFF_PW), *pm1 = pw + NPW;
     // chunk c of the walk starts at token chunk_t(c) of the segment and has chunk_n(c) tokens
-    auto chunk_t = [&](int c) { return (int64_t)(rev ? nch - 1 - c : c) * Q; };
-    auto chunk_n = [&](int c) {
-        const int64_t n = ntok - chunk_t(c);
-        return (int)(n < Q ? n : Q);
-    };
+    auto chunk_t = [&](int c) { return (rev ? nch - 1 - c : c) * Q; };
+    auto chunk_n = [&](int c) { return min(Q, ntok - chunk_t(c)); };
 
     if (tid == 0) {
         for (int i = 0; i < NST; i++) {
@@ -166,10 +172,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
 
     if (warp == W_TMA) {
         const int ha = (int)(h / g.ra), hb = (int)(h / g.rb), hc = (int)(h / g.rc);
+        int st = 0, k = 0;                              // stage, turn of the ring
         for (int c = 0; c < nch; c++) {
-            const int st = c % NST, k = c / NST;
             if (k > 0 && !wait(B_EMPTY + st, k - 1, 101)) break;
-            const int t = (int)(t_beg + chunk_t(c));
+            const int t = (int)t_beg + chunk_t(c);
             const uint32_t s0 = sbase + OFF_STAGE + st * SZ_STAGE, fb = bar(B_FULL + st);
             if (elect_one()) {
                 mbar_expect_tx(fb, SO ? SZ_AB + SZ_C : SZ_STAGE);
@@ -180,9 +186,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 tma_load4(s0 + 2 * SZ_AB, &P.mc[pi], p0, hc, t, (int)b, fb);
             }
             __syncwarp();
+            if (++st == NST) st = 0, k++;
         }
-        // every load issued has landed before the CTA's memory goes away: the
-        // UMMA warp waits for each stage unless it gave up
+        // every load issued lands before the CTA's memory goes away: the other
+        // roles have waited for each stage, unless they gave up
         if (*abort_flag) {
             const long long t0 = clock64();
             for (int c = (nch > NST ? nch - NST : 0); c < nch; c++)
@@ -192,72 +199,79 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     } else if (warp == W_MMA) {
         constexpr uint32_t id_kk = idesc(64, 64, 0, 0), id_kmn = idesc(64, 64, 0, 1), id_st = idesc(128, 64, 1, 1);
         // K-major operand, K-step kk of 16: 32 bytes inside a 128-byte row, the
-        // second 64 columns Q rows further; MN-major: two groups of 8 rows
-        auto kstep_k = [](int kk) { return (uint64_t)(((kk >> 2) * (Q * 128) + (kk & 3) * 32) >> 4); };
-        auto kstep_mn = [](int kk) { return (uint64_t)((kk * 2048) >> 4); };
+        // second 64 columns Q rows further; MN-major: two groups of 8 rows.
+        // The issue loops are unrolled: rolled, the descriptor arithmetic
+        // between two UMMAs takes 65 to 100 cycles, twice what a UMMA does
+        // (measured beside busy warps: 3264 against 1437 cycles for a chunk's).
+        constexpr auto kstep_k = [](int kk) { return (uint64_t)(((kk >> 2) * (Q * 128) + (kk & 3) * 32) >> 4); };
+        constexpr auto kstep_mn = [](int kk) { return (uint64_t)((kk * 2048) >> 4); };
         const uint64_t d_k0 = sdesc(sbase + OFF_STAGE, 16, 1024), d_mn0 = sdesc(sbase + OFF_STAGE, Q * 128, 1024);
         const uint64_t d_cw0 = sdesc(sbase + OFF_CW, Q * 128, 1024), d_p0 = sdesc(sbase + OFF_P, 16, 1024);
         const uint64_t d_m0 = sdesc(sbase + OFF_M, DA * 128, 1024);
         constexpr uint64_t ST = SZ_STAGE >> 4, AB = SZ_AB >> 4, TT = SZ_T >> 4, MM = SZ_M >> 4;
+        int s1 = 0, k1 = 0;                             // stage and turn of the scores, one chunk ahead
         auto scores = [&](int c) {                      // D1 of chunk c
-            const int st = c % NST;
-            if (!wait(B_FULL + st, c / NST, 102)) return false;
+            if (!wait(B_FULL + s1, k1, 102)) return false;
             if (c > 1 && !wait(B_SEMPTY + (c & 1), (c >> 1) - 1, 103)) return false;
             tc_fence_after();
             if (elect_one()) {
-                const uint64_t da = d_k0 + st * ST, db = da + AB;
-#pragma unroll 1
-                for (int kk = 0; kk < nk; kk++)
-                    umma(tmem + COL_S + (c & 1) * 64, da + kstep_k(kk), db + kstep_k(kk), id_kk, kk > 0);
+                const uint64_t da = d_k0 + s1 * ST, db = da + AB;
+                const uint32_t d = tmem + COL_S + (c & 1) * 64;
+#pragma unroll
+                for (int kk = 0; kk < DA / 16; kk++) umma(d, da + kstep_k(kk), db + kstep_k(kk), id_kk, kk > 0);
                 umma_commit(bar(B_SFULL + (c & 1)));
             }
             __syncwarp();
+            if (++s1 == NST) s1 = 0, k1++;
             return true;
         };
         bool ok = SO || nch == 0 || scores(0);
+        int st = 0, k3 = 0;
         for (int c = 0; c < nch && ok; c++) {
-            const int st = c % NST, pb = c & 1, k2 = c >> 1;
+            const int pb = c & 1, k2 = c >> 1;
             if (!SO && c + 1 < nch && !(ok = scores(c + 1))) break;
             // D4: the stage has arrived, since Cw was built from it
             if (!(ok = wait(B_CWFULL + pb, k2, 104))) break;
-            if (SO && !(ok = wait(B_FULL + st, c / NST, 105))) break;
+            if (SO && !(ok = wait(B_FULL + st, k3, 105))) break;
             if (c > 1 && !(ok = wait(B_DEMPTY + pb, k2 - 1, 106))) break;
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t db = d_mn0 + st * ST + AB, dw = d_cw0 + pb * (3 * TT);
-#pragma unroll 1
-                for (int kk = 0; kk < 12; kk++)         // pieces lo, mid, hi of 4 K-steps
-                    umma(tmem + COL_D + pb * 64, db + kstep_mn(kk & 3), dw + (kk >> 2) * TT + kstep_mn(kk & 3), id_st,
-                         kk > 0);
+                const uint32_t d = tmem + COL_D + pb * 64;
+#pragma unroll
+                for (int kk = 0; kk < 12; kk++)         // the pieces lo, mid, hi of 4 K-steps
+                    umma(d, db + kstep_mn(kk & 3), dw + (kk >> 2) * TT + kstep_mn(kk & 3), id_st, kk > 0);
                 umma_commit(bar(B_DFULL + pb));
                 umma_commit(bar(B_CWEMPTY + pb));
                 if (SO) umma_commit(bar(B_EMPTY + st));
             }
             __syncwarp();
-            if (SO) continue;
-            if (!(ok = wait(B_MFULL + pb, k2, 107))) break;
-            if (c > 1 && !(ok = wait(B_YEMPTY + pb, k2 - 1, 108))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t da = d_k0 + st * ST, dm = d_m0 + pb * MM;
-#pragma unroll 1
-                for (int kk = 0; kk < nk; kk++)
-                    umma(tmem + COL_Y3 + pb * 64, da + kstep_k(kk), dm + kstep_mn(kk), id_kmn, kk > 0);
-                umma_commit(bar(B_MEMPTY + pb));
+            if (!SO) {
+                if (!(ok = wait(B_MFULL + pb, k2, 107))) break;
+                if (c > 1 && !(ok = wait(B_YEMPTY + pb, k2 - 1, 108))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t da = d_k0 + st * ST, dm = d_m0 + pb * MM;
+                    const uint32_t d = tmem + COL_Y3 + pb * 64;
+#pragma unroll
+                    for (int kk = 0; kk < DA / 16; kk++) umma(d, da + kstep_k(kk), dm + kstep_mn(kk), id_kmn, kk > 0);
+                    umma_commit(bar(B_MEMPTY + pb));
+                }
+                __syncwarp();
+                if (!(ok = wait(B_PFULL + pb, k2, 109))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t dp = d_p0 + pb * TT, dc = d_mn0 + st * ST + 2 * AB;
+                    const uint32_t d = tmem + COL_Y2 + pb * 64;
+#pragma unroll
+                    for (int kk = 0; kk < 4; kk++) umma(d, dp + (uint64_t)(kk * 2), dc + kstep_mn(kk), id_kmn, kk > 0);
+                    umma_commit(bar(B_YFULL + pb));
+                    umma_commit(bar(B_PEMPTY + pb));
+                    umma_commit(bar(B_EMPTY + st));
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            if (!(ok = wait(B_PFULL + pb, k2, 109))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t dp = d_p0 + pb * TT, dc = d_mn0 + st * ST + 2 * AB;
-#pragma unroll 1
-                for (int kk = 0; kk < 4; kk++)
-                    umma(tmem + COL_Y2 + pb * 64, dp + (uint64_t)(kk * 2), dc + kstep_mn(kk), id_kmn, kk > 0);
-                umma_commit(bar(B_YFULL + pb));
-                umma_commit(bar(B_PEMPTY + pb));
-                umma_commit(bar(B_EMPTY + st));
-            }
-            __syncwarp();
+            if (++st == NST) st = 0, k3++;
         }
         // every UMMA issued has completed before TMEM is freed
         if (elect_one()) umma_commit(bar(B_DRAIN));
@@ -268,159 +282,175 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         __syncwarp();
     } else if (warp < W_SC) {
         // ---- Cw = w c in three bf16 pieces; rows behind the sequence zeroed in B and C
-        const int wt = tid - W_CW * 32;                 // 0..127: 16-byte piece wt & 7 of rows wt/8 + 16u
+        const int wt = tid - W_CW * 32;                 // 16-byte piece wt & 7 of rows wt/8 + 16u
+        const int r0 = wt >> 3;
+        const float sw = g.scale_w;
+        int st = 0, k = 0;
         for (int c = 0; c < nch; c++) {
-            const int st = c % NST, pb = c & 1, L = chunk_n(c);
-            if (!wait(B_FULL + st, c / NST, 110)) break;
+            const int pb = c & 1, L = chunk_n(c);
+            if (!wait(B_FULL + st, k, 110)) break;
             if (c > 1 && !wait(B_CWEMPTY + pb, (c >> 1) - 1, 111)) break;
-            uint8_t *ct = sm + OFF_STAGE + st * SZ_STAGE + 2 * SZ_AB;
-            uint8_t *cw = sm + OFF_CW + pb * 3 * SZ_T;
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const int row = (wt >> 3) + 16 * u, o = (wt + 128 * u) * 16;
-                uint4 x = *reinterpret_cast<const uint4 *>(ct + o), hi, mid, lo;
+            uint8_t *ct = sm + OFF_STAGE + st * SZ_STAGE + 2 * SZ_AB + wt * 16;
+            uint8_t *cw = sm + OFF_CW + pb * 3 * SZ_T + wt * 16;
+            const float *wp = rev ? pw + r0 + 1 : pw + (L - 1 - r0);
+            const int dw = rev ? 16 : -16;
+#pragma unroll 1
+            for (int row = r0; row < Q; row += 16, ct += 2048, cw += 2048, wp += dw) {
+                uint4 x = *reinterpret_cast<const uint4 *>(ct);
                 float w = 0.f;
-                if (row < L) w = pw[rev ? row + 1 : L - 1 - row] * g.scale_w;
-                else x = make_uint4(0u, 0u, 0u, 0u);
+                if (row < L) {
+                    w = *wp * sw;
+                } else {
+                    // behind the sequence but inside the tensor: may hold anything
+                    x = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(ct) = x;
+                    *reinterpret_cast<uint4 *>(ct - SZ_AB) = x;
+                    *reinterpret_cast<uint4 *>(ct - SZ_AB / 2) = x;
+                }
+                // cut off, not rounded: the 24 bits of w c fall apart into three
+                // bf16 exactly, by masks and byte moves alone
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
                 uint32_t hs[4], ms[4], ls[4];
+                const f32x2 ww = pair(w, w);
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
-                    float v0 = bf16_lo(xs[q]) * w, v1 = bf16_hi(xs[q]) * w;
-                    hs[q] = pack_bf16(v0, v1);
-                    v0 -= bf16_lo(hs[q]);
-                    v1 -= bf16_hi(hs[q]);
-                    ms[q] = pack_bf16(v0, v1);
-                    ls[q] = pack_bf16(v0 - bf16_lo(ms[q]), v1 - bf16_hi(ms[q]));
+                    float a, b2;
+                    const f32x2 v = mul2(pair(bf16_lo(xs[q]), bf16_hi(xs[q])), ww);
+                    unpair(v, a, b2);
+                    hs[q] = cut2(a, b2);
+                    const f32x2 r = add2(v, pair(-cut(a), -cut(b2)));
+                    unpair(r, a, b2);
+                    ms[q] = cut2(a, b2);
+                    const f32x2 l = add2(r, pair(-cut(a), -cut(b2)));
+                    unpair(l, a, b2);
+                    ls[q] = cut2(a, b2);
                 }
-                hi = make_uint4(hs[0], hs[1], hs[2], hs[3]);
-                mid = make_uint4(ms[0], ms[1], ms[2], ms[3]);
-                lo = make_uint4(ls[0], ls[1], ls[2], ls[3]);
-                *reinterpret_cast<uint4 *>(cw + o) = lo;
-                *reinterpret_cast<uint4 *>(cw + SZ_T + o) = mid;
-                *reinterpret_cast<uint4 *>(cw + 2 * SZ_T + o) = hi;
-                if (row >= L) {
-                    // behind the sequence but inside the tensor: may hold anything
-                    *reinterpret_cast<uint4 *>(ct + o) = x;
-                    uint8_t *bt = sm + OFF_STAGE + st * SZ_STAGE + SZ_AB + o;
-                    *reinterpret_cast<uint4 *>(bt) = x;
-                    *reinterpret_cast<uint4 *>(bt + SZ_AB / 2) = x;
-                }
+                *reinterpret_cast<uint4 *>(cw) = make_uint4(ls[0], ls[1], ls[2], ls[3]);
+                *reinterpret_cast<uint4 *>(cw + SZ_T) = make_uint4(ms[0], ms[1], ms[2], ms[3]);
+                *reinterpret_cast<uint4 *>(cw + 2 * SZ_T) = make_uint4(hs[0], hs[1], hs[2], hs[3]);
             }
             fence_async_smem();
-            arrive(B_CWFULL + pb);
-            if (l32 == 0) mbar_arrive(bar(B_EMPTY + st));
+            __syncwarp();
+            if (l32 == 0) {
+                mbar_arrive(bar(B_CWFULL + pb));
+                mbar_arrive(bar(B_EMPTY + st));
+            }
+            if (++st == NST) st = 0, k++;
         }
     } else if (warp < W_ST) {
         // ---- scores: mask, round, store
         if (!SO) {
             const int q = warp & 3;                     // TMEM lane quarter: rows 16q .. 16q+15
-            const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+            const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + COL_S;
             const int ra = 16 * q + (l32 >> 2), cq = 2 * (l32 & 3);
-            float m[2][16];                             // the mask at this thread's places
+            f32x2 m[2][8];                              // the mask at this thread's places
 #pragma unroll
             for (int hf = 0; hf < 2; hf++)
 #pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    const int row = ra + ((e & 2) ? 8 : 0), s = 32 * hf + 8 * (e >> 2) + cq + (e & 1);
-                    const int d = rev ? s - row : row - s;
-                    m[hf][e] = d >= 0 ? pw[d] * g.scale_p : 0.f;
+                for (int e = 0; e < 8; e++) {
+                    const int row = ra + ((e & 1) ? 8 : 0), s = 32 * hf + 8 * (e >> 1) + cq;
+                    const int d0 = rev ? s - row : row - s, d1 = rev ? d0 + 1 : d0 - 1;
+                    m[hf][e] = pair(d0 >= 0 ? pw[d0] * g.scale_p : 0.f, d1 >= 0 ? pw[d1] * g.scale_p : 0.f);
                 }
+            // stmatrix: blocks (rows 0-7, 8-15) x (column groups i, i + 1)
+            const int mr = 16 * q + (l32 & 15), mc = l32 >> 4;
+            const uint32_t prow = sbase + OFF_P + mr * 128;
+            uint32_t po[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) po[i] = prow + (((2 * i + mc) ^ (mr & 7)) << 4);
+            // 16 x 32 blocks wholly on the masked side are zero: written into each buffer once
+            const int zhf = rev ? (q >= 2 ? 0 : 2) : (q < 2 ? 1 : 2);
             for (int c = 0; c < nch; c++) {
                 const int pb = c & 1, L = chunk_n(c);
-                uint8_t *pt = sm + OFF_P + pb * SZ_T;
                 if (!wait(B_SFULL + pb, c >> 1, 112)) break;
                 if (c > 1 && !wait(B_PEMPTY + pb, (c >> 1) - 1, 113)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
-                    // 16 x 32 blocks wholly on the masked side are zero: written
-                    // into each buffer once
-                    const bool zero = rev ? (hf == 0 && q >= 2) : (hf == 1 && q < 2);
-                    if (zero && c > 1) continue;
-                    float v[16];
-                    if (!zero) {
-                        tmem_ld16x256b_x4(tl + COL_S + pb * 64 + 32 * hf, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; e++) v[e] *= m[hf][e];
-                        if (L < Q) {                    // columns behind the sequence may be anything: select
-#pragma unroll
-                            for (int e = 0; e < 16; e++)
-                                if (32 * hf + 8 * (e >> 2) + cq + (e & 1) >= L) v[e] = 0.f;
+                    if (hf == zhf) {
+                        if (c < 2) {
+                            stmatrix4(po[2 * hf] + pb * SZ_T, 0u, 0u, 0u, 0u);
+                            stmatrix4(po[2 * hf + 1] + pb * SZ_T, 0u, 0u, 0u, 0u);
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e++) v[e] = 0.f;
+                        continue;
                     }
+                    float v[16];
+                    uint32_t o[8];
+                    tmem_ld16x256b_x4(tl + pb * 64 + 32 * hf, v);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int col = 32 * hf + 8 * i + cq;
-                        *reinterpret_cast<uint32_t *>(pt + sw128(ra, col)) = pack_bf16(v[4 * i], v[4 * i + 1]);
-                        *reinterpret_cast<uint32_t *>(pt + sw128(ra + 8, col)) = pack_bf16(v[4 * i + 2], v[4 * i + 3]);
+                    for (int e = 0; e < 8; e++) o[e] = round2(mul2(pair(v[2 * e], v[2 * e + 1]), m[hf][e]));
+                    if (L < Q) {                        // columns behind the sequence may be anything
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const int s = 32 * hf + 8 * (e >> 1) + cq;
+                            if (s >= L) o[e] = 0u;
+                            else if (s + 1 >= L) o[e] &= 0xffffu;
+                        }
                     }
+                    stmatrix4(po[2 * hf] + pb * SZ_T, o[0], o[1], o[2], o[3]);
+                    stmatrix4(po[2 * hf + 1] + pb * SZ_T, o[4], o[5], o[6], o[7]);
                 }
                 tc_fence_before();
                 fence_async_smem();
-                arrive(B_SEMPTY + pb);
-                if (l32 == 0) mbar_arrive(bar(B_PFULL + pb));
+                __syncwarp();
+                if (l32 == 0) {
+                    mbar_arrive(bar(B_SEMPTY + pb));
+                    mbar_arrive(bar(B_PFULL + pb));
+                }
             }
         }
     } else if (warp < W_Y) {
-        // ---- the state: this thread's row, 64 columns, fp32
+        // ---- the state: this thread's row, the tile's 64 columns, fp32
         const int q = warp & 3, n = 32 * q + l32;
-        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + COL_D;
         const size_t elems = (size_t)g.da * g.dc;
         float *slots = g.ws + (size_t)lane * (g.nseg - 1) * elems;
         const bool mine = n < g.da;
-        float M[DC];
+        f32x2 M[DC / 2];
         {
             const float *src = (SO || (seg == 0 && !g.m0)) ? nullptr
                                : (seg == 0 ? g.m0 + lane * elems : slots + (size_t)(seg - 1) * elems);
+            const bool tr = seg == 0 && g.m_trans;
 #pragma unroll
-            for (int p = 0; p < DC; p++) M[p] = 0.f;
+            for (int p = 0; p < DC / 2; p++) M[p] = 0ull;
             if (src && mine) {
-                if (seg == 0 && g.m_trans) {
 #pragma unroll
-                    for (int p = 0; p < DC; p++)
-                        if (p0 + p < g.dc) M[p] = src[(size_t)(p0 + p) * g.da + n];
-                } else {
-#pragma unroll
-                    for (int p = 0; p < DC; p += 4)     // dc is a multiple of 8
-                        if (p0 + p < g.dc) {
-                            const float4 v = *reinterpret_cast<const float4 *>(src + (size_t)n * g.dc + p0 + p);
-                            M[p] = v.x; M[p + 1] = v.y; M[p + 2] = v.z; M[p + 3] = v.w;
+                for (int p = 0; p < DC; p += 2)         // dc is a multiple of 8
+                    if (p0 + p < g.dc) {
+                        if (tr) {
+                            M[p / 2] = pair(src[(size_t)(p0 + p) * g.da + n], src[(size_t)(p0 + p + 1) * g.da + n]);
+                        } else {
+                            const float2 v = *reinterpret_cast<const float2 *>(src + (size_t)n * g.dc + p0 + p);
+                            M[p / 2] = pair(v.x, v.y);
                         }
-                }
+                    }
             }
         }
         auto publish = [&](int buf) {                   // the rounded copy that D3 reads
             uint8_t *mt = sm + OFF_M + buf * SZ_M + n * 128;
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                uint4 v;
-                v.x = pack_bf16(M[8 * k], M[8 * k + 1]);
-                v.y = pack_bf16(M[8 * k + 2], M[8 * k + 3]);
-                v.z = pack_bf16(M[8 * k + 4], M[8 * k + 5]);
-                v.w = pack_bf16(M[8 * k + 6], M[8 * k + 7]);
-                *reinterpret_cast<uint4 *>(mt + ((k ^ (n & 7)) << 4)) = v;
-            }
+            for (int k = 0; k < 8; k++)
+                *reinterpret_cast<uint4 *>(mt + ((k ^ (n & 7)) << 4)) =
+                    make_uint4(round2(M[4 * k]), round2(M[4 * k + 1]), round2(M[4 * k + 2]), round2(M[4 * k + 3]));
             fence_async_smem();
             arrive(B_MFULL + buf);
         };
         if (!SO && nch > 0) publish(0);
         for (int c = 0; c < nch; c++) {
             const int pb = c & 1;
-            const float dm1 = pm1[chunk_n(c)];
+            const float d1 = pm1[chunk_n(c)];
+            const f32x2 dm1 = pair(d1, d1);
             if (!wait(B_DFULL + pb, c >> 1, 114)) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < DC / 16; k++) {
                 float d[16];
-                tmem_ld16(tl + COL_D + pb * 64 + 16 * k, d);
+                tmem_ld16(tl + pb * 64 + 16 * k, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 16; u++) M[16 * k + u] = fmaf(M[16 * k + u], dm1, M[16 * k + u]) + d[u];
+                for (int u = 0; u < 8; u++)
+                    M[8 * k + u] = add2(fma2(M[8 * k + u], dm1, M[8 * k + u]), pair(d[2 * u], d[2 * u + 1]));
             }
             tc_fence_before();
             arrive(B_DEMPTY + pb);
@@ -433,76 +463,85 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         float *dst = SO ? slots + (size_t)seg * elems
                         : (seg == g.nseg - 1 && g.m_out ? g.m_out + lane * elems : nullptr);
         if (dst && mine && !*abort_flag) {
-            if (!SO && g.m_trans) {
+            const bool tr = !SO && g.m_trans;
 #pragma unroll
-                for (int p = 0; p < DC; p++)
-                    if (p0 + p < g.dc) dst[(size_t)(p0 + p) * g.da + n] = M[p];
-            } else {
-#pragma unroll
-                for (int p = 0; p < DC; p += 4)
-                    if (p0 + p < g.dc)
-                        *reinterpret_cast<float4 *>(dst + (size_t)n * g.dc + p0 + p) =
-                            make_float4(M[p], M[p + 1], M[p + 2], M[p + 3]);
-            }
+            for (int p = 0; p < DC; p += 2)
+                if (p0 + p < g.dc) {
+                    float a, b2;
+                    unpair(M[p / 2], a, b2);
+                    if (tr) {
+                        dst[(size_t)(p0 + p) * g.da + n] = a;
+                        dst[(size_t)(p0 + p + 1) * g.da + n] = b2;
+                    } else {
+                        *reinterpret_cast<float2 *>(dst + (size_t)n * g.dc + p0 + p) = make_float2(a, b2);
+                    }
+                }
         }
     } else if (!SO && g.y) {
         // ---- the answers
         const int q = warp & 3, wy = warp - W_Y;
         const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
-        const int r0 = l32 >> 2, ra = 16 * q + r0, rb = ra + 8, cq = 2 * (l32 & 3);
-        uint8_t *yt = sm + OFF_Y + 16 * q * 128;        // this warp's 16 rows
-        float *yf = static_cast<float *>(g.y);
+        const int ra = 16 * q + (l32 >> 2), rb = ra + 8, cq = 2 * (l32 & 3);
+        const int mr = l32 & 15, mc = l32 >> 4;         // stmatrix rows, as for the scores
+        const uint32_t ybase = sbase + OFF_Y + 16 * q * 128;   // this warp's 16 rows
+        uint32_t yo[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) yo[i] = ybase + mr * 128 + (((2 * i + mc) ^ (mr & 7)) << 4);
+        const float si = g.scale_i;
+        const bool f32 = g.y_f32;
+        float *yf = static_cast<float *>(g.y) + ((b * g.T + t_beg) * g.H + h) * g.dc + p0 + cq;
         for (int c = 0; c < nch; c++) {
-            const int pb = c & 1, L = chunk_n(c);
-            const int64_t t = t_beg + chunk_t(c);
+            const int pb = c & 1, L = chunk_n(c), t = chunk_t(c);
             if (!wait(B_YFULL + pb, c >> 1, 116)) break;
             tc_fence_after();
-            const bool la = ra < L, lb = rb < L;
-            const float fa = la ? pw[rev ? L - 1 - ra : ra + 1] * g.scale_i : 0.f;
-            const float fb = lb ? pw[rev ? L - 1 - rb : rb + 1] * g.scale_i : 0.f;
-            if (!g.y_f32) {
+            const float fa = ra < L ? pw[rev ? L - 1 - ra : ra + 1] * si : 0.f;
+            const float fb = rb < L ? pw[rev ? L - 1 - rb : rb + 1] * si : 0.f;
+            const f32x2 fa2 = pair(fa, fa), fb2 = pair(fb, fb);
+            if (!f32) {
                 if (l32 == 0) tma_store_wait_read();    // the rows of the chunk before are on their way
                 __syncwarp();
             }
 #pragma unroll
             for (int hf = 0; hf < 2; hf++) {
                 float y2[16], y3[16];
+                f32x2 o[8];
                 tmem_ld16x256b_x4(tl + COL_Y2 + pb * 64 + 32 * hf, y2);
                 tmem_ld16x256b_x4(tl + COL_Y3 + pb * 64 + 32 * hf, y3);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int col = 32 * hf + 8 * i + cq;
-                    const float a0 = la ? fmaf(fa, y3[4 * i], y2[4 * i]) : 0.f;
-                    const float a1 = la ? fmaf(fa, y3[4 * i + 1], y2[4 * i + 1]) : 0.f;
-                    const float b0 = lb ? fmaf(fb, y3[4 * i + 2], y2[4 * i + 2]) : 0.f;
-                    const float b1 = lb ? fmaf(fb, y3[4 * i + 3], y2[4 * i + 3]) : 0.f;
-                    if (!g.y_f32) {
-                        *reinterpret_cast<uint32_t *>(yt + sw128(r0, col)) = pack_bf16(a0, a1);
-                        *reinterpret_cast<uint32_t *>(yt + sw128(r0 + 8, col)) = pack_bf16(b0, b1);
-                    } else if (p0 + col < g.dc) {       // dc is a multiple of 8: pairs stay whole
-                        if (t + ra < g.T)
-                            *reinterpret_cast<float2 *>(yf + ((b * g.T + t + ra) * g.H + h) * g.dc + p0 + col) =
-                                make_float2(a0, a1);
-                        if (t + rb < g.T)
-                            *reinterpret_cast<float2 *>(yf + ((b * g.T + t + rb) * g.H + h) * g.dc + p0 + col) =
-                                make_float2(b0, b1);
+                for (int e = 0; e < 8; e++)
+                    o[e] = fma2((e & 1) ? fb2 : fa2, pair(y3[2 * e], y3[2 * e + 1]), pair(y2[2 * e], y2[2 * e + 1]));
+                if (L < Q) {                            // rows behind the sequence are zeros
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (((e & 1) ? rb : ra) >= L) o[e] = 0ull;
+                }
+                if (!f32) {
+                    stmatrix4(yo[2 * hf], round2(o[0]), round2(o[1]), round2(o[2]), round2(o[3]));
+                    stmatrix4(yo[2 * hf + 1], round2(o[4]), round2(o[5]), round2(o[6]), round2(o[7]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const int row = (e & 1) ? rb : ra, col = 32 * hf + 8 * (e >> 1);
+                        // dc is a multiple of 8: a pair is inside or outside
+                        if (p0 + col + cq < g.dc && t_beg + t + row < g.T)
+                            *reinterpret_cast<f32x2 *>(yf + (int64_t)(t + row) * g.H * g.dc + col) = o[e];
                     }
                 }
             }
             tc_fence_before();
-            arrive(B_YEMPTY + pb);
-            if (!g.y_f32) {
-                fence_async_smem();
-                __syncwarp();
-                if (l32 == 0 && t + 16 * q < g.T)
-                    tma_store4(&P.my[pi], p0, (int)h, (int)(t + 16 * q), (int)b, sbase + OFF_Y + 16 * q * 128);
-                __syncwarp();
+            fence_async_smem();
+            __syncwarp();
+            if (l32 == 0) {
+                mbar_arrive(bar(B_YEMPTY + pb));
+                if (!f32 && t_beg + t + 16 * q < g.T)
+                    tma_store4(&P.my[pi], p0, (int)h, (int)t_beg + t + 16 * q, (int)b, ybase);
             }
+            __syncwarp();
         }
         // rows behind the sequence in the segment's chunks that were not walked: zeros
         const int64_t e = t_beg + g.seg_len < g.T ? t_beg + g.seg_len : g.T;
-        const int cols = g.dc - p0 < DC ? g.dc - p0 : DC, es = g.y_f32 ? 4 : 2, nv = cols * es / 16;
+        const int cols = g.dc - p0 < DC ? g.dc - p0 : DC, es = f32 ? 4 : 2, nv = cols * es / 16;
         for (int64_t t = t_beg + (int64_t)nch * Q + wy; t < e; t += 4) {
             uint8_t *row = static_cast<uint8_t *>(g.y) + (((b * g.T + t) * g.H + h) * g.dc + p0) * es;
             for (int v = l32; v < nv; v += 32) reinterpret_cast<uint4 *>(row)[v] = make_uint4(0u, 0u, 0u, 0u);
