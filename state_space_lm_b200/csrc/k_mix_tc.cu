@@ -20,8 +20,10 @@
 // bf16 pieces, hi + mid + lo = w c exactly, summed by the tensor cores.
 //
 // One CTA owns one lane, one tile of 64 columns of c and one segment of the
-// time axis, and walks its chunks.  18 warps: 0 TMA, 1 UMMA issue (and TMEM),
-// 2-5 Cw, 6-9 scores, 10-13 state, 14-17 outputs.  The hand-overs are buffered
+// time axis, and walks its chunks.  20 warps: 0 TMA, 1-3 UMMA issue (D1 and D2; D4; D3),
+// 4-7 Cw, 8-11 scores, 12-15 state, 16-19 outputs.  Three issuing warps, not
+// one: a section of waits, fence, issue and commit takes a warp 400 to 700
+// cycles, four of them in a row more than anything else in a chunk.  The hand-overs are buffered
 // in TMEM or shared memory, so the roles work on different chunks;
 // the chain from chunk to chunk is only the state's update.  A split time
 // axis takes two passes: B and C alone for every segment's own state, the
@@ -40,7 +42,8 @@ namespace mixtc {
 using namespace ptx;
 
 constexpr int Q = 64, DC = 64, DA = 128;               // chunk, columns of a tile, widest a and b rows
-constexpr int W_TMA = 0, W_MMA = 1, W_CW = 2, W_SC = 6, W_ST = 10, W_Y = 14, NWARPS = 18, THREADS = NWARPS * 32;
+constexpr int W_TMA = 0, W_SY = 1, W_D = 2, W_IN = 3, W_CW = 4, W_SC = 8, W_ST = 12, W_Y = 16, NWARPS = 20;
+constexpr int THREADS = NWARPS * 32;
 
 // ---- shared memory (bytes from a 1024-aligned base), all tiles 128B-swizzled
 constexpr int NST = 3;                                  // stages of A, B, C
@@ -70,8 +73,8 @@ enum {
     B_MEMPTY = B_MFULL + 2,
     B_YFULL = B_MEMPTY + 2,        // both parts of the answer in TMEM
     B_YEMPTY = B_YFULL + 2,
-    B_DRAIN = B_YEMPTY + 2,
-    NBAR
+    B_DRAIN = B_YEMPTY + 2,        // 3: every UMMA of an issuing warp is done
+    NBAR = B_DRAIN + 3
 };
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     if (tid == 0) {
         for (int i = 0; i < NST; i++) {
             mbar_init(bar(B_FULL + i), 1);
-            mbar_init(bar(B_EMPTY + i), 5);             // the chunk's last UMMA, four Cw warps
+            mbar_init(bar(B_EMPTY + i), SO ? 5 : 7);    // each issuing warp's last UMMA, four Cw warps
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(bar(B_CWFULL + i), 4);
@@ -142,23 +145,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             mbar_init(bar(B_DEMPTY + i), 4);
             mbar_init(bar(B_MFULL + i), 4);
             mbar_init(bar(B_MEMPTY + i), 1);
-            mbar_init(bar(B_YFULL + i), 1);
+            mbar_init(bar(B_YFULL + i), 2);             // D2 and D3
             mbar_init(bar(B_YEMPTY + i), 4);
         }
-        mbar_init(bar(B_DRAIN), 1);
+        for (int i = 0; i < 3; i++) mbar_init(bar(B_DRAIN + i), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == W_MMA) {
+    if (warp == W_SY) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(TMEM_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (tid >= 64 && tid < 64 + Q + 1) {
+    if (tid >= 128 && tid <= 128 + Q) {
         const double lg = (double)g.log_decay[h];
-        pw[tid - 64] = decay_pow(lg, tid - 64);
-        pm1[tid - 64] = decay_pow_m1(lg, tid - 64);
+        pw[tid - 128] = decay_pow(lg, tid - 128);
+        pm1[tid - 128] = decay_pow_m1(lg, tid - 128);
     }
     tc_fence_before();
     __syncthreads();
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 while (!mbar_try(bar(B_FULL + c % NST), (c / NST) & 1) && clock64() - t0 < WAIT_LIMIT_CYCLES / 16) {
                 }
         }
-    } else if (warp == W_MMA) {
+    } else if (warp < W_CW) {
         constexpr uint32_t id_kk = idesc(64, 64, 0, 0), id_kmn = idesc(64, 64, 0, 1), id_st = idesc(128, 64, 1, 1);
         // K-major operand, K-step kk of 16: 32 bytes inside a 128-byte row, the
         // second 64 columns Q rows further; MN-major: two groups of 8 rows.
@@ -209,56 +212,30 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         const uint64_t d_cw0 = sdesc(sbase + OFF_CW, Q * 128, 1024), d_p0 = sdesc(sbase + OFF_P, 16, 1024);
         const uint64_t d_m0 = sdesc(sbase + OFF_M, DA * 128, 1024);
         constexpr uint64_t ST = SZ_STAGE >> 4, AB = SZ_AB >> 4, TT = SZ_T >> 4, MM = SZ_M >> 4;
-        int s1 = 0, k1 = 0;                             // stage and turn of the scores, one chunk ahead
-        auto scores = [&](int c) {                      // D1 of chunk c
-            if (!wait(B_FULL + s1, k1, 102)) return false;
-            if (c > 1 && !wait(B_SEMPTY + (c & 1), (c >> 1) - 1, 103)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t da = d_k0 + s1 * ST, db = da + AB;
-                const uint32_t d = tmem + COL_S + (c & 1) * 64;
-#pragma unroll
-                for (int kk = 0; kk < DA / 16; kk++) umma(d, da + kstep_k(kk), db + kstep_k(kk), id_kk, kk > 0);
-                umma_commit(bar(B_SFULL + (c & 1)));
-            }
-            __syncwarp();
-            if (++s1 == NST) s1 = 0, k1++;
-            return true;
-        };
-        bool ok = SO || nch == 0 || scores(0);
-        int st = 0, k3 = 0;
-        for (int c = 0; c < nch && ok; c++) {
-            const int pb = c & 1, k2 = c >> 1;
-            if (!SO && c + 1 < nch && !(ok = scores(c + 1))) break;
-            // D4: the stage has arrived, since Cw was built from it
-            if (!(ok = wait(B_CWFULL + pb, k2, 104))) break;
-            if (SO && !(ok = wait(B_FULL + st, k3, 105))) break;
-            if (c > 1 && !(ok = wait(B_DEMPTY + pb, k2 - 1, 106))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t db = d_mn0 + st * ST + AB, dw = d_cw0 + pb * (3 * TT);
-                const uint32_t d = tmem + COL_D + pb * 64;
-#pragma unroll
-                for (int kk = 0; kk < 12; kk++)         // the pieces lo, mid, hi of 4 K-steps
-                    umma(d, db + kstep_mn(kk & 3), dw + (kk >> 2) * TT + kstep_mn(kk & 3), id_st, kk > 0);
-                umma_commit(bar(B_DFULL + pb));
-                umma_commit(bar(B_CWEMPTY + pb));
-                if (SO) umma_commit(bar(B_EMPTY + st));
-            }
-            __syncwarp();
-            if (!SO) {
-                if (!(ok = wait(B_MFULL + pb, k2, 107))) break;
-                if (c > 1 && !(ok = wait(B_YEMPTY + pb, k2 - 1, 108))) break;
+        int st = 0, k3 = 0;                             // stage, turn of the ring
+        if (warp == W_SY && !SO) {
+            int s1 = 0, k1 = 0;                         // the scores run one chunk ahead
+            auto scores = [&](int c) {                  // D1 of chunk c
+                if (!wait(B_FULL + s1, k1, 102)) return false;
+                if (c > 1 && !wait(B_SEMPTY + (c & 1), (c >> 1) - 1, 103)) return false;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t da = d_k0 + st * ST, dm = d_m0 + pb * MM;
-                    const uint32_t d = tmem + COL_Y3 + pb * 64;
+                    const uint64_t da = d_k0 + s1 * ST, db = da + AB;
+                    const uint32_t d = tmem + COL_S + (c & 1) * 64;
 #pragma unroll
-                    for (int kk = 0; kk < DA / 16; kk++) umma(d, da + kstep_k(kk), dm + kstep_mn(kk), id_kmn, kk > 0);
-                    umma_commit(bar(B_MEMPTY + pb));
+                    for (int kk = 0; kk < DA / 16; kk++) umma(d, da + kstep_k(kk), db + kstep_k(kk), id_kk, kk > 0);
+                    umma_commit(bar(B_SFULL + (c & 1)));
                 }
                 __syncwarp();
+                if (++s1 == NST) s1 = 0, k1++;
+                return true;
+            };
+            bool ok = nch == 0 || scores(0);
+            for (int c = 0; c < nch && ok; c++) {
+                const int pb = c & 1, k2 = c >> 1;
+                if (c + 1 < nch && !(ok = scores(c + 1))) break;
                 if (!(ok = wait(B_PFULL + pb, k2, 109))) break;
+                if (c > 1 && !(ok = wait(B_YEMPTY + pb, k2 - 1, 108))) break;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t dp = d_p0 + pb * TT, dc = d_mn0 + st * ST + 2 * AB;
@@ -270,18 +247,58 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     umma_commit(bar(B_EMPTY + st));
                 }
                 __syncwarp();
+                if (++st == NST) st = 0, k3++;
             }
-            if (++st == NST) st = 0, k3++;
+        } else if (warp == W_D) {
+            for (int c = 0; c < nch; c++) {
+                const int pb = c & 1, k2 = c >> 1;
+                if (!wait(B_FULL + st, k3, 105)) break;
+                if (!wait(B_CWFULL + pb, k2, 104)) break;
+                if (c > 1 && !wait(B_DEMPTY + pb, k2 - 1, 106)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t db = d_mn0 + st * ST + AB, dw = d_cw0 + pb * (3 * TT);
+                    const uint32_t d = tmem + COL_D + pb * 64;
+#pragma unroll
+                    for (int kk = 0; kk < 12; kk++)     // the pieces lo, mid, hi of 4 K-steps
+                        umma(d, db + kstep_mn(kk & 3), dw + (kk >> 2) * TT + kstep_mn(kk & 3), id_st, kk > 0);
+                    umma_commit(bar(B_DFULL + pb));
+                    umma_commit(bar(B_CWEMPTY + pb));
+                    umma_commit(bar(B_EMPTY + st));
+                }
+                __syncwarp();
+                if (++st == NST) st = 0, k3++;
+            }
+        } else if (warp == W_IN && !SO) {
+            for (int c = 0; c < nch; c++) {
+                const int pb = c & 1, k2 = c >> 1;
+                if (!wait(B_FULL + st, k3, 118)) break;
+                if (c > 1 && !wait(B_YEMPTY + pb, k2 - 1, 119)) break;
+                if (!wait(B_MFULL + pb, k2, 107)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t da = d_k0 + st * ST, dm = d_m0 + pb * MM;
+                    const uint32_t d = tmem + COL_Y3 + pb * 64;
+#pragma unroll
+                    for (int kk = 0; kk < DA / 16; kk++) umma(d, da + kstep_k(kk), dm + kstep_mn(kk), id_kmn, kk > 0);
+                    umma_commit(bar(B_MEMPTY + pb));
+                    umma_commit(bar(B_YFULL + pb));
+                    umma_commit(bar(B_EMPTY + st));
+                }
+                __syncwarp();
+                if (++st == NST) st = 0, k3++;
+            }
         }
-        // every UMMA issued has completed before TMEM is freed
-        if (elect_one()) umma_commit(bar(B_DRAIN));
+        // every UMMA this warp issued has completed before TMEM is freed
+        const int dr = B_DRAIN + warp - W_SY;
+        if (elect_one()) umma_commit(bar(dr));
         __syncwarp();
         const long long t0 = clock64();
-        while (!mbar_try(bar(B_DRAIN), 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+        while (!mbar_try(bar(dr), 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
         }
         __syncwarp();
     } else if (warp < W_SC) {
-        // ---- Cw = w c in three bf16 pieces; rows behind the sequence zeroed in B and C
+        // ---- Cw = w c in three bf16 pieces; rows behind the sequence zeroed in B
         const int wt = tid - W_CW * 32;                 // 16-byte piece wt & 7 of rows wt/8 + 16u
         const int r0 = wt >> 3;
         const float sw = g.scale_w;
@@ -301,9 +318,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 if (row < L) {
                     w = *wp * sw;
                 } else {
-                    // behind the sequence but inside the tensor: may hold anything
+                    // behind the sequence but inside the tensor: may hold
+                    // anything, and D4 multiplies it (D2's C rows are zeroed by
+                    // the score warps, which hand D2 its chunk)
                     x = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(ct) = x;
                     *reinterpret_cast<uint4 *>(ct - SZ_AB) = x;
                     *reinterpret_cast<uint4 *>(ct - SZ_AB / 2) = x;
                 }
@@ -360,6 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             for (int i = 0; i < 4; i++) po[i] = prow + (((2 * i + mc) ^ (mr & 7)) << 4);
             // 16 x 32 blocks wholly on the masked side are zero: written into each buffer once
             const int zhf = rev ? (q >= 2 ? 0 : 2) : (q < 2 ? 1 : 2);
+            int st = 0;
             for (int c = 0; c < nch; c++) {
                 const int pb = c & 1, L = chunk_n(c);
                 if (!wait(B_SFULL + pb, c >> 1, 112)) break;
@@ -391,6 +410,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     stmatrix4(po[2 * hf] + pb * SZ_T, o[0], o[1], o[2], o[3]);
                     stmatrix4(po[2 * hf + 1] + pb * SZ_T, o[4], o[5], o[6], o[7]);
                 }
+                if (L < Q)                              // this warp's 16 rows of C, those behind the sequence
+                    for (int r = 16 * q + (l32 >> 3); r < 16 * q + 16; r += 4)
+                        if (r >= L)
+                            *reinterpret_cast<uint4 *>(sm + OFF_STAGE + st * SZ_STAGE + 2 * SZ_AB + r * 128 +
+                                                       (l32 & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 tc_fence_before();
                 fence_async_smem();
                 __syncwarp();
@@ -398,6 +422,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     mbar_arrive(bar(B_SEMPTY + pb));
                     mbar_arrive(bar(B_PFULL + pb));
                 }
+                if (++st == NST) st = 0;
             }
         }
     } else if (warp < W_Y) {
@@ -556,7 +581,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == W_MMA) {
+    if (warp == W_SY) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
     }
