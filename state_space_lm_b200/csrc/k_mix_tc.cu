@@ -20,7 +20,7 @@
 // bf16 pieces, hi + mid + lo = w c exactly, summed by the tensor cores.
 //
 // One CTA owns one lane, one tile of 64 columns of c and one segment of the
-// time axis, and walks its chunks.  20 warps: 0 TMA, 1-3 UMMA issue (D1 and D2; D4; D3),
+// time axis, and walks its chunks.  20 warps: 0 TMA, 1-3 UMMA issue (D1; D4; D3 and D2),
 // 4-7 Cw, 8-11 scores, 12-15 state, 16-19 outputs.  Three issuing warps, not
 // one: a section of waits, fence, issue and commit takes a warp 400 to 700
 // cycles, four of them in a row more than anything else in a chunk.  The hand-overs are buffered
@@ -42,11 +42,12 @@ namespace mixtc {
 using namespace ptx;
 
 constexpr int Q = 64, DC = 64, DA = 128;               // chunk, columns of a tile, widest a and b rows
-constexpr int W_TMA = 0, W_SY = 1, W_D = 2, W_IN = 3, W_CW = 4, W_SC = 8, W_ST = 12, W_Y = 16, NWARPS = 20;
+constexpr int W_TMA = 0, W_S = 1, W_D = 2, W_Y23 = 3, W_CW = 4, W_SC = 8, W_ST = 12, W_Y = 16, NWARPS = 20;
 constexpr int THREADS = NWARPS * 32;
 
 // ---- shared memory (bytes from a 1024-aligned base), all tiles 128B-swizzled
 constexpr int NST = 3;                                  // stages of A, B, C
+constexpr int PFD = 3;                                  // chunks that the L2 prefetch runs ahead of the loads
 constexpr int SZ_AB = Q * DA * 2, SZ_C = Q * DC * 2, SZ_STAGE = 2 * SZ_AB + SZ_C;
 constexpr int SZ_T = Q * DC * 2;                        // one 64 x 64 bf16 tile
 constexpr int SZ_M = DA * DC * 2;
@@ -61,19 +62,19 @@ constexpr int OFF_BAR = OFF_PW + 2 * NPW * 4;
 enum {
     B_FULL = 0,                    // NST: a stage has arrived
     B_EMPTY = B_FULL + NST,        // NST: its readers are done
-    B_CWFULL = B_EMPTY + NST,      // 2 of each from here on
-    B_CWEMPTY = B_CWFULL + 2,
-    B_SFULL = B_CWEMPTY + 2,       // scores in TMEM
+    // 2 of each from here on.  "Full" of an accumulator also says that the
+    // operands it was made from may be overwritten: Cw (D), P and M (Y)
+    B_CWFULL = B_EMPTY + NST,      // Cw in shared memory
+    B_SFULL = B_CWFULL + 2,        // scores in TMEM
     B_SEMPTY = B_SFULL + 2,
     B_PFULL = B_SEMPTY + 2,        // masked scores in shared memory
-    B_PEMPTY = B_PFULL + 2,
-    B_DFULL = B_PEMPTY + 2,        // a chunk's own state in TMEM
+    B_DFULL = B_PFULL + 2,         // a chunk's own state in TMEM
     B_DEMPTY = B_DFULL + 2,
     B_MFULL = B_DEMPTY + 2,        // the entering state in shared memory
-    B_MEMPTY = B_MFULL + 2,
-    B_YFULL = B_MEMPTY + 2,        // both parts of the answer in TMEM
+    B_YFULL = B_MFULL + 2,         // both parts of the answer in TMEM
     B_YEMPTY = B_YFULL + 2,
-    B_DRAIN = B_YEMPTY + 2,        // 3: every UMMA of an issuing warp is done
+    B_ZERO = B_YEMPTY + 2,         // 1: rows behind the sequence are zeroed in B and C
+    B_DRAIN = B_ZERO + 1,          // 3: every UMMA of an issuing warp is done
     NBAR = B_DRAIN + 3
 };
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -132,27 +133,25 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     if (tid == 0) {
         for (int i = 0; i < NST; i++) {
             mbar_init(bar(B_FULL + i), 1);
-            mbar_init(bar(B_EMPTY + i), SO ? 5 : 7);    // each issuing warp's last UMMA, four Cw warps
+            mbar_init(bar(B_EMPTY + i), SO ? 5 : 6);    // D4, D2 and D3; four Cw warps
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(bar(B_CWFULL + i), 4);
-            mbar_init(bar(B_CWEMPTY + i), 1);
             mbar_init(bar(B_SFULL + i), 1);
             mbar_init(bar(B_SEMPTY + i), 4);
             mbar_init(bar(B_PFULL + i), 4);
-            mbar_init(bar(B_PEMPTY + i), 1);
             mbar_init(bar(B_DFULL + i), 1);
             mbar_init(bar(B_DEMPTY + i), 4);
             mbar_init(bar(B_MFULL + i), 4);
-            mbar_init(bar(B_MEMPTY + i), 1);
-            mbar_init(bar(B_YFULL + i), 2);             // D2 and D3
+            mbar_init(bar(B_YFULL + i), 1);
             mbar_init(bar(B_YEMPTY + i), 4);
         }
+        mbar_init(bar(B_ZERO), 4);
         for (int i = 0; i < 3; i++) mbar_init(bar(B_DRAIN + i), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == W_SY) {
+    if (warp == W_S) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(TMEM_COLS)
                      : "memory");
@@ -187,6 +186,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     tma_load4(s0 + SZ_AB + x * (SZ_AB / 2), &P.mb[pi], 64 * x, hb, t, (int)b, fb);
                 }
                 tma_load4(s0 + 2 * SZ_AB, &P.mc[pi], p0, hc, t, (int)b, fb);
+                // the chunk that this stage takes next, on its way to L2
+                if (c + PFD < nch) {
+                    const int tp = (int)t_beg + chunk_t(c + PFD);
+                    for (int x = 0; x < g.da; x += 64) {
+                        if (!SO) tma_prefetch4(&P.ma[pi], x, ha, tp, (int)b);
+                        tma_prefetch4(&P.mb[pi], x, hb, tp, (int)b);
+                    }
+                    tma_prefetch4(&P.mc[pi], p0, hc, tp, (int)b);
+                }
             }
             __syncwarp();
             if (++st == NST) st = 0, k++;
@@ -201,50 +209,35 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         }
     } else if (warp < W_CW) {
         constexpr uint32_t id_kk = idesc(64, 64, 0, 0), id_kmn = idesc(64, 64, 0, 1), id_st = idesc(128, 64, 1, 1);
-        // K-major operand, K-step kk of 16: 32 bytes inside a 128-byte row, the
-        // second 64 columns Q rows further; MN-major: two groups of 8 rows.
-        // The issue loops are unrolled: rolled, the descriptor arithmetic
-        // between two UMMAs takes 65 to 100 cycles, twice what a UMMA does
-        // (measured beside busy warps: 3264 against 1437 cycles for a chunk's).
-        constexpr auto kstep_k = [](int kk) { return (uint64_t)(((kk >> 2) * (Q * 128) + (kk & 3) * 32) >> 4); };
-        constexpr auto kstep_mn = [](int kk) { return (uint64_t)((kk * 2048) >> 4); };
+        // Descriptor steps (16-byte units): a K-step of 16 is 32 bytes of a
+        // K-major row (the second 64 columns lie half a tile further), and two
+        // groups of 8 rows (MN) of an MN-major one.  The issue loops are
+        // unrolled by four: rolled, the descriptor arithmetic between two
+        // UMMAs takes 65 to 100 cycles, twice what a UMMA does (measured
+        // beside busy warps: 3264 against 1437 cycles for a chunk's); unrolled
+        // further, the code of all roles leaves the instruction cache.
+        constexpr uint64_t MN = 2048 >> 4;
         const uint64_t d_k0 = sdesc(sbase + OFF_STAGE, 16, 1024), d_mn0 = sdesc(sbase + OFF_STAGE, Q * 128, 1024);
         const uint64_t d_cw0 = sdesc(sbase + OFF_CW, Q * 128, 1024), d_p0 = sdesc(sbase + OFF_P, 16, 1024);
         const uint64_t d_m0 = sdesc(sbase + OFF_M, DA * 128, 1024);
         constexpr uint64_t ST = SZ_STAGE >> 4, AB = SZ_AB >> 4, TT = SZ_T >> 4, MM = SZ_M >> 4;
         int st = 0, k3 = 0;                             // stage, turn of the ring
-        if (warp == W_SY && !SO) {
-            int s1 = 0, k1 = 0;                         // the scores run one chunk ahead
-            auto scores = [&](int c) {                  // D1 of chunk c
-                if (!wait(B_FULL + s1, k1, 102)) return false;
-                if (c > 1 && !wait(B_SEMPTY + (c & 1), (c >> 1) - 1, 103)) return false;
+        if (warp == W_S && !SO) {
+            for (int c = 0; c < nch; c++) {
+                const int pb = c & 1;
+                if (!wait(B_FULL + st, k3, 102)) break;
+                if (c > 1 && !wait(B_SEMPTY + pb, (c >> 1) - 1, 103)) break;
+                if (chunk_n(c) < Q && !wait(B_ZERO, 0, 120)) break;     // one chunk of the walk at most
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t da = d_k0 + s1 * ST, db = da + AB;
-                    const uint32_t d = tmem + COL_S + (c & 1) * 64;
+                    const uint64_t da = d_k0 + st * ST, db = da + AB;
+                    const uint32_t d = tmem + COL_S + pb * 64;
+#pragma unroll 1
+                    for (int x = 0; x < 2; x++)
 #pragma unroll
-                    for (int kk = 0; kk < DA / 16; kk++) umma(d, da + kstep_k(kk), db + kstep_k(kk), id_kk, kk > 0);
-                    umma_commit(bar(B_SFULL + (c & 1)));
-                }
-                __syncwarp();
-                if (++s1 == NST) s1 = 0, k1++;
-                return true;
-            };
-            bool ok = nch == 0 || scores(0);
-            for (int c = 0; c < nch && ok; c++) {
-                const int pb = c & 1, k2 = c >> 1;
-                if (c + 1 < nch && !(ok = scores(c + 1))) break;
-                if (!(ok = wait(B_PFULL + pb, k2, 109))) break;
-                if (c > 1 && !(ok = wait(B_YEMPTY + pb, k2 - 1, 108))) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t dp = d_p0 + pb * TT, dc = d_mn0 + st * ST + 2 * AB;
-                    const uint32_t d = tmem + COL_Y2 + pb * 64;
-#pragma unroll
-                    for (int kk = 0; kk < 4; kk++) umma(d, dp + (uint64_t)(kk * 2), dc + kstep_mn(kk), id_kmn, kk > 0);
-                    umma_commit(bar(B_YFULL + pb));
-                    umma_commit(bar(B_PEMPTY + pb));
-                    umma_commit(bar(B_EMPTY + st));
+                        for (int kk = 0; kk < 4; kk++)
+                            umma(d, da + x * (AB / 2) + kk * 2, db + x * (AB / 2) + kk * 2, id_kk, x + kk > 0);
+                    umma_commit(bar(B_SFULL + pb));
                 }
                 __syncwarp();
                 if (++st == NST) st = 0, k3++;
@@ -253,35 +246,47 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             for (int c = 0; c < nch; c++) {
                 const int pb = c & 1, k2 = c >> 1;
                 if (!wait(B_FULL + st, k3, 105)) break;
-                if (!wait(B_CWFULL + pb, k2, 104)) break;
                 if (c > 1 && !wait(B_DEMPTY + pb, k2 - 1, 106)) break;
+                if (!wait(B_CWFULL + pb, k2, 104)) break;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t db = d_mn0 + st * ST + AB, dw = d_cw0 + pb * (3 * TT);
                     const uint32_t d = tmem + COL_D + pb * 64;
+#pragma unroll 1
+                    for (int x = 0; x < 3; x++)         // the pieces lo, mid, hi
 #pragma unroll
-                    for (int kk = 0; kk < 12; kk++)     // the pieces lo, mid, hi of 4 K-steps
-                        umma(d, db + kstep_mn(kk & 3), dw + (kk >> 2) * TT + kstep_mn(kk & 3), id_st, kk > 0);
+                        for (int kk = 0; kk < 4; kk++)
+                            umma(d, db + kk * MN, dw + x * TT + kk * MN, id_st, x + kk > 0);
                     umma_commit(bar(B_DFULL + pb));
-                    umma_commit(bar(B_CWEMPTY + pb));
                     umma_commit(bar(B_EMPTY + st));
                 }
                 __syncwarp();
                 if (++st == NST) st = 0, k3++;
             }
-        } else if (warp == W_IN && !SO) {
+        } else if (warp == W_Y23 && !SO) {
             for (int c = 0; c < nch; c++) {
                 const int pb = c & 1, k2 = c >> 1;
-                if (!wait(B_FULL + st, k3, 118)) break;
-                if (c > 1 && !wait(B_YEMPTY + pb, k2 - 1, 119)) break;
-                if (!wait(B_MFULL + pb, k2, 107)) break;
+                if (!wait(B_FULL + st, k3, 107)) break;
+                if (c > 1 && !wait(B_YEMPTY + pb, k2 - 1, 108)) break;
+                if (!wait(B_MFULL + pb, k2, 109)) break;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t da = d_k0 + st * ST, dm = d_m0 + pb * MM;
                     const uint32_t d = tmem + COL_Y3 + pb * 64;
+#pragma unroll 1
+                    for (int x = 0; x < 2; x++)
 #pragma unroll
-                    for (int kk = 0; kk < DA / 16; kk++) umma(d, da + kstep_k(kk), dm + kstep_mn(kk), id_kmn, kk > 0);
-                    umma_commit(bar(B_MEMPTY + pb));
+                        for (int kk = 0; kk < 4; kk++)
+                            umma(d, da + x * (AB / 2) + kk * 2, dm + (4 * x + kk) * MN, id_kmn, x + kk > 0);
+                }
+                __syncwarp();
+                if (!wait(B_PFULL + pb, k2, 118)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t dp = d_p0 + pb * TT, dc = d_mn0 + st * ST + 2 * AB;
+                    const uint32_t d = tmem + COL_Y2 + pb * 64;
+#pragma unroll
+                    for (int kk = 0; kk < 4; kk++) umma(d, dp + kk * 2, dc + kk * MN, id_kmn, kk > 0);
                     umma_commit(bar(B_YFULL + pb));
                     umma_commit(bar(B_EMPTY + st));
                 }
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             }
         }
         // every UMMA this warp issued has completed before TMEM is freed
-        const int dr = B_DRAIN + warp - W_SY;
+        const int dr = B_DRAIN + warp - W_S;
         if (elect_one()) umma_commit(bar(dr));
         __syncwarp();
         const long long t0 = clock64();
@@ -298,33 +303,38 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         }
         __syncwarp();
     } else if (warp < W_SC) {
-        // ---- Cw = w c in three bf16 pieces; rows behind the sequence zeroed in B
+        // ---- Cw = w c in three bf16 pieces; rows behind the sequence zeroed in B and C
         const int wt = tid - W_CW * 32;                 // 16-byte piece wt & 7 of rows wt/8 + 16u
         const int r0 = wt >> 3;
+        const f32x2 neg1 = pair(-1.f, -1.f);
         const float sw = g.scale_w;
         int st = 0, k = 0;
         for (int c = 0; c < nch; c++) {
             const int pb = c & 1, L = chunk_n(c);
+            if (c > 1 && !wait(B_DFULL + pb, (c >> 1) - 1, 111)) break;     // Cw two chunks ago has been read
             if (!wait(B_FULL + st, k, 110)) break;
-            if (c > 1 && !wait(B_CWEMPTY + pb, (c >> 1) - 1, 111)) break;
             uint8_t *ct = sm + OFF_STAGE + st * SZ_STAGE + 2 * SZ_AB + wt * 16;
+            if (L < Q) {
+                // behind the sequence but inside the tensor B and C may hold
+                // anything: zeroed before any UMMA reads this chunk
+                for (int row = r0, o = 0; row < Q; row += 16, o += 2048)
+                    if (row >= L) {
+                        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(ct + o) = z;
+                        *reinterpret_cast<uint4 *>(ct + o - SZ_AB) = z;
+                        *reinterpret_cast<uint4 *>(ct + o - SZ_AB / 2) = z;
+                    }
+                fence_async_smem();
+                arrive(B_ZERO);
+            }
             uint8_t *cw = sm + OFF_CW + pb * 3 * SZ_T + wt * 16;
             const float *wp = rev ? pw + r0 + 1 : pw + (L - 1 - r0);
             const int dw = rev ? 16 : -16;
+            // rolled, for the instruction cache
 #pragma unroll 1
             for (int row = r0; row < Q; row += 16, ct += 2048, cw += 2048, wp += dw) {
-                uint4 x = *reinterpret_cast<const uint4 *>(ct);
-                float w = 0.f;
-                if (row < L) {
-                    w = *wp * sw;
-                } else {
-                    // behind the sequence but inside the tensor: may hold
-                    // anything, and D4 multiplies it (D2's C rows are zeroed by
-                    // the score warps, which hand D2 its chunk)
-                    x = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(ct - SZ_AB) = x;
-                    *reinterpret_cast<uint4 *>(ct - SZ_AB / 2) = x;
-                }
+                const uint4 x = *reinterpret_cast<const uint4 *>(ct);
+                const float w = row < L ? *wp * sw : 0.f;
                 // cut off, not rounded: the 24 bits of w c fall apart into three
                 // bf16 exactly, by masks and byte moves alone
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
@@ -336,10 +346,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     const f32x2 v = mul2(pair(bf16_lo(xs[q]), bf16_hi(xs[q])), ww);
                     unpair(v, a, b2);
                     hs[q] = cut2(a, b2);
-                    const f32x2 r = add2(v, pair(-cut(a), -cut(b2)));
+                    const f32x2 r = fma2(pair(cut(a), cut(b2)), neg1, v);
                     unpair(r, a, b2);
                     ms[q] = cut2(a, b2);
-                    const f32x2 l = add2(r, pair(-cut(a), -cut(b2)));
+                    const f32x2 l = fma2(pair(cut(a), cut(b2)), neg1, r);
                     unpair(l, a, b2);
                     ls[q] = cut2(a, b2);
                 }
@@ -378,11 +388,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             for (int i = 0; i < 4; i++) po[i] = prow + (((2 * i + mc) ^ (mr & 7)) << 4);
             // 16 x 32 blocks wholly on the masked side are zero: written into each buffer once
             const int zhf = rev ? (q >= 2 ? 0 : 2) : (q < 2 ? 1 : 2);
-            int st = 0;
             for (int c = 0; c < nch; c++) {
-                const int pb = c & 1, L = chunk_n(c);
+                const int pb = c & 1;
                 if (!wait(B_SFULL + pb, c >> 1, 112)) break;
-                if (c > 1 && !wait(B_PEMPTY + pb, (c >> 1) - 1, 113)) break;
+                if (c > 1 && !wait(B_YFULL + pb, (c >> 1) - 1, 113)) break;    // P two chunks ago has been read
                 tc_fence_after();
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
@@ -399,22 +408,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; e++) o[e] = round2(mul2(pair(v[2 * e], v[2 * e + 1]), m[hf][e]));
-                    if (L < Q) {                        // columns behind the sequence may be anything
-#pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            const int s = 32 * hf + 8 * (e >> 1) + cq;
-                            if (s >= L) o[e] = 0u;
-                            else if (s + 1 >= L) o[e] &= 0xffffu;
-                        }
-                    }
                     stmatrix4(po[2 * hf] + pb * SZ_T, o[0], o[1], o[2], o[3]);
                     stmatrix4(po[2 * hf + 1] + pb * SZ_T, o[4], o[5], o[6], o[7]);
                 }
-                if (L < Q)                              // this warp's 16 rows of C, those behind the sequence
-                    for (int r = 16 * q + (l32 >> 3); r < 16 * q + 16; r += 4)
-                        if (r >= L)
-                            *reinterpret_cast<uint4 *>(sm + OFF_STAGE + st * SZ_STAGE + 2 * SZ_AB + r * 128 +
-                                                       (l32 & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 tc_fence_before();
                 fence_async_smem();
                 __syncwarp();
@@ -422,7 +418,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     mbar_arrive(bar(B_SEMPTY + pb));
                     mbar_arrive(bar(B_PFULL + pb));
                 }
-                if (++st == NST) st = 0;
             }
         }
     } else if (warp < W_Y) {
@@ -481,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             arrive(B_DEMPTY + pb);
             if (!SO && c + 1 < nch) {
                 // buffer (c+1) & 1 was last read by D3 of chunk c - 1
-                if (c > 0 && !wait(B_MEMPTY + (pb ^ 1), (c - 1) >> 1, 115)) break;
+                if (c > 0 && !wait(B_YFULL + (pb ^ 1), (c - 1) >> 1, 115)) break;
                 publish(pb ^ 1);
             }
         }
@@ -581,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == W_SY) {
+    if (warp == W_S) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
     }
