@@ -114,14 +114,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     while (pi + 1 < P.n && blockIdx.x >= P.first[pi + 1]) pi++;
     const MixArgs &g = P.g[pi];
     const unsigned bid = blockIdx.x - P.first[pi];
-    const int ntile = (g.dc + DC - 1) / DC, nsb = SO ? g.nseg - 1 : g.nseg;
-    const int tile = (int)(bid % ntile), seg = (int)(bid / ntile % nsb);
-    const int64_t lane = bid / ntile / nsb, b = lane / g.H, h = lane % g.H;
+    const unsigned ntile = (g.dc + DC - 1) / DC, nsb = SO ? g.nseg - 1 : g.nseg, H = (unsigned)g.H;
+    const int seg = (int)(bid / ntile % nsb), p0 = (int)(bid % ntile) * DC;
+    const unsigned lane32 = bid / ntile / nsb, b32 = lane32 / H, h32 = lane32 % H;
+    const int64_t lane = lane32, b = b32, h = h32;
     const int64_t t_beg = seg_begin(seg, g.nseg, g.seg_len, g.reverse);
     const int ntok = (int)seg_tokens(seg, g.nseg, g.seg_len, g.reverse, lane_length(g.lengths, b, g.T));
     const int nch = (ntok + Q - 1) / Q;
     const bool rev = g.reverse != 0;
-    const int p0 = tile * DC;
     auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + OFF_MISC + 4);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_MISC);
@@ -130,11 +130,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     auto chunk_t = [&](int c) { return (rev ? nch - 1 - c : c) * Q; };
     auto chunk_n = [&](int c) { return min(Q, ntok - chunk_t(c)); };
 
-    if (tid == 0) {
-        for (int i = 0; i < NST; i++) {
-            mbar_init(bar(B_FULL + i), 1);
-            mbar_init(bar(B_EMPTY + i), SO ? 5 : 6);    // D4, D2 and D3; four Cw warps
+    // a chunk's loads, by one lane
+    const int ha = (int)(h32 / (unsigned)g.ra), hb = (int)(h32 / (unsigned)g.rb), hc = (int)(h32 / (unsigned)g.rc);
+    auto load = [&](int c, int st) {
+        const int t = (int)t_beg + chunk_t(c);
+        const uint32_t s0 = sbase + OFF_STAGE + st * SZ_STAGE, fb = bar(B_FULL + st);
+        mbar_expect_tx(fb, SO ? SZ_AB + SZ_C : SZ_STAGE);
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+            if (!SO) tma_load4(s0 + x * (SZ_AB / 2), &P.ma[pi], 64 * x, ha, t, (int)b32, fb);
+            tma_load4(s0 + SZ_AB + x * (SZ_AB / 2), &P.mb[pi], 64 * x, hb, t, (int)b32, fb);
         }
+        tma_load4(s0 + 2 * SZ_AB, &P.mc[pi], p0, hc, t, (int)b32, fb);
+    };
+
+    // The first loads go out before anything else: the rest of the set-up
+    // (about 3000 cycles) passes while they are on their way.
+    if (tid == 0) {
+        for (int i = 0; i < NST; i++) mbar_init(bar(B_FULL + i), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int c = 0; c < NST && c < nch; c++) load(c, c);
+        for (int i = 0; i < NST; i++) mbar_init(bar(B_EMPTY + i), SO ? 5 : 6);   // D4, D2 and D3; four Cw warps
         for (int i = 0; i < 2; i++) {
             mbar_init(bar(B_CWFULL + i), 4);
             mbar_init(bar(B_SFULL + i), 1);
@@ -157,11 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (tid >= 128 && tid <= 128 + Q) {
-        const double lg = (double)g.log_decay[h];
-        pw[tid - 128] = decay_pow(lg, tid - 128);
-        pm1[tid - 128] = decay_pow_m1(lg, tid - 128);
-    }
+    if (tid >= 128 && tid <= 128 + Q) decay_pow_f32(g.log_decay[h], tid - 128, pw[tid - 128], pm1[tid - 128]);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -173,28 +185,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
     };
 
     if (warp == W_TMA) {
-        const int ha = (int)(h / g.ra), hb = (int)(h / g.rb), hc = (int)(h / g.rc);
-        int st = 0, k = 0;                              // stage, turn of the ring
-        for (int c = 0; c < nch; c++) {
-            if (k > 0 && !wait(B_EMPTY + st, k - 1, 101)) break;
+        auto prefetch = [&](int c) {                    // a chunk on its way to L2
             const int t = (int)t_beg + chunk_t(c);
-            const uint32_t s0 = sbase + OFF_STAGE + st * SZ_STAGE, fb = bar(B_FULL + st);
+            for (int x = 0; x < g.da; x += 64) {
+                if (!SO) tma_prefetch4(&P.ma[pi], x, ha, t, (int)b32);
+                tma_prefetch4(&P.mb[pi], x, hb, t, (int)b32);
+            }
+            tma_prefetch4(&P.mc[pi], p0, hc, t, (int)b32);
+        };
+        if (elect_one())
+            for (int c = NST; c < NST + PFD && c < nch; c++) prefetch(c);
+        __syncwarp();
+        int st = 0, k = 1;                              // stage, turn of the ring
+        for (int c = NST; c < nch; c++) {
+            if (!wait(B_EMPTY + st, k - 1, 101)) break;
             if (elect_one()) {
-                mbar_expect_tx(fb, SO ? SZ_AB + SZ_C : SZ_STAGE);
-                for (int x = 0; x < 2; x++) {
-                    if (!SO) tma_load4(s0 + x * (SZ_AB / 2), &P.ma[pi], 64 * x, ha, t, (int)b, fb);
-                    tma_load4(s0 + SZ_AB + x * (SZ_AB / 2), &P.mb[pi], 64 * x, hb, t, (int)b, fb);
-                }
-                tma_load4(s0 + 2 * SZ_AB, &P.mc[pi], p0, hc, t, (int)b, fb);
-                // the chunk that this stage takes next, on its way to L2
-                if (c + PFD < nch) {
-                    const int tp = (int)t_beg + chunk_t(c + PFD);
-                    for (int x = 0; x < g.da; x += 64) {
-                        if (!SO) tma_prefetch4(&P.ma[pi], x, ha, tp, (int)b);
-                        tma_prefetch4(&P.mb[pi], x, hb, tp, (int)b);
-                    }
-                    tma_prefetch4(&P.mc[pi], p0, hc, tp, (int)b);
-                }
+                load(c, st);
+                if (c + PFD < nch) prefetch(c + PFD);
             }
             __syncwarp();
             if (++st == NST) st = 0, k++;
@@ -330,8 +337,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             uint8_t *cw = sm + OFF_CW + pb * 3 * SZ_T + wt * 16;
             const float *wp = rev ? pw + r0 + 1 : pw + (L - 1 - r0);
             const int dw = rev ? 16 : -16;
-            // rolled, for the instruction cache
-#pragma unroll 1
+            // two rows at a time: one leaves its latencies bare, four push the
+            // other roles' code out of the instruction cache
+#pragma unroll 2
             for (int row = r0; row < Q; row += 16, ct += 2048, cw += 2048, wp += dw) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(ct);
                 const float w = row < L ? *wp * sw : 0.f;
@@ -428,23 +436,43 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         float *slots = g.ws + (size_t)lane * (g.nseg - 1) * elems;
         const bool mine = n < g.da;
         f32x2 M[DC / 2];
+        // fp32 states go to and from global memory by way of this warp's 32 rows
+        // of the M buffers, as fp32 rows of 256 bytes (16-byte pieces XOR row):
+        // a thread's own row is a scattered access, two rows a warp are not
+        uint8_t *stg = sm + OFF_M + q * 8192;
+        auto piece = [&](int row, int k) { return reinterpret_cast<float4 *>(stg + row * 256 + ((k ^ (row & 7)) << 4)); };
+        const int wr = l32 >> 4, wk = l32 & 15;         // row of two, 16-byte piece
+        const bool in = p0 + 4 * wk < g.dc;             // dc is a multiple of 8
         {
             const float *src = (SO || (seg == 0 && !g.m0)) ? nullptr
                                : (seg == 0 ? g.m0 + lane * elems : slots + (size_t)(seg - 1) * elems);
-            const bool tr = seg == 0 && g.m_trans;
 #pragma unroll
             for (int p = 0; p < DC / 2; p++) M[p] = 0ull;
-            if (src && mine) {
+            if (src && seg == 0 && g.m_trans) {
+                if (mine) {
 #pragma unroll
-                for (int p = 0; p < DC; p += 2)         // dc is a multiple of 8
-                    if (p0 + p < g.dc) {
-                        if (tr) {
+                    for (int p = 0; p < DC; p += 2)
+                        if (p0 + p < g.dc)
                             M[p / 2] = pair(src[(size_t)(p0 + p) * g.da + n], src[(size_t)(p0 + p + 1) * g.da + n]);
-                        } else {
-                            const float2 v = *reinterpret_cast<const float2 *>(src + (size_t)n * g.dc + p0 + p);
-                            M[p / 2] = pair(v.x, v.y);
-                        }
-                    }
+                }
+            } else if (src) {
+#pragma unroll 4
+                for (int r = wr; r < 32; r += 2) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (in && 32 * q + r < g.da)
+                        v = *reinterpret_cast<const float4 *>(src + (size_t)(32 * q + r) * g.dc + p0 + 4 * wk);
+                    *piece(r, wk) = v;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < DC / 4; k++) {
+                    const float4 v = *piece(l32, k);
+                    M[2 * k] = pair(v.x, v.y);
+                    M[2 * k + 1] = pair(v.z, v.w);
+                }
+                // the other warps' rows are in the buffers that publish() writes:
+                // meet here (every state warp takes this branch together)
+                asm volatile("bar.sync 1, 128;" ::: "memory");
             }
         }
         auto publish = [&](int buf) {                   // the rounded copy that D3 reads
@@ -482,20 +510,33 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         }
         float *dst = SO ? slots + (size_t)seg * elems
                         : (seg == g.nseg - 1 && g.m_out ? g.m_out + lane * elems : nullptr);
-        if (dst && mine && !*abort_flag) {
-            const bool tr = !SO && g.m_trans;
+        bool out = dst && !*abort_flag;
+        // the last chunk's D3 still reads the buffers
+        if (out && !SO && !g.m_trans && nch > 0) out = wait(B_YFULL + ((nch - 1) & 1), (nch - 1) >> 1, 121);
+        if (out && !SO && g.m_trans) {
+            if (mine) {
 #pragma unroll
-            for (int p = 0; p < DC; p += 2)
-                if (p0 + p < g.dc) {
-                    float a, b2;
-                    unpair(M[p / 2], a, b2);
-                    if (tr) {
+                for (int p = 0; p < DC; p += 2)
+                    if (p0 + p < g.dc) {
+                        float a, b2;
+                        unpair(M[p / 2], a, b2);
                         dst[(size_t)(p0 + p) * g.da + n] = a;
                         dst[(size_t)(p0 + p + 1) * g.da + n] = b2;
-                    } else {
-                        *reinterpret_cast<float2 *>(dst + (size_t)n * g.dc + p0 + p) = make_float2(a, b2);
                     }
-                }
+            }
+        } else if (out) {
+#pragma unroll
+            for (int k = 0; k < DC / 4; k++) {
+                float4 v;
+                unpair(M[2 * k], v.x, v.y);
+                unpair(M[2 * k + 1], v.z, v.w);
+                *piece(l32, k) = v;
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int r = wr; r < 32; r += 2)
+                if (in && 32 * q + r < g.da)
+                    *reinterpret_cast<float4 *>(dst + (size_t)(32 * q + r) * g.dc + p0 + 4 * wk) = *piece(r, wk);
         }
     } else if (!SO && g.y) {
         // ---- the answers

@@ -76,6 +76,17 @@ __device__ __forceinline__ float decay_pow_m1(double lg, int64_t n) {
     return n == 0 ? 0.f : (float)expm1(lg * (double)n);
 }
 
+// The same from fp32 arithmetic for n <= 64, within a few roundings: the
+// product's own rounding is put back in (its derivative is the power itself).
+// (A double exp is 2 KB of code that every CTA of a short kernel waits for.)
+__device__ __forceinline__ void decay_pow_f32(float lg, int n, float &p, float &pm1) {
+    const float x = lg * (float)n;
+    const float e = isfinite(x) ? fmaf(lg, (float)n, -x) : 0.f;
+    const float m = expm1f(x);
+    pm1 = n == 0 ? 0.f : fmaf(m + 1.f, e, m);
+    p = n == 0 ? 1.f : expf(x) * (1.f + e);
+}
+
 // segment plan (nseg, seg_len) and launch of the fp32 kernel: any sizes
 // within the limits
 void mix_simt_plan(MixArgs &a);
