@@ -20,8 +20,8 @@
 // bf16 pieces, hi + mid + lo = w c exactly, summed by the tensor cores.
 //
 // One CTA owns one lane, one tile of 64 columns of c and one segment of the
-// time axis, and walks its chunks.  20 warps: 0 TMA, 1-3 UMMA issue (D1; D4; D3 and D2),
-// 4-7 Cw, 8-11 scores, 12-15 state, 16-19 outputs.  Three issuing warps, not
+// time axis, and walks its chunks.  24 warps: 0 TMA, 1-3 UMMA issue (D1; D4; D3 and D2),
+// 4-7 Cw, 8-11 scores, 12-19 state, 20-23 outputs.  Three issuing warps, not
 // one: a section of waits, fence, issue and commit takes a warp 400 to 700
 // cycles, four of them in a row more than anything else in a chunk.  The hand-overs are buffered
 // in TMEM or shared memory, so the roles work on different chunks;
@@ -42,7 +42,7 @@ namespace mixtc {
 using namespace ptx;
 
 constexpr int Q = 64, DC = 64, DA = 128;               // chunk, columns of a tile, widest a and b rows
-constexpr int W_TMA = 0, W_S = 1, W_D = 2, W_Y23 = 3, W_CW = 4, W_SC = 8, W_ST = 12, W_Y = 16, NWARPS = 20;
+constexpr int W_TMA = 0, W_S = 1, W_D = 2, W_Y23 = 3, W_CW = 4, W_SC = 8, W_ST = 12, W_Y = 20, NWARPS = 24;
 constexpr int THREADS = NWARPS * 32;
 
 // ---- shared memory (bytes from a 1024-aligned base), all tiles 128B-swizzled
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             mbar_init(bar(B_SEMPTY + i), 4);
             mbar_init(bar(B_PFULL + i), 4);
             mbar_init(bar(B_DFULL + i), 1);
-            mbar_init(bar(B_DEMPTY + i), 4);
-            mbar_init(bar(B_MFULL + i), 4);
+            mbar_init(bar(B_DEMPTY + i), 8);
+            mbar_init(bar(B_MFULL + i), 8);
             mbar_init(bar(B_YFULL + i), 1);
             mbar_init(bar(B_YEMPTY + i), 4);
         }
@@ -429,57 +429,57 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             }
         }
     } else if (warp < W_Y) {
-        // ---- the state: this thread's row, the tile's 64 columns, fp32
-        const int q = warp & 3, n = 32 * q + l32;
-        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + COL_D;
+        // ---- the state: this thread's row, 32 of the tile's columns, fp32
+        const int q = warp & 3, n = 32 * q + l32, ch = (warp - W_ST) >> 2, c0 = 32 * ch;
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + COL_D + c0;
         const size_t elems = (size_t)g.da * g.dc;
         float *slots = g.ws + (size_t)lane * (g.nseg - 1) * elems;
         const bool mine = n < g.da;
-        f32x2 M[DC / 2];
+        f32x2 M[16];
         // fp32 states go to and from global memory by way of this warp's 32 rows
-        // of the M buffers, as fp32 rows of 256 bytes (16-byte pieces XOR row):
-        // a thread's own row is a scattered access, two rows a warp are not
-        uint8_t *stg = sm + OFF_M + q * 8192;
-        auto piece = [&](int row, int k) { return reinterpret_cast<float4 *>(stg + row * 256 + ((k ^ (row & 7)) << 4)); };
-        const int wr = l32 >> 4, wk = l32 & 15;         // row of two, 16-byte piece
-        const bool in = p0 + 4 * wk < g.dc;             // dc is a multiple of 8
+        // of the M buffers, as fp32 rows of 128 bytes (16-byte pieces XOR row):
+        // a thread's own row is a scattered access, four rows a warp are not
+        uint8_t *stg = sm + OFF_M + (q * 2 + ch) * 4096;
+        auto piece = [&](int row, int k) { return reinterpret_cast<float4 *>(stg + row * 128 + ((k ^ (row & 7)) << 4)); };
+        const int wr = l32 >> 3, wk = l32 & 7;          // row of four, 16-byte piece
+        const bool in = p0 + c0 + 4 * wk < g.dc;        // dc is a multiple of 8
         {
             const float *src = (SO || (seg == 0 && !g.m0)) ? nullptr
                                : (seg == 0 ? g.m0 + lane * elems : slots + (size_t)(seg - 1) * elems);
 #pragma unroll
-            for (int p = 0; p < DC / 2; p++) M[p] = 0ull;
+            for (int p = 0; p < 16; p++) M[p] = 0ull;
             if (src && seg == 0 && g.m_trans) {
                 if (mine) {
 #pragma unroll
-                    for (int p = 0; p < DC; p += 2)
-                        if (p0 + p < g.dc)
-                            M[p / 2] = pair(src[(size_t)(p0 + p) * g.da + n], src[(size_t)(p0 + p + 1) * g.da + n]);
+                    for (int p = 0; p < 32; p += 2)
+                        if (p0 + c0 + p < g.dc)
+                            M[p / 2] = pair(src[(size_t)(p0 + c0 + p) * g.da + n], src[(size_t)(p0 + c0 + p + 1) * g.da + n]);
                 }
             } else if (src) {
 #pragma unroll 4
-                for (int r = wr; r < 32; r += 2) {
+                for (int r = wr; r < 32; r += 4) {
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (in && 32 * q + r < g.da)
-                        v = *reinterpret_cast<const float4 *>(src + (size_t)(32 * q + r) * g.dc + p0 + 4 * wk);
+                        v = *reinterpret_cast<const float4 *>(src + (size_t)(32 * q + r) * g.dc + p0 + c0 + 4 * wk);
                     *piece(r, wk) = v;
                 }
                 __syncwarp();
 #pragma unroll
-                for (int k = 0; k < DC / 4; k++) {
+                for (int k = 0; k < 8; k++) {
                     const float4 v = *piece(l32, k);
                     M[2 * k] = pair(v.x, v.y);
                     M[2 * k + 1] = pair(v.z, v.w);
                 }
                 // the other warps' rows are in the buffers that publish() writes:
                 // meet here (every state warp takes this branch together)
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                asm volatile("bar.sync 1, 256;" ::: "memory");
             }
         }
         auto publish = [&](int buf) {                   // the rounded copy that D3 reads
             uint8_t *mt = sm + OFF_M + buf * SZ_M + n * 128;
 #pragma unroll
-            for (int k = 0; k < 8; k++)
-                *reinterpret_cast<uint4 *>(mt + ((k ^ (n & 7)) << 4)) =
+            for (int k = 0; k < 4; k++)
+                *reinterpret_cast<uint4 *>(mt + (((4 * ch + k) ^ (n & 7)) << 4)) =
                     make_uint4(round2(M[4 * k]), round2(M[4 * k + 1]), round2(M[4 * k + 2]), round2(M[4 * k + 3]));
             fence_async_smem();
             arrive(B_MFULL + buf);
@@ -491,15 +491,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             const f32x2 dm1 = pair(d1, d1);
             if (!wait(B_DFULL + pb, c >> 1, 114)) break;
             tc_fence_after();
+            float d[32];
+            tmem_ld16(tl + pb * 64, d);
+            tmem_ld16(tl + pb * 64 + 16, d + 16);
+            tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < DC / 16; k++) {
-                float d[16];
-                tmem_ld16(tl + pb * 64 + 16 * k, d);
-                tmem_wait_ld();
-#pragma unroll
-                for (int u = 0; u < 8; u++)
-                    M[8 * k + u] = add2(fma2(M[8 * k + u], dm1, M[8 * k + u]), pair(d[2 * u], d[2 * u + 1]));
-            }
+            for (int u = 0; u < 16; u++) M[u] = add2(fma2(M[u], dm1, M[u]), pair(d[2 * u], d[2 * u + 1]));
             tc_fence_before();
             arrive(B_DEMPTY + pb);
             if (!SO && c + 1 < nch) {
@@ -516,17 +513,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         if (out && !SO && g.m_trans) {
             if (mine) {
 #pragma unroll
-                for (int p = 0; p < DC; p += 2)
-                    if (p0 + p < g.dc) {
+                for (int p = 0; p < 32; p += 2)
+                    if (p0 + c0 + p < g.dc) {
                         float a, b2;
                         unpair(M[p / 2], a, b2);
-                        dst[(size_t)(p0 + p) * g.da + n] = a;
-                        dst[(size_t)(p0 + p + 1) * g.da + n] = b2;
+                        dst[(size_t)(p0 + c0 + p) * g.da + n] = a;
+                        dst[(size_t)(p0 + c0 + p + 1) * g.da + n] = b2;
                     }
             }
         } else if (out) {
 #pragma unroll
-            for (int k = 0; k < DC / 4; k++) {
+            for (int k = 0; k < 8; k++) {
                 float4 v;
                 unpair(M[2 * k], v.x, v.y);
                 unpair(M[2 * k + 1], v.z, v.w);
@@ -534,9 +531,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             }
             __syncwarp();
 #pragma unroll 4
-            for (int r = wr; r < 32; r += 2)
+            for (int r = wr; r < 32; r += 4)
                 if (in && 32 * q + r < g.da)
-                    *reinterpret_cast<float4 *>(dst + (size_t)(32 * q + r) * g.dc + p0 + 4 * wk) = *piece(r, wk);
+                    *reinterpret_cast<float4 *>(dst + (size_t)(32 * q + r) * g.dc + p0 + c0 + 4 * wk) = *piece(r, wk);
         }
     } else if (!SO && g.y) {
         // ---- the answers
