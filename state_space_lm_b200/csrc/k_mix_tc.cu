@@ -8,7 +8,7 @@
 //   P_ji = scale_p g^|j-i| D1_ji  (i <= j; walking backwards i >= j), bf16
 //   D2 = P C                own chunk's answer         M=64  N=64 K=64
 //   D3 = A M                the past's answer          M=64  N=64 K=da
-//   D4 = B^T Cw             own chunk's state          M=128 N=64 K=64 (three times)
+//   D4 = B^T Cw             own chunk's state          M=128 N=3x64 K=64
 //   y_j = D2_j + scale_i g^(j+1) D3_j                  (backwards g^(L-1-j))
 //   M  <- M + M (g^L - 1) + D4,  Cw_i = scale_w g^(L-1-i) c_i   (backwards g^(i+1))
 // The decay is a constant of the lane, so every weight is a table of the 65
@@ -17,7 +17,7 @@
 // Roundings: A, B, C enter as they are.  P and the copy of M that D3 reads
 // are rounded to bf16, one rounding for each term of y, as y itself has.  The
 // state is carried in fp32 and is an output in fp32, so Cw goes in as three
-// bf16 pieces, hi + mid + lo = w c exactly, summed by the tensor cores.
+// bf16 pieces, hi + mid + lo = w c exactly, side by side in D4's columns.
 //
 // One CTA owns one lane, one tile of 64 columns of c and one segment of the
 // time axis, and walks its chunks.  24 warps: 0 TMA, 1-3 UMMA issue (D1; D4; D3 and D2),
@@ -63,17 +63,18 @@ enum {
     B_FULL = 0,                    // NST: a stage has arrived
     B_EMPTY = B_FULL + NST,        // NST: its readers are done
     // 2 of each from here on.  "Full" of an accumulator also says that the
-    // operands it was made from may be overwritten: Cw (D), P and M (Y)
+    // operands it was made from may be overwritten: P and M (Y)
     B_CWFULL = B_EMPTY + NST,      // Cw in shared memory
-    B_SFULL = B_CWFULL + 2,        // scores in TMEM
-    B_SEMPTY = B_SFULL + 2,
-    B_PFULL = B_SEMPTY + 2,        // masked scores in shared memory
-    B_DFULL = B_PFULL + 2,         // a chunk's own state in TMEM
-    B_DEMPTY = B_DFULL + 2,
-    B_MFULL = B_DEMPTY + 2,        // the entering state in shared memory
+    B_CWEMPTY = B_CWFULL + 2,
+    B_PFULL = B_CWEMPTY + 2,       // masked scores in shared memory
+    B_MFULL = B_PFULL + 2,         // the entering state in shared memory
     B_YFULL = B_MFULL + 2,         // both parts of the answer in TMEM
     B_YEMPTY = B_YFULL + 2,
-    B_ZERO = B_YEMPTY + 2,         // 1: rows behind the sequence are zeroed in B and C
+    B_SFULL = B_YEMPTY + 2,        // 1 of each from here on.  Scores in TMEM
+    B_SEMPTY,
+    B_DFULL,                       // a chunk's own state in TMEM
+    B_DEMPTY,
+    B_ZERO,                        // rows behind the sequence are zeroed in B and C
     B_DRAIN = B_ZERO + 1,          // 3: every UMMA of an issuing warp is done
     NBAR = B_DRAIN + 3
 };
@@ -81,7 +82,7 @@ constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 
-constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_Y2 = 128, COL_Y3 = 256, COL_D = 384;   // each two tiles of 64
+constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_D = 64, COL_Y2 = 256, COL_Y3 = 384;   // 64, 3 x 64, 2 x 64, 2 x 64
 
 constexpr int MAXP = 3;
 struct Batch {
@@ -153,15 +154,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         for (int i = 0; i < NST; i++) mbar_init(bar(B_EMPTY + i), SO ? 5 : 6);   // D4, D2 and D3; four Cw warps
         for (int i = 0; i < 2; i++) {
             mbar_init(bar(B_CWFULL + i), 4);
-            mbar_init(bar(B_SFULL + i), 1);
-            mbar_init(bar(B_SEMPTY + i), 4);
+            mbar_init(bar(B_CWEMPTY + i), 1);
             mbar_init(bar(B_PFULL + i), 4);
-            mbar_init(bar(B_DFULL + i), 1);
-            mbar_init(bar(B_DEMPTY + i), 8);
             mbar_init(bar(B_MFULL + i), 8);
             mbar_init(bar(B_YFULL + i), 1);
             mbar_init(bar(B_YEMPTY + i), 4);
         }
+        mbar_init(bar(B_SFULL), 1);
+        mbar_init(bar(B_SEMPTY), 4);
+        mbar_init(bar(B_DFULL), 1);
+        mbar_init(bar(B_DEMPTY), 8);
         mbar_init(bar(B_ZERO), 4);
         for (int i = 0; i < 3; i++) mbar_init(bar(B_DRAIN + i), 1);
         *abort_flag = 0;
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 }
         }
     } else if (warp < W_CW) {
-        constexpr uint32_t id_kk = idesc(64, 64, 0, 0), id_kmn = idesc(64, 64, 0, 1), id_st = idesc(128, 64, 1, 1);
+        constexpr uint32_t id_kk = idesc(64, 64, 0, 0), id_kmn = idesc(64, 64, 0, 1), id_st = idesc(128, 192, 1, 1);
         // Descriptor steps (16-byte units): a K-step of 16 is 32 bytes of a
         // K-major row (the second 64 columns lie half a tile further), and two
         // groups of 8 rows (MN) of an MN-major one.  The issue loops are
@@ -225,26 +227,25 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         // further, the code of all roles leaves the instruction cache.
         constexpr uint64_t MN = 2048 >> 4;
         const uint64_t d_k0 = sdesc(sbase + OFF_STAGE, 16, 1024), d_mn0 = sdesc(sbase + OFF_STAGE, Q * 128, 1024);
-        const uint64_t d_cw0 = sdesc(sbase + OFF_CW, Q * 128, 1024), d_p0 = sdesc(sbase + OFF_P, 16, 1024);
+        const uint64_t d_cw0 = sdesc(sbase + OFF_CW, SZ_T, 1024), d_p0 = sdesc(sbase + OFF_P, 16, 1024);
         const uint64_t d_m0 = sdesc(sbase + OFF_M, DA * 128, 1024);
         constexpr uint64_t ST = SZ_STAGE >> 4, AB = SZ_AB >> 4, TT = SZ_T >> 4, MM = SZ_M >> 4;
         int st = 0, k3 = 0;                             // stage, turn of the ring
         if (warp == W_S && !SO) {
             for (int c = 0; c < nch; c++) {
-                const int pb = c & 1;
                 if (!wait(B_FULL + st, k3, 102)) break;
-                if (c > 1 && !wait(B_SEMPTY + pb, (c >> 1) - 1, 103)) break;
+                if (c > 0 && !wait(B_SEMPTY, c - 1, 103)) break;
                 if (chunk_n(c) < Q && !wait(B_ZERO, 0, 120)) break;     // one chunk of the walk at most
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t da = d_k0 + st * ST, db = da + AB;
-                    const uint32_t d = tmem + COL_S + pb * 64;
+                    const uint32_t d = tmem + COL_S;
 #pragma unroll 1
                     for (int x = 0; x < 2; x++)
 #pragma unroll
                         for (int kk = 0; kk < 4; kk++)
                             umma(d, da + x * (AB / 2) + kk * 2, db + x * (AB / 2) + kk * 2, id_kk, x + kk > 0);
-                    umma_commit(bar(B_SFULL + pb));
+                    umma_commit(bar(B_SFULL));
                 }
                 __syncwarp();
                 if (++st == NST) st = 0, k3++;
@@ -253,18 +254,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             for (int c = 0; c < nch; c++) {
                 const int pb = c & 1, k2 = c >> 1;
                 if (!wait(B_FULL + st, k3, 105)) break;
-                if (c > 1 && !wait(B_DEMPTY + pb, k2 - 1, 106)) break;
+                if (c > 0 && !wait(B_DEMPTY, c - 1, 106)) break;
                 if (!wait(B_CWFULL + pb, k2, 104)) break;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t db = d_mn0 + st * ST + AB, dw = d_cw0 + pb * (3 * TT);
-                    const uint32_t d = tmem + COL_D + pb * 64;
-#pragma unroll 1
-                    for (int x = 0; x < 3; x++)         // the pieces lo, mid, hi
+                    // the three pieces side by side in N = 192: B is read once,
+                    // not three times (shared-memory bandwidth is the limit of
+                    // the loop), and the state warps add them up
 #pragma unroll
-                        for (int kk = 0; kk < 4; kk++)
-                            umma(d, db + kk * MN, dw + x * TT + kk * MN, id_st, x + kk > 0);
-                    umma_commit(bar(B_DFULL + pb));
+                    for (int kk = 0; kk < 4; kk++) umma(tmem + COL_D, db + kk * MN, dw + kk * MN, id_st, kk > 0);
+                    umma_commit(bar(B_DFULL));
+                    umma_commit(bar(B_CWEMPTY + pb));
                     umma_commit(bar(B_EMPTY + st));
                 }
                 __syncwarp();
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         int st = 0, k = 0;
         for (int c = 0; c < nch; c++) {
             const int pb = c & 1, L = chunk_n(c);
-            if (c > 1 && !wait(B_DFULL + pb, (c >> 1) - 1, 111)) break;     // Cw two chunks ago has been read
+            if (c > 1 && !wait(B_CWEMPTY + pb, (c >> 1) - 1, 111)) break;
             if (!wait(B_FULL + st, k, 110)) break;
             uint8_t *ct = sm + OFF_STAGE + st * SZ_STAGE + 2 * SZ_AB + wt * 16;
             if (L < Q) {
@@ -361,9 +362,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     unpair(l, a, b2);
                     ls[q] = cut2(a, b2);
                 }
-                *reinterpret_cast<uint4 *>(cw) = make_uint4(ls[0], ls[1], ls[2], ls[3]);
+                *reinterpret_cast<uint4 *>(cw) = make_uint4(hs[0], hs[1], hs[2], hs[3]);
                 *reinterpret_cast<uint4 *>(cw + SZ_T) = make_uint4(ms[0], ms[1], ms[2], ms[3]);
-                *reinterpret_cast<uint4 *>(cw + 2 * SZ_T) = make_uint4(hs[0], hs[1], hs[2], hs[3]);
+                *reinterpret_cast<uint4 *>(cw + 2 * SZ_T) = make_uint4(ls[0], ls[1], ls[2], ls[3]);
             }
             fence_async_smem();
             __syncwarp();
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             const int zhf = rev ? (q >= 2 ? 0 : 2) : (q < 2 ? 1 : 2);
             for (int c = 0; c < nch; c++) {
                 const int pb = c & 1;
-                if (!wait(B_SFULL + pb, c >> 1, 112)) break;
+                if (!wait(B_SFULL, c, 112)) break;
                 if (c > 1 && !wait(B_YFULL + pb, (c >> 1) - 1, 113)) break;    // P two chunks ago has been read
                 tc_fence_after();
 #pragma unroll
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     }
                     float v[16];
                     uint32_t o[8];
-                    tmem_ld16x256b_x4(tl + pb * 64 + 32 * hf, v);
+                    tmem_ld16x256b_x4(tl + 32 * hf, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; e++) o[e] = round2(mul2(pair(v[2 * e], v[2 * e + 1]), m[hf][e]));
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 fence_async_smem();
                 __syncwarp();
                 if (l32 == 0) {
-                    mbar_arrive(bar(B_SEMPTY + pb));
+                    mbar_arrive(bar(B_SEMPTY));
                     mbar_arrive(bar(B_PFULL + pb));
                 }
             }
@@ -489,16 +490,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             const int pb = c & 1;
             const float d1 = pm1[chunk_n(c)];
             const f32x2 dm1 = pair(d1, d1);
-            if (!wait(B_DFULL + pb, c >> 1, 114)) break;
+            if (!wait(B_DFULL, c, 114)) break;
             tc_fence_after();
-            float d[32];
-            tmem_ld16(tl + pb * 64, d);
-            tmem_ld16(tl + pb * 64 + 16, d + 16);
-            tmem_wait_ld();
 #pragma unroll
-            for (int u = 0; u < 16; u++) M[u] = add2(fma2(M[u], dm1, M[u]), pair(d[2 * u], d[2 * u + 1]));
+            for (int k = 0; k < 4; k++) {
+                float hi[8], mid[8], lo[8];
+                tmem_ld8(tl + 8 * k, hi);
+                tmem_ld8(tl + 64 + 8 * k, mid);
+                tmem_ld8(tl + 128 + 8 * k, lo);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    const f32x2 s = add2(add2(pair(lo[2 * u], lo[2 * u + 1]), pair(mid[2 * u], mid[2 * u + 1])),
+                                         pair(hi[2 * u], hi[2 * u + 1]));
+                    M[4 * k + u] = add2(fma2(M[4 * k + u], dm1, M[4 * k + u]), s);
+                }
+            }
             tc_fence_before();
-            arrive(B_DEMPTY + pb);
+            arrive(B_DEMPTY);
             if (!SO && c + 1 < nch) {
                 // buffer (c+1) & 1 was last read by D3 of chunk c - 1
                 if (c > 0 && !wait(B_YFULL + (pb ^ 1), (c - 1) >> 1, 115)) break;
