@@ -46,6 +46,39 @@ __device__ __forceinline__ float act_only(float u, int act) {
     return f;
 }
 
+// VEC consecutive elements as they lie in memory: loaded early, unpacked late.
+template <typename T, int VEC>
+struct Raw {
+    T v[VEC];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < VEC; i++) v[i] = p[i];
+    }
+    __device__ __forceinline__ void get(float *o) const {
+#pragma unroll
+        for (int i = 0; i < VEC; i++) o[i] = ldf(v, i);
+    }
+};
+template <>
+struct Raw<float, 4> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void get(float *o) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float *o) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            o[2 * i] = __uint_as_float(w[i] << 16);
+            o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
 // VEC consecutive elements
 template <int VEC>
 __device__ __forceinline__ void ldv(const float *p, float *v) {
@@ -145,6 +178,7 @@ __device__ __forceinline__ RowGeo row_geo(const GnArgs &a, int tw) {
     return r;
 }
 
+// The next row's vectors are on their way while a row is worked on.
 template <typename T, int VEC, int NV, int ACT, bool GATE>
 __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
     constexpr bool FAST = sizeof(T) == 2;
@@ -153,6 +187,21 @@ __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
     const int D = (int)(a.C / a.G), nvec = D / VEC;
     const float invD = 1.f / (float)D;
     float w[NV][VEC], b[NV][VEC];
+    Raw<T, VEC> nx[NV], nz[NV];
+    const T *xp = static_cast<const T *>(a.x) + r.g * D, *zp = static_cast<const T *>(a.gate) + r.g * D;
+    auto fetch = [&](int64_t row) {
+        if (r.on && row < a.Bt) {
+#pragma unroll
+            for (int m = 0; m < NV; m++) {
+                const int v = m * tw + r.lane_in;
+                if (v < nvec) {
+                    nx[m].load(xp + row * a.C + v * VEC);
+                    if (GATE) nz[m].load(zp + row * a.C + v * VEC);
+                }
+            }
+        }
+    };
+    fetch(r.slot);
 #pragma unroll
     for (int m = 0; m < NV; m++)
 #pragma unroll
@@ -167,21 +216,23 @@ __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
         const int64_t row = r.slot + k * r.nslots;
         const bool on = r.on && row < a.Bt;
         const int64_t base = row * a.C + r.g * D;
-        float x[NV][VEC], z[NV][VEC];
+        float x[NV][VEC];
+        Raw<T, VEC> z[NV];
         float s = 0.f;
 #pragma unroll
         for (int m = 0; m < NV; m++) {
-            const int v = m * tw + r.lane_in;
-            const bool in = on && v < nvec;
-#pragma unroll
-            for (int e = 0; e < VEC; e++) x[m][e] = 0.f;
+            const bool in = on && m * tw + r.lane_in < nvec;
             if (in) {
-                ldv<VEC>(static_cast<const T *>(a.x) + base + v * VEC, x[m]);
-                if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + base + v * VEC, z[m]);
+                nx[m].get(x[m]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; e++) x[m][e] = 0.f;
             }
+            z[m] = nz[m];
 #pragma unroll
             for (int e = 0; e < VEC; e++) s += x[m][e];
         }
+        fetch(row + r.nslots);
         const float mean = row_sum(s, tw, sh) * invD;
         float q = 0.f;
 #pragma unroll
@@ -202,11 +253,12 @@ __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
         for (int m = 0; m < NV; m++) {
             const int v = m * tw + r.lane_in;
             if (on && v < nvec) {
-                float y[VEC];
+                float y[VEC], zf[VEC];
+                if (GATE) z[m].get(zf);
 #pragma unroll
                 for (int e = 0; e < VEC; e++) {
                     const float u = fmaf(x[m][e] * rstd, w[m][e], b[m][e]);
-                    y[e] = GATE ? u * act_only<ACT, FAST>(z[m][e], a.act) : act_only<ACT, FAST>(u, a.act);
+                    y[e] = GATE ? u * act_only<ACT, FAST>(zf[e], a.act) : act_only<ACT, FAST>(u, a.act);
                 }
                 stv<VEC>(static_cast<T *>(a.y) + base + v * VEC, y);
             }
@@ -214,17 +266,39 @@ __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
     }
 }
 
-// The gradients of w and b are summed in registers over a team's rows and
-// left as one row of partial sums per slot, (slot, 2, C); k_gn_reduce adds the
-// slots up in their order.
+// The gradients of w and b are summed in registers over a team's rows, then
+// over the block's teams of the same group (in their order, in shared memory),
+// and leave as one row of partial sums per block or slot, (row, 2, C);
+// k_gn_reduce adds those up in their order.
 template <typename T, int VEC, int NV, int ACT, bool GATE>
-__global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw) {
+__global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw, int fold) {
     constexpr bool FAST = sizeof(T) == 2;
+    extern __shared__ float part[];                       // 2 C sums, when the block folds its slots
     __shared__ float2 sh[RT / 32];
     const RowGeo r = row_geo(a, tw);
     const int D = (int)(a.C / a.G), nvec = D / VEC;
     const float invD = 1.f / (float)D;
     float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    Raw<T, VEC> nx[NV], ny[NV], nz[NV];
+    float nmean = 0.f, nrstd = 0.f;
+    const T *xp = static_cast<const T *>(a.x) + r.g * D, *zp = static_cast<const T *>(a.gate) + r.g * D;
+    const T *yp = static_cast<const T *>(a.dy) + r.g * D;
+    auto fetch = [&](int64_t row) {
+        if (r.on && row < a.Bt) {
+            nmean = a.mean_in[row * a.G + r.g];
+            nrstd = a.rstd_in[row * a.G + r.g];
+#pragma unroll
+            for (int m = 0; m < NV; m++) {
+                const int v = m * tw + r.lane_in;
+                if (v < nvec) {
+                    nx[m].load(xp + row * a.C + v * VEC);
+                    ny[m].load(yp + row * a.C + v * VEC);
+                    if (GATE) nz[m].load(zp + row * a.C + v * VEC);
+                }
+            }
+        }
+    };
+    fetch(r.slot);
 #pragma unroll
     for (int m = 0; m < NV; m++)
 #pragma unroll
@@ -240,46 +314,49 @@ __global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw) {
         const int64_t row = r.slot + k * r.nslots;
         const bool on = r.on && row < a.Bt;
         const int64_t base = row * a.C + r.g * D;
-        const float mean = on ? a.mean_in[row * a.G + r.g] : 0.f;
-        const float rstd = on ? a.rstd_in[row * a.G + r.g] : 0.f;
+        const float mean = nmean, rstd = nrstd;
         float xh[NV][VEC], dn[NV][VEC];
+        Raw<T, VEC> z[NV];
         float m1 = 0.f, m2 = 0.f;
 #pragma unroll
         for (int m = 0; m < NV; m++) {
-            const int v = m * tw + r.lane_in;
-            const bool in = on && v < nvec;
-            float dy[VEC], z[VEC], dz[VEC];
+            if (on && m * tw + r.lane_in < nvec) {
+                nx[m].get(xh[m]);
+                ny[m].get(dn[m]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < VEC; e++) xh[m][e] = dy[e] = z[e] = 0.f;
-            if (in) {
-                ldv<VEC>(static_cast<const T *>(a.x) + base + v * VEC, xh[m]);
-                ldv<VEC>(static_cast<const T *>(a.dy) + base + v * VEC, dy);
-                if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + base + v * VEC, z);
+                for (int e = 0; e < VEC; e++) xh[m][e] = dn[m][e] = 0.f;
             }
+            z[m] = nz[m];
+        }
+        fetch(row + r.nslots);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                float f, df, du;
-                if (in) {
+        for (int m = 0; m < NV; m++) {
+            const int v = m * tw + r.lane_in;
+            if (on && v < nvec) {
+                float zf[VEC], dz[VEC];
+                if (GATE) z[m].get(zf);
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    float f, df, du;
                     xh[m][e] = (xh[m][e] - mean) * rstd;
                     const float u = fmaf(xh[m][e], w[m][e], b[m][e]);
                     if (GATE) {
-                        act_both<ACT, FAST>(z[e], a.act, f, df);
-                        du = dy[e] * f;
-                        dz[e] = dy[e] * u * df;
+                        act_both<ACT, FAST>(zf[e], a.act, f, df);
+                        du = dn[m][e] * f;
+                        dz[e] = dn[m][e] * u * df;
                     } else {
                         act_both<ACT, FAST>(u, a.act, f, df);
-                        du = dy[e] * df;
+                        du = dn[m][e] * df;
                     }
                     dw[m][e] = fmaf(du, xh[m][e], dw[m][e]);
                     db[m][e] += du;
-                } else {
-                    du = 0.f;
+                    dn[m][e] = du * w[m][e];
+                    m1 += dn[m][e];
+                    m2 = fmaf(dn[m][e], xh[m][e], m2);
                 }
-                dn[m][e] = du * w[m][e];
-                m1 += dn[m][e];
-                m2 = fmaf(dn[m][e], xh[m][e], m2);
+                if (GATE && a.dgate) stv<VEC>(static_cast<T *>(a.dgate) + base + v * VEC, dz);
             }
-            if (GATE && in && a.dgate) stv<VEC>(static_cast<T *>(a.dgate) + base + v * VEC, dz);
         }
         const float2 mm = row_sum2(make_float2(m1, m2), tw, sh);
         m1 = mm.x * invD;
@@ -297,27 +374,35 @@ __global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw) {
             }
         }
     }
-    if (r.on) {
-        float *pw = a.ws + (size_t)r.slot * 2 * a.C + r.g * D, *pb = pw + a.C;
+    if (!(a.dw || a.db)) return;
+    // fold: every block holds the same number of whole sets of G teams
+    const int mine = fold ? (int)(r.slot % fold) : 0;
+    for (int f = 0; f < (fold ? fold : 1); f++) {
+        if (r.on && mine == f) {
+            float *pw = fold ? part + r.g * D : a.ws + (size_t)r.slot * 2 * a.C + r.g * D, *pb = pw + a.C;
 #pragma unroll
-        for (int m = 0; m < NV; m++)
+            for (int m = 0; m < NV; m++)
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const int c = (m * tw + r.lane_in) * VEC + e;
-                if (c < D) {
-                    pw[c] = dw[m][e];
-                    pb[c] = db[m][e];
+                for (int e = 0; e < VEC; e++) {
+                    const int c = (m * tw + r.lane_in) * VEC + e;
+                    if (c < D) {
+                        pw[c] = (f ? pw[c] : 0.f) + dw[m][e];
+                        pb[c] = (f ? pb[c] : 0.f) + db[m][e];
+                    }
                 }
-            }
+        }
+        if (fold) __syncthreads();
     }
+    if (fold)
+        for (int c = threadIdx.x; c < 2 * a.C; c += RT) a.ws[(size_t)blockIdx.x * 2 * a.C + c] = part[c];
 }
 
 // dw, db from partial sums (n rows of 2 C): one block per 32 channels, its 8
 // warps take rows in turn, then add up in a fixed order.
-__global__ void __launch_bounds__(256) k_gn_reduce(const float *part, int64_t n, int64_t C, float *dw, float *db) {
+__device__ __forceinline__ void reduce_rows(const float *part, int64_t n, int64_t C, float *dw, float *db, int64_t blk) {
     __shared__ float sh[8][32];
     const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-    const int64_t c = (int64_t)blockIdx.x * 32 + l;       // of 2 C
+    const int64_t c = blk * 32 + l;                       // of 2 C
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
     if (c < 2 * C) {
         int64_t r = w;
@@ -343,107 +428,141 @@ __global__ void __launch_bounds__(256) k_gn_reduce(const float *part, int64_t n,
     }
 }
 
+__global__ void __launch_bounds__(256) k_gn_reduce(const float *part, int64_t n, int64_t C, float *dw, float *db) {
+    reduce_rows(part, n, C, dw, db, blockIdx.x);
+}
+
 // ------------------------------------------------------------------- seq plan
 // The L tokens of a sequence are cut into chunks of `rows` tokens, one CTA
-// each, all channels of a token read as one contiguous piece.
+// each, all channels of a token read as one contiguous piece: a thread owns a
+// vector of channels (every SQT-th where there are more), and where there are
+// fewer vectors than threads, `np` threads share a vector's tokens.
 constexpr int SQT = 256;
 
-// Per (sequence, chunk, group): count is known, (mean, M2) are written.  A
-// thread sums a vector of channels over the chunk's tokens as differences
-// from its first value (so a large mean cancels nothing), the vectors of a
-// group are merged by the pairwise update of means.
+struct SeqGeo {
+    int64_t bi, ch, base;
+    int64_t t0, t1;
+    int nvec, dvec, np, ph, v0;
+};
+__device__ __forceinline__ SeqGeo seq_geo(const GnArgs &a, int vec, int64_t rows, int64_t nch) {
+    SeqGeo s;
+    s.bi = blockIdx.x / nch;
+    s.ch = blockIdx.x % nch;
+    s.base = s.bi * a.L * a.C;
+    s.t0 = s.ch * rows;
+    s.t1 = s.t0 + rows < a.L ? s.t0 + rows : a.L;
+    s.nvec = (int)(a.C / vec);
+    s.dvec = (int)(a.C / a.G) / vec;
+    s.np = s.nvec < SQT ? SQT / s.nvec : 1;
+    s.ph = s.np > 1 ? (int)threadIdx.x / s.nvec : 0;
+    s.v0 = s.np > 1 ? (s.ph < s.np ? (int)threadIdx.x % s.nvec : s.nvec) : (int)threadIdx.x;   // nvec: idle
+    return s;
+}
+
+// Per (sequence, chunk, group): the count is known, (mean, M2) are written.  A
+// thread sums a vector of channels over its tokens as differences from its
+// first value (so a large mean cancels nothing); the threads' (n, mean, M2)
+// of a group are merged by the pairwise update of means.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int64_t rows, int64_t nch) {
-    extern __shared__ float2 vstat[];                     // C / VEC pairs (mean, M2)
-    const int64_t bi = blockIdx.x / nch, ch = blockIdx.x % nch;
-    const int64_t t0 = ch * rows, t1 = t0 + rows < a.L ? t0 + rows : a.L;
-    const int nvec = (int)(a.C / VEC), D = (int)(a.C / a.G), dvec = D / VEC;
-    const T *x = static_cast<const T *>(a.x) + bi * a.L * a.C;
-    const float n1 = (float)((t1 - t0) * VEC);
-    for (int v = threadIdx.x; v < nvec; v += SQT) {
-        float k0[VEC], s[VEC], q[VEC];
-        ldv<VEC>(x + t0 * a.C + (int64_t)v * VEC, k0);
-        const float K = k0[0];
+    extern __shared__ float2 vstat[];                     // (np, nvec) pairs (mean, M2)
+    const SeqGeo s = seq_geo(a, VEC, rows, nch);
+    const T *x = static_cast<const T *>(a.x) + s.base;
+    for (int v = s.v0; v < s.nvec; v += s.np > 1 ? s.nvec : SQT) {
+        const int64_t n = (s.t1 - s.t0 - s.ph + s.np - 1) / s.np;      // this thread's tokens
+        float K = 0.f, S = 0.f, Q = 0.f;
+        if (n > 0) {
+            const T *p = x + (s.t0 + s.ph) * a.C + (int64_t)v * VEC;
+            const int64_t step = s.np * a.C;
+            float sum[VEC], q[VEC];
+            K = ldf(p, 0);
 #pragma unroll
-        for (int e = 0; e < VEC; e++) s[e] = q[e] = 0.f;
+            for (int e = 0; e < VEC; e++) sum[e] = q[e] = 0.f;
 #pragma unroll 4
-        for (int64_t t = t0; t < t1; t++) {
-            float y[VEC];
-            ldv<VEC>(x + t * a.C + (int64_t)v * VEC, y);
+            for (int64_t t = 0; t < n; t++) {
+                float y[VEC];
+                ldv<VEC>(p + t * step, y);
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    const float d = y[e] - K;
+                    sum[e] += d;
+                    q[e] = fmaf(d, d, q[e]);
+                }
+            }
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                const float d = y[e] - K;
-                s[e] += d;
-                q[e] = fmaf(d, d, q[e]);
+                S += sum[e];
+                Q += q[e];
             }
+            const float m = S / (float)(n * VEC);
+            K += m;
+            Q = fmaxf(Q - S * m, 0.f);
         }
-        float S = 0.f, Q = 0.f;
-#pragma unroll
-        for (int e = 0; e < VEC; e++) {
-            S += s[e];
-            Q += q[e];
-        }
-        const float m = S / n1;
-        vstat[v] = make_float2(K + m, fmaxf(Q - S * m, 0.f));
+        vstat[s.ph * s.nvec + v] = make_float2(K, Q);
     }
     __syncthreads();
-    // one warp per group: mean of the vectors' means, then their spread
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-    float2 *out = reinterpret_cast<float2 *>(a.ws) + (bi * nch + ch) * a.G;
+    // one warp per group: the mean of the threads' means, then their spread
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31, nt = (int)(s.t1 - s.t0);
+    const float tot = (float)nt * (float)s.dvec;          // tokens times vectors
+    float2 *out = reinterpret_cast<float2 *>(a.ws) + (s.bi * nch + s.ch) * a.G;
     for (int g = w; g < a.G; g += SQT / 32) {
         float m = 0.f;
-        for (int v = l; v < dvec; v += 32) m += vstat[g * dvec + v].x;
-        m = team_sum(m, 32) / (float)dvec;
+        for (int ph = 0; ph < s.np; ph++) {
+            const float n = (float)((nt - ph + s.np - 1) / s.np);
+            for (int v = l; v < s.dvec; v += 32) m = fmaf(vstat[ph * s.nvec + g * s.dvec + v].x, n, m);
+        }
+        m = team_sum(m, 32) / tot;
         float M2 = 0.f;
-        for (int v = l; v < dvec; v += 32) {
-            const float2 p = vstat[g * dvec + v];
-            const float d = p.x - m;
-            M2 += fmaf(n1 * d, d, p.y);
+        for (int ph = 0; ph < s.np; ph++) {
+            const float n = (float)((nt - ph + s.np - 1) / s.np * VEC);
+            for (int v = l; v < s.dvec; v += 32) {
+                const float2 p = vstat[ph * s.nvec + g * s.dvec + v];
+                const float d = p.x - m;
+                M2 += fmaf(n * d, d, p.y);
+            }
         }
         M2 = team_sum(M2, 32);
         if (l == 0) out[g] = make_float2(m, M2);
     }
 }
 
-// (mean, rstd) of every (sequence, group) from its chunks: a warp each.
-__global__ void __launch_bounds__(256) k_gn_seq_final(GnArgs a, int64_t rows, int64_t nch, float2 *stat) {
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int l = threadIdx.x & 31;
-    if (i >= a.Bt * a.G) return;
-    const int64_t bi = i / a.G, g = i % a.G;
-    const float2 *p = reinterpret_cast<const float2 *>(a.ws) + bi * nch * a.G + g;
-    const float D = (float)(a.C / a.G), n = (float)a.L * D;
-    float m = 0.f;
-    for (int64_t c = l; c < nch; c += 32) {
-        const float nc = (float)((c + 1) * rows < a.L ? rows : a.L - c * rows) * D;
-        m = fmaf(p[c * a.G].x, nc / n, m);
-    }
-    m = team_sum(m, 32);
-    float M2 = 0.f;
-    for (int64_t c = l; c < nch; c += 32) {
-        const float nc = (float)((c + 1) * rows < a.L ? rows : a.L - c * rows) * D;
-        const float2 s = p[c * a.G];
-        const float d = s.x - m;
-        M2 += fmaf(nc * d, d, s.y);
-    }
-    M2 = team_sum(M2, 32);
-    if (l == 0) {
-        const float rstd = rsqrtf(M2 / n + a.eps);
-        stat[i] = make_float2(m, rstd);
-        if (a.mean) a.mean[i] = m;
-        if (a.rstd) a.rstd[i] = rstd;
-    }
-}
-
+// Every CTA merges its sequence's chunks itself (a few KB from L2), a warp a
+// group, before it applies them: less than a launch of its own costs.
 template <typename T, int VEC, int ACT, bool GATE>
-__global__ void __launch_bounds__(SQT) k_gn_seq_apply(GnArgs a, int64_t rows, int64_t nch, const float2 *stat) {
+__global__ void __launch_bounds__(SQT) k_gn_seq_apply(GnArgs a, int64_t rows, int64_t nch) {
     constexpr bool FAST = sizeof(T) == 2;
-    const int64_t bi = blockIdx.x / nch, ch = blockIdx.x % nch;
-    const int64_t t0 = ch * rows, t1 = t0 + rows < a.L ? t0 + rows : a.L;
-    const int nvec = (int)(a.C / VEC), dvec = (int)(a.C / a.G) / VEC;
-    const int64_t base = bi * a.L * a.C;
-    for (int v = threadIdx.x; v < nvec; v += SQT) {
-        const float2 st = stat[bi * a.G + v / dvec];
+    extern __shared__ float2 gstat[];                     // G pairs (mean, rstd)
+    const SeqGeo s = seq_geo(a, VEC, rows, nch);
+    {
+        const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+        const float D = (float)(a.C / a.G), n = (float)a.L * D, inv = 1.f / n;
+        for (int g = w; g < a.G; g += SQT / 32) {
+            const float2 *p = reinterpret_cast<const float2 *>(a.ws) + s.bi * nch * a.G + g;
+            float m = 0.f;
+            for (int64_t c = l; c < nch; c += 32) {
+                const float nc = (float)((c + 1) * rows < a.L ? rows : a.L - c * rows) * D;
+                m = fmaf(p[c * a.G].x, nc * inv, m);
+            }
+            m = team_sum(m, 32);
+            float M2 = 0.f;
+            for (int64_t c = l; c < nch; c += 32) {
+                const float nc = (float)((c + 1) * rows < a.L ? rows : a.L - c * rows) * D;
+                const float2 q = p[c * a.G];
+                const float d = q.x - m;
+                M2 += fmaf(nc * d, d, q.y);
+            }
+            M2 = team_sum(M2, 32);
+            if (l == 0) {
+                const float rstd = rsqrtf(M2 / n + a.eps);
+                gstat[g] = make_float2(m, rstd);
+                if (s.ch == 0 && a.mean) a.mean[s.bi * a.G + g] = m;
+                if (s.ch == 0 && a.rstd) a.rstd[s.bi * a.G + g] = rstd;
+            }
+        }
+        __syncthreads();
+    }
+    for (int v = s.v0; v < s.nvec; v += s.np > 1 ? s.nvec : SQT) {
+        const float2 st = gstat[v / s.dvec];
         float w[VEC], b[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; e++) {
@@ -451,8 +570,8 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_apply(GnArgs a, int64_t rows, in
             b[e] = a.b ? a.b[v * VEC + e] : 0.f;
         }
 #pragma unroll 4
-        for (int64_t t = t0; t < t1; t++) {
-            const int64_t o = base + t * a.C + (int64_t)v * VEC;
+        for (int64_t t = s.t0 + s.ph; t < s.t1; t += s.np) {
+            const int64_t o = s.base + t * a.C + (int64_t)v * VEC;
             float x[VEC], z[VEC];
             ldv<VEC>(static_cast<const T *>(a.x) + o, x);
             if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + o, z);
@@ -487,24 +606,23 @@ __device__ __forceinline__ float gn_du(float x, float dy, float z, float2 st, fl
 template <typename T, int VEC, int ACT, bool GATE>
 __global__ void __launch_bounds__(SQT) k_gn_seq_bsums(GnArgs a, int64_t rows, int64_t nch) {
     constexpr bool FAST = sizeof(T) == 2;
-    const int64_t bi = blockIdx.x / nch, ch = blockIdx.x % nch;
-    const int64_t t0 = ch * rows, t1 = t0 + rows < a.L ? t0 + rows : a.L;
-    const int nvec = (int)(a.C / VEC), dvec = (int)(a.C / a.G) / VEC;
-    const int64_t base = bi * a.L * a.C;
+    extern __shared__ float psum[];                       // (np - 1, 2, C): the other phases' sums
+    const SeqGeo s = seq_geo(a, VEC, rows, nch);
     float *out = a.ws + (size_t)blockIdx.x * 2 * a.C;
-    for (int v = threadIdx.x; v < nvec; v += SQT) {
-        const int64_t gi = bi * a.G + v / dvec;
+    float s1[VEC], s2[VEC];
+    for (int v = s.v0; v < s.nvec; v += s.np > 1 ? s.nvec : SQT) {
+        const int64_t gi = s.bi * a.G + v / s.dvec;
         const float2 st = make_float2(a.mean_in[gi], a.rstd_in[gi]);
-        float w[VEC], b[VEC], s1[VEC], s2[VEC];
+        float w[VEC], b[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; e++) {
             w[e] = a.w ? a.w[v * VEC + e] : 1.f;
             b[e] = a.b ? a.b[v * VEC + e] : 0.f;
             s1[e] = s2[e] = 0.f;
         }
-#pragma unroll 2
-        for (int64_t t = t0; t < t1; t++) {
-            const int64_t o = base + t * a.C + (int64_t)v * VEC;
+#pragma unroll 4
+        for (int64_t t = s.t0 + s.ph; t < s.t1; t += s.np) {
+            const int64_t o = s.base + t * a.C + (int64_t)v * VEC;
             float x[VEC], dy[VEC], z[VEC], dz[VEC];
             ldv<VEC>(static_cast<const T *>(a.x) + o, x);
             ldv<VEC>(static_cast<const T *>(a.dy) + o, dy);
@@ -518,62 +636,93 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_bsums(GnArgs a, int64_t rows, in
             }
             if (GATE && a.dgate) stv<VEC>(static_cast<T *>(a.dgate) + o, dz);
         }
+        float *to = s.ph > 0 ? psum + (size_t)(s.ph - 1) * 2 * a.C : out;
+        if (s.np == 1 || s.ph > 0) {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) {
-            out[v * VEC + e] = s1[e];
-            out[a.C + v * VEC + e] = s2[e];
+            for (int e = 0; e < VEC; e++) {
+                to[v * VEC + e] = s1[e];
+                to[a.C + v * VEC + e] = s2[e];
+            }
+        }
+    }
+    if (s.np > 1) {                                       // one vector a thread: the first phase adds the others'
+        __syncthreads();
+        if (s.ph == 0) {
+            const int v = s.v0;
+            for (int ph = 1; ph < s.np; ph++) {
+                const float *q = psum + (size_t)(ph - 1) * 2 * a.C;
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    s1[e] += q[v * VEC + e];
+                    s2[e] += q[a.C + v * VEC + e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                out[v * VEC + e] = s1[e];
+                out[a.C + v * VEC + e] = s2[e];
+            }
         }
     }
 }
 
-// Per sequence: the chunks' sums added up into (sequence, 2, C), 32 channels a
-// block, eight warps over the chunks.
-__global__ void __launch_bounds__(256) k_gn_seq_fold(const float *part, int64_t nch, int64_t C, int cb, float *sums) {
-    __shared__ float sh[8][32];
+// Per (sequence, group): the chunks' sums added up into (sequence, 2, C), and
+// from them mean(dn xh) and mean(dn).  One block a (sequence, group): warps
+// over chunks, lanes over the group's channels.
+__global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, int64_t nch, float *sums, float2 *mom) {
+    __shared__ float sh[2][8][32];
+    __shared__ float red[2];
     const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-    const int64_t bi = blockIdx.x / cb, c = (int64_t)(blockIdx.x % cb) * 32 + l;
-    float s = 0.f;
-    if (c < 2 * C)
-        for (int64_t k = w; k < nch; k += 8) s += part[(bi * nch + k) * 2 * C + c];
-    sh[w][l] = s;
-    __syncthreads();
-    if (w == 0 && c < 2 * C) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) t += sh[i][l];
-        sums[bi * 2 * C + c] = t;
-    }
-}
-
-// Per (sequence, group): mean(dn xh) and mean(dn) from the channels' sums.
-__global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, const float *sums, float2 *mom) {
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int l = threadIdx.x & 31;
-    if (i >= a.Bt * a.G) return;
-    const int64_t bi = i / a.G, g = i % a.G;
+    const int64_t bi = blockIdx.x / a.G, g = blockIdx.x % a.G;
     const int D = (int)(a.C / a.G);
-    const float *p = sums + bi * 2 * a.C + g * D;
     float m2 = 0.f, m1 = 0.f;
-    for (int c = l; c < D; c += 32) {
-        const float w = a.w ? a.w[g * D + c] : 1.f;
-        m2 = fmaf(p[c], w, m2);
-        m1 = fmaf(p[a.C + c], w, m1);
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        const int c = c0 + l;
+        float s1 = 0.f, s2 = 0.f;
+        if (c < D) {
+            const float *p = a.ws + (size_t)bi * nch * 2 * a.C + g * D + c;
+#pragma unroll 4
+            for (int64_t k = w; k < nch; k += 8) {
+                s1 += p[k * 2 * a.C];
+                s2 += p[k * 2 * a.C + a.C];
+            }
+        }
+        __syncthreads();
+        sh[0][w][l] = s1;
+        sh[1][w][l] = s2;
+        __syncthreads();
+        if (w < 2) {
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; i++) t += sh[w][i][l];
+            if (c < D) {
+                sums[bi * 2 * a.C + w * a.C + g * D + c] = t;
+                const float wt = a.w ? a.w[g * D + c] : 1.f;
+                if (w == 0) m2 = fmaf(t, wt, m2);
+                else m1 = fmaf(t, wt, m1);
+            }
+        }
     }
-    const float n = (float)a.L * (float)D;
-    m2 = team_sum(m2, 32) / n;
-    m1 = team_sum(m1, 32) / n;
-    if (l == 0) mom[i] = make_float2(m2, m1);
+    if (w < 2) {
+        const float t = team_sum(w == 0 ? m2 : m1, 32);
+        if (l == 0) red[w] = t / ((float)a.L * (float)D);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) mom[bi * a.G + g] = make_float2(red[0], red[1]);
 }
 
+// dx; the last blocks add up dw and db instead
 template <typename T, int VEC, int ACT, bool GATE>
-__global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int64_t rows, int64_t nch, const float2 *mom) {
+__global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int64_t rows, int64_t nch, const float *sums,
+                                                   const float2 *mom, unsigned dx_blocks) {
     constexpr bool FAST = sizeof(T) == 2;
-    const int64_t bi = blockIdx.x / nch, ch = blockIdx.x % nch;
-    const int64_t t0 = ch * rows, t1 = t0 + rows < a.L ? t0 + rows : a.L;
-    const int nvec = (int)(a.C / VEC), dvec = (int)(a.C / a.G) / VEC;
-    const int64_t base = bi * a.L * a.C;
-    for (int v = threadIdx.x; v < nvec; v += SQT) {
-        const int64_t gi = bi * a.G + v / dvec;
+    if (blockIdx.x >= dx_blocks) {
+        reduce_rows(sums, a.Bt, a.C, a.dw, a.db, blockIdx.x - dx_blocks);
+        return;
+    }
+    const SeqGeo s = seq_geo(a, VEC, rows, nch);
+    for (int v = s.v0; v < s.nvec; v += s.np > 1 ? s.nvec : SQT) {
+        const int64_t gi = s.bi * a.G + v / s.dvec;
         const float2 st = make_float2(a.mean_in[gi], a.rstd_in[gi]), mm = mom[gi];
         float w[VEC], b[VEC];
 #pragma unroll
@@ -581,9 +730,9 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int64_t rows, int64
             w[e] = a.w ? a.w[v * VEC + e] : 1.f;
             b[e] = a.b ? a.b[v * VEC + e] : 0.f;
         }
-#pragma unroll 2
-        for (int64_t t = t0; t < t1; t++) {
-            const int64_t o = base + t * a.C + (int64_t)v * VEC;
+#pragma unroll 4
+        for (int64_t t = s.t0 + s.ph; t < s.t1; t += s.np) {
+            const int64_t o = s.base + t * a.C + (int64_t)v * VEC;
             float x[VEC], dy[VEC], z[VEC];
             ldv<VEC>(static_cast<const T *>(a.x) + o, x);
             ldv<VEC>(static_cast<const T *>(a.dy) + o, dy);
@@ -604,7 +753,9 @@ struct Plan {
     bool row;
     int vec, nv, tw;           // row plan: vector width, vectors a lane, lanes a team
     unsigned blocks;
-    int64_t nslots;            // row plan: rows in flight (rows of partial sums)
+    int64_t nslots;            // row plan: rows in flight
+    int fold;                  // row plan: slots of a block that the backward adds up in shared memory (0: one at most)
+    int64_t parts;             // row plan: rows of partial sums
     int64_t rows, nch;         // seq plan: tokens a chunk, chunks a sequence
 };
 
@@ -637,11 +788,16 @@ Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd)
         // once a team); always enough teams for one of each group
         const int64_t teams_cta = RT / p.tw, need = ceil_div(G, teams_cta);
         int64_t blocks = ceil_div(Bt * G, teams_cta * 2);
-        const int64_t cap = 148 * (bwd ? 3 : 6);
+        const int64_t cap = 148 * (bwd ? 3 : 6);          // CTAs that fit: 80 and 40 registers a thread
         if (blocks > cap) blocks = cap;
         if (blocks < need) blocks = need;
         p.blocks = (unsigned)blocks;
         p.nslots = blocks * teams_cta / G;
+        p.parts = p.nslots;
+        if (teams_cta % G == 0 && teams_cta > G) {
+            p.fold = (int)(teams_cta / G);
+            p.parts = blocks;
+        }
         return p;
     }
     // chunks of tokens: about four CTAs per SM, at least 4 tokens each
@@ -677,7 +833,8 @@ Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd)
 template <typename T, int VEC, int NV>
 cudaError_t row_launch(const GnArgs &a, const Plan &p, bool bwd, cudaStream_t s) {
     if (bwd) {
-        GN_ACTS(k_gn_row_bwd, T, VEC, GN_COMMA_NV(NV), <<<p.blocks, RT, 0, s>>>(a, p.tw))
+        const int smem = p.fold ? (int)(2 * a.C * sizeof(float)) : 0;      // C <= 4096 there
+        GN_ACTS(k_gn_row_bwd, T, VEC, GN_COMMA_NV(NV), <<<p.blocks, RT, smem, s>>>(a, p.tw, p.fold))
     } else {
         GN_ACTS(k_gn_row_fwd, T, VEC, GN_COMMA_NV(NV), <<<p.blocks, RT, 0, s>>>(a, p.tw))
     }
@@ -690,7 +847,7 @@ cudaError_t row_dispatch(const GnArgs &a, const Plan &p, bool bwd, cudaStream_t 
     if (p.vec == WIDE) {
         if (p.nv == 1) return row_launch<T, WIDE, 1>(a, p, bwd, s);
         if (p.nv == 2) return row_launch<T, WIDE, 2>(a, p, bwd, s);
-        if (WIDE == 4) {
+        if constexpr (WIDE == 4) {
             if (p.nv == 4) return row_launch<T, 4, 4>(a, p, bwd, s);
             return row_launch<T, 4, 8>(a, p, bwd, s);
         }
@@ -702,10 +859,16 @@ cudaError_t row_dispatch(const GnArgs &a, const Plan &p, bool bwd, cudaStream_t 
     return row_launch<T, 1, 8>(a, p, bwd, s);
 }
 
+// phases that share a vector's tokens (as seq_geo)
+int seq_phases(int64_t C, int vec) {
+    const int64_t nvec = C / vec;
+    return nvec < SQT ? (int)(SQT / nvec) : 1;
+}
+
 template <typename T, int VEC>
 cudaError_t seq_fwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
     const unsigned blocks = (unsigned)(a.Bt * p.nch);
-    const int smem = (int)(a.C / VEC * sizeof(float2));
+    const int smem = (int)(seq_phases(a.C, VEC) * (a.C / VEC) * sizeof(float2));
     cudaError_t e;
     if (smem > 48 * 1024 &&
         (e = cudaFuncSetAttribute(k_gn_seq_stats<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
@@ -713,11 +876,18 @@ cudaError_t seq_fwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
     k_gn_seq_stats<T, VEC><<<blocks, SQT, smem, s>>>(a, p.rows, p.nch);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    float2 *stat = reinterpret_cast<float2 *>(a.ws) + a.Bt * p.nch * a.G;
-    k_gn_seq_final<<<(unsigned)ceil_div(a.Bt * a.G, 8), 256, 0, s>>>(a, p.rows, p.nch, stat);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    GN_ACTS(k_gn_seq_apply, T, VEC, , <<<blocks, SQT, 0, s>>>(a, p.rows, p.nch, stat))
+    const int gsm = (int)(a.G * sizeof(float2));
+#define GN_APPLY_SMEM(T, V, A, Z)                                                                          \
+    if (gsm > 48 * 1024 &&                                                                                 \
+        (e = cudaFuncSetAttribute(k_gn_seq_apply<T, V, A, Z>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
+                                  gsm)) != cudaSuccess)                                                    \
+        return e;
+    if (VEC == 1) {                                       // G > 6144 only without vectors
+        if (a.gate) { GN_APPLY_SMEM(T, 1, ACT_ANY, true) }
+        else { GN_APPLY_SMEM(T, 1, ACT_ANY, false) }
+    }
+#undef GN_APPLY_SMEM
+    GN_ACTS(k_gn_seq_apply, T, VEC, , <<<blocks, SQT, gsm, s>>>(a, p.rows, p.nch))
     count_launch();
     return cudaGetLastError();
 }
@@ -725,26 +895,19 @@ cudaError_t seq_fwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
 template <typename T, int VEC>
 cudaError_t seq_bwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
     const unsigned blocks = (unsigned)(a.Bt * p.nch);
+    const int smem = (int)((seq_phases(a.C, VEC) - 1) * 2 * a.C * sizeof(float));   // below 16 KB: np C / VEC <= 256
     cudaError_t e;
-    GN_ACTS(k_gn_seq_bsums, T, VEC, , <<<blocks, SQT, 0, s>>>(a, p.rows, p.nch))
+    GN_ACTS(k_gn_seq_bsums, T, VEC, , <<<blocks, SQT, smem, s>>>(a, p.rows, p.nch))
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     float *sums = a.ws + (size_t)a.Bt * p.nch * 2 * a.C;
     float2 *mom = reinterpret_cast<float2 *>(sums + (size_t)a.Bt * 2 * a.C);
-    const unsigned cb = (unsigned)ceil_div(2 * a.C, 32);
-    k_gn_seq_fold<<<cb * (unsigned)a.Bt, 256, 0, s>>>(a.ws, p.nch, a.C, (int)cb, sums);
+    k_gn_seq_moments<<<(unsigned)(a.Bt * a.G), 256, 0, s>>>(a, p.nch, sums, mom);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (a.dw || a.db) {
-        k_gn_reduce<<<cb, 256, 0, s>>>(sums, a.Bt, a.C, a.dw, a.db);
-        count_launch();
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (!a.dx) return cudaSuccess;
-    k_gn_seq_moments<<<(unsigned)ceil_div(a.Bt * a.G, 8), 256, 0, s>>>(a, sums, mom);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    GN_ACTS(k_gn_seq_dx, T, VEC, , <<<blocks, SQT, 0, s>>>(a, p.rows, p.nch, mom))
+    const unsigned dxb = a.dx ? blocks : 0, rb = (a.dw || a.db) ? (unsigned)ceil_div(2 * a.C, 32) : 0;
+    if (dxb + rb == 0) return cudaSuccess;
+    GN_ACTS(k_gn_seq_dx, T, VEC, , <<<dxb + rb, SQT, 0, s>>>(a, p.rows, p.nch, sums, mom, dxb))
     count_launch();
     return cudaGetLastError();
 }
@@ -753,12 +916,12 @@ cudaError_t seq_bwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
 
 size_t gn_fwd_workspace_floats(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt) {
     const Plan p = plan_of(Bt, L, C, G, dt, false);
-    return p.row ? 0 : (size_t)(Bt * p.nch * G + Bt * G) * 2;
+    return p.row ? 0 : (size_t)(Bt * p.nch * G) * 2;
 }
 
 size_t gn_bwd_workspace_floats(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt) {
     const Plan p = plan_of(Bt, L, C, G, dt, true);
-    return p.row ? (size_t)p.nslots * 2 * C : (size_t)Bt * (p.nch + 1) * 2 * C + (size_t)Bt * G * 2;
+    return p.row ? (size_t)p.parts * 2 * C : (size_t)Bt * (p.nch + 1) * 2 * C + (size_t)Bt * G * 2;
 }
 
 cudaError_t launch_gn_fwd(const GnArgs &a, m3_dtype dt, cudaStream_t s) {
@@ -781,7 +944,7 @@ cudaError_t launch_gn_bwd(const GnArgs &a, m3_dtype dt, cudaStream_t s) {
         cudaError_t e =
             dt == M3_BF16 ? row_dispatch<__nv_bfloat16, 8>(a, p, true, s) : row_dispatch<float, 4>(a, p, true, s);
         if (e != cudaSuccess || !(a.dw || a.db)) return e;
-        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 256, 0, s>>>(a.ws, p.nslots, a.C, a.dw, a.db);
+        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 256, 0, s>>>(a.ws, p.parts, a.C, a.dw, a.db);
         count_launch();
         return cudaGetLastError();
     }

@@ -32,6 +32,7 @@
 // The problems of a call (three in the backward) share one launch.  Every
 // wait is bounded: past ~1 s the kernel records the site, stops issuing work,
 // drains what it has in flight and returns.
+#include <atomic>
 #include <initializer_list>
 
 #include "linattn.cuh"
@@ -706,12 +707,29 @@ void mix_tc_plan(MixArgs *g, int n) {
     }
 }
 
+// What a launch needs of its device, looked up once per device: the kernels'
+// shared-memory size set, the error word's address.
+static cudaError_t device_setup(int **err) {
+    using namespace mixtc;
+    static std::atomic<int *> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*err = known[dev].load(std::memory_order_acquire))) return cudaSuccess;
+    if ((e = cudaFuncSetAttribute(k_mix_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(k_mix_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess ||
+        (e = cudaGetSymbolAddress(reinterpret_cast<void **>(err), g_error)) != cudaSuccess)
+        return e;
+    if (dev < 64) known[dev].store(*err, std::memory_order_release);
+    return cudaSuccess;
+}
+
 cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
     using namespace mixtc;
     if (n < 1 || n > MAXP) return cudaErrorInvalidValue;
     Batch P;
     P.n = n;
-    cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&P.err), g_error);
+    cudaError_t e = device_setup(&P.err);
     if (e != cudaSuccess) return e;
     bool split = false;
     for (int i = 0; i < n; i++) {
@@ -731,8 +749,6 @@ cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
             k += (unsigned)(g[i].Bt * g[i].H * (g[i].nseg - 1) * ((g[i].dc + DC - 1) / DC));
         }
         P.first[n] = k;
-        if ((e = cudaFuncSetAttribute(k_mix_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
-            return e;
         k_mix_tc<true><<<k, THREADS, SMEM, s>>>(P);
         count_launch();
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -745,8 +761,6 @@ cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
         k += (unsigned)(g[i].Bt * g[i].H * g[i].nseg * ((g[i].dc + DC - 1) / DC));
     }
     P.first[n] = k;
-    if ((e = cudaFuncSetAttribute(k_mix_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
-        return e;
     k_mix_tc<false><<<k, THREADS, SMEM, s>>>(P);
     count_launch();
     return cudaGetLastError();

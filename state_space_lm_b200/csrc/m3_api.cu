@@ -495,30 +495,25 @@ LinPlan fwd_mix(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
     return p;
 }
 // dq = mix(dy, v, k) forwards, dk = mix(v, dy, q) and dv = mix(k, q, dy)
-// backwards: those that are wanted.
-LinPlan bwd_mixes(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype, bool dq, bool dk, bool dv) {
+// backwards.
+LinPlan bwd_mixes(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
     LinPlan p;
-    p.n = 0;
+    p.n = 3;
     const int rep = (int)(d.nheads / o.G);
     const int64_t ldd = d.nheads * d.headdim;
-    if (dq) {
-        MixArgs &m = p.m[p.n++] = mix_of(d, d.headdim, d.dstate, dtype);
-        m.lda = ldd; m.ldb = o.ldv; m.ldc = o.ldk; m.rc = rep;
-        m.m_trans = 1;
-        if (rep > 1) m.y_f32 = 1;
+    MixArgs &dq = p.m[0] = mix_of(d, d.headdim, d.dstate, dtype);
+    dq.lda = ldd; dq.ldb = o.ldv; dq.ldc = o.ldk; dq.rc = rep;
+    MixArgs &dk = p.m[1] = dq;
+    dk.lda = o.ldv; dk.ldb = ldd; dk.ldc = o.ldq;
+    dk.reverse = 1;
+    for (MixArgs *m : {&dq, &dk}) {
+        m->m_trans = 1;
+        if (rep > 1) m->y_f32 = 1;
     }
-    if (dk) {
-        MixArgs &m = p.m[p.n++] = mix_of(d, d.headdim, d.dstate, dtype);
-        m.lda = o.ldv; m.ldb = ldd; m.ldc = o.ldq; m.rc = rep;
-        m.m_trans = m.reverse = 1;
-        if (rep > 1) m.y_f32 = 1;
-    }
-    if (dv) {
-        MixArgs &m = p.m[p.n++] = mix_of(d, d.dstate, d.headdim, dtype);
-        m.lda = o.ldk; m.ldb = o.ldq; m.ldc = ldd;
-        m.ra = m.rb = rep;
-        m.reverse = 1;
-    }
+    MixArgs &dv = p.m[2] = mix_of(d, d.dstate, d.headdim, dtype);
+    dv.lda = o.ldk; dv.ldb = o.ldq; dv.ldc = ldd;
+    dv.ra = dv.rb = rep;
+    dv.reverse = 1;
     return p;
 }
 // bytes of one gradient of shared heads, per head in fp32
@@ -528,28 +523,21 @@ size_t head_bytes(const m3_linattn_dims &d, const LinGeo &o) {
 inline bool tma_aligned(const void *q, const void *k, const void *v) { return aligned16(q) && aligned16(k) && aligned16(v); }
 }  // namespace
 
-// Enough for either path (the choice depends on the bases' alignment) and for
-// any of the gradients.
+// Enough for either path (the choice depends on the bases' alignment).  The
+// backward's plan is that of all three products, whichever are wanted.
 size_t m3_linattn_workspace_bytes(int which, m3_linattn_dims d, m3_dtype dtype) {
     LinGeo o;
     if (check_dtype(dtype) != M3_OK || check_linattn_dims(d, true, o) != M3_OK) return 0;
+    if (which != M3_WS_LINATTN_FWD && which != M3_WS_LINATTN_BWD) return 0;
+    const bool bwd = which == M3_WS_LINATTN_BWD;
     size_t most = 0;
-    for (int want = which == M3_WS_LINATTN_BWD ? 1 : 7; want < 8; want++)
-        for (bool aligned : {false, true}) {
-            LinPlan p;
-            size_t heads = 0;
-            if (which == M3_WS_LINATTN_FWD) {
-                p = fwd_mix(d, o, dtype);
-            } else if (which == M3_WS_LINATTN_BWD) {
-                p = bwd_mixes(d, o, dtype, want & 1, want & 2, want & 4);
-                heads = ((want & 1) + (want >> 1 & 1)) * head_bytes(d, o);
-            } else {
-                return 0;
-            }
-            plan_mixes(p, dtype, aligned);
-            if (p.bytes + heads > most) most = p.bytes + heads;
-        }
-    return most;
+    for (bool aligned : {false, true}) {
+        LinPlan p = bwd ? bwd_mixes(d, o, dtype) : fwd_mix(d, o, dtype);
+        plan_mixes(p, dtype, aligned);
+        if (p.bytes > most) most = p.bytes;
+        if (!p.tc && aligned) break;
+    }
+    return most + (bwd ? 2 * head_bytes(d, o) : 0);
 }
 
 m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3_dtype dtype, const float *log_decay,
@@ -618,16 +606,17 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
     M3_OPT(g.dq); M3_OPT(g.dk); M3_OPT(g.dv); M3_OPT(g.ds0);
     const size_t need = m3_linattn_workspace_bytes(M3_WS_LINATTN_BWD, d, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
-    LinPlan p = bwd_mixes(d, o, dtype, g.dq, g.dk, g.dv || g.ds0);
-    if (d.batch == 0 || p.n == 0) return M3_OK;
+    const bool want[3] = {g.dq != nullptr, g.dk != nullptr, g.dv || g.ds0};
+    if (d.batch == 0 || !(want[0] || want[1] || want[2])) return M3_OK;
+    LinPlan p = bwd_mixes(d, o, dtype);
     plan_mixes(p, dtype, tma_aligned(q, k, v));
     const size_t hb = head_bytes(d, o);
     const bool shared = hb > 0;
     char *heads = static_cast<char *>(workspace) + p.bytes;
     struct { const void *in; void *out; } sums[2] = {};
-    int i = 0, ns = 0;
-    auto next = [&](const void *a, const void *b, const void *c, const float *m0, void *y) -> MixArgs & {
-        MixArgs &m = p.m[i++];
+    int ns = 0;
+    auto fill = [&](int i, const void *a, const void *b, const void *c, const float *m0, void *y) -> MixArgs & {
+        MixArgs &m = p.m[i];
         m.a = a; m.b = b; m.c = c;
         m.m0 = m0;
         m.y = y;
@@ -645,9 +634,15 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
         sums[ns++].out = out;
         return in;
     };
-    if (g.dq) next(dy, v, k, s0, summed(g.dq));
-    if (g.dk) next(v, dy, q, ds_final, summed(g.dk));
-    if (g.dv || g.ds0) next(k, q, dy, ds_final, g.dv).m_out = g.ds0;
+    if (want[0]) fill(0, dy, v, k, s0, summed(g.dq));
+    if (want[1]) fill(1, v, dy, q, ds_final, summed(g.dk));
+    if (want[2]) fill(2, k, q, dy, ds_final, g.dv).m_out = g.ds0;
+    p.n = 0;                                    // those that are wanted, with their places in the workspace
+    for (int i = 0; i < 3; i++)
+        if (want[i]) {
+            p.m[p.n] = p.m[i];
+            p.states[p.n++] = p.states[i];
+        }
     const cudaStream_t s = (cudaStream_t)stream;
     return launch_unless_injected([&]() -> cudaError_t {
         cudaError_t e = launch_mixes(p, dtype, workspace, s);

@@ -7,6 +7,7 @@ If the library has not been built, every call raises ``RuntimeError`` -- there
 is no other implementation behind these names.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -531,6 +532,9 @@ def chunked_bwd(x, dt, A, lam, theta, B, C, D, dy, chunk, W_x=None, W_y=None, no
 
 
 # ---- linear attention with a decay for each head, group norm -------------------
+# These calls are short on the device (a single token's takes a few
+# microseconds), so what only depends on the sizes is worked out once for each
+# set of sizes: the dims structure and the workspace that the library asks for.
 def _row_ptr(t):
     """Address of a tensor whose strides the caller has checked."""
     if t is None:
@@ -546,7 +550,7 @@ class _Device:
     caller's, or that device's current one."""
 
     def __init__(self, dev, stream):
-        self.guard = None if dev.type != "cuda" or dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
         self.dev, self.stream = dev, stream
 
     def __enter__(self):
@@ -560,53 +564,71 @@ class _Device:
         return False
 
 
+def _run(fn, where, args, dev, stream):
+    """fn(*args, stream) on dev."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with _Device(dev, stream) as s:
+            rc = fn(*args, s)
+    if rc != M3_OK:
+        raise M3Error(rc, where)
+
+
 def _ld(where, name, t):
     """Elements between the rows of consecutive tokens of a (Bt,[T,]heads,d)
     tensor whose rows are contiguous: a slice of a fused projection has more
     than heads * d."""
-    size, stride = t.shape, t.stride()
+    size = t.shape
     heads, d = size[-2], size[-1]
-    ok = (d <= 1 or stride[-1] == 1) and (heads <= 1 or stride[-2] == d)
-    lead = [(n, s) for n, s in zip(size[:-2], stride[:-2])]
     ld = heads * d
-    if len(lead) == 1:
-        if lead[0][0] > 1:
-            ld = lead[0][1]
+    if t.is_contiguous():
+        return ld
+    stride = t.stride()
+    ok = (d <= 1 or stride[-1] == 1) and (heads <= 1 or stride[-2] == d)
+    if len(size) == 3:
+        if size[0] > 1:
+            ld = stride[0]
     else:
-        (B, sb), (T, st) = lead
+        B, T = size[:2]
         if T > 1:
-            ld = st
-            ok = ok and (B <= 1 or sb == T * ld)
+            ld = stride[1]
+            ok = ok and (B <= 1 or stride[0] == T * ld)
         elif B > 1:
-            ld = sb
+            ld = stride[0]
     if not ok or ld < heads * d:
         raise ValueError("%s: %s has strides %s; the rows of a token have to be contiguous and the batch stride "
                          "seqlen times the token stride" % (where, name, tuple(stride)))
     return ld
 
 
-def _linattn_dims(w, q, k, v, seq):
-    if q.dim() != 3 + seq or v.dim() != 3 + seq:
+@functools.lru_cache(maxsize=512)
+def _linattn_plan(B, T, H, dv, dk, G, ldq, ldk, ldv, dtype, which):
+    """The dims structure of a set of sizes, and its workspace (which: a query
+    of m3_linattn_workspace_bytes, or None)."""
+    d = LinattnDims(B, T, H, dv, dk, G, ldq, ldk, ldv)
+    return d, (0 if which is None else int(lib().m3_linattn_workspace_bytes(which, d, dtype)))
+
+
+def _linattn_dims(w, q, k, v, seq, which=None):
+    vs, qs = v.shape, q.shape
+    if len(qs) != 3 + seq or len(vs) != 3 + seq:
         raise ValueError("%s: q, k, v are (Bt,%sheads,d)" % (w, "T," if seq else ""))
-    B, H, dv = v.shape[0], v.shape[-2], v.shape[-1]
-    T = v.shape[1] if seq else 1
-    G, dk = q.shape[-2], q.shape[-1]
-    if v.dtype not in _DTYPE:
+    dt = _DTYPE.get(v.dtype)
+    if dt is None:
         raise ValueError("%s: q, k, v must be float32 or bfloat16, got %s" % (w, v.dtype))
-    dev = v.device
-    _expect(w, dev, "q", q, B * T * G * dk, v.dtype)
-    _expect(w, dev, "k", k, B * T * G * dk, v.dtype)
-    for name, t in (("q", q), ("k", k)):
-        if t.shape[:-2] != v.shape[:-2] or t.shape[-2:] != q.shape[-2:]:
-            raise ValueError("%s: %s is %s for v %s" % (w, name, tuple(t.shape), tuple(v.shape)))
+    dev, io = v.device, v.dtype
+    if qs != k.shape or qs[:-2] != vs[:-2] or q.dtype != io or k.dtype != io or q.device != dev or k.device != dev:
+        n = q.numel() // max(1, qs[-2] * qs[-1]) * qs[-2] * qs[-1]
+        _expect(w, dev, "q", q, v.numel() // max(1, vs[-2] * vs[-1]) * qs[-2] * qs[-1], io)
+        _expect(w, dev, "k", k, n, io)
+        raise ValueError("%s: q is %s, k %s and v %s" % (w, tuple(qs), tuple(k.shape), tuple(vs)))
+    H, G = vs[-2], qs[-2]
     if G < 1 or H % G:
         raise ValueError("%s: %d heads over %d groups of q and k" % (w, H, G))
-    d = LinattnDims(B, T, H, dv, dk, G, _ld(w, "q", q), _ld(w, "k", k), _ld(w, "v", v))
-    return d, dev
-
-
-def _linattn_scale(scale, dk):
-    return float(dk) ** -0.5 if scale is None else float(scale)
+    d, need = _linattn_plan(vs[0], vs[1] if seq else 1, H, vs[-1], qs[-1], G, _ld(w, "q", q), _ld(w, "k", k),
+                            _ld(w, "v", v), dt, which)
+    return d, need, dev, dt
 
 
 def _own_workspace(need, workspace, dev):
@@ -630,7 +652,7 @@ def linattn_chunked_fwd(q, k, v, log_decay, scale=None, s0=None, lengths=None, w
     (Bt,H,dk,dv) fp32, the state for linattn_step_decode; ``out`` may hold
     both (s_final None when it is not wanted)."""
     w, f = "m3_linattn_chunked_fwd", torch.float32
-    d, dev = _linattn_dims(w, q, k, v, True)
+    d, need, dev, dt = _linattn_dims(w, q, k, v, True, M3_WS_LINATTN_FWD)
     ns = d.batch * d.nheads * d.dstate * d.headdim
     _expect(w, dev, "log_decay", log_decay, d.nheads, f)
     _expect(w, dev, "s0", s0, ns, f, required=False)
@@ -641,12 +663,11 @@ def linattn_chunked_fwd(q, k, v, log_decay, scale=None, s0=None, lengths=None, w
     y, sf = out
     _expect(w, dev, "y", y, v.numel(), v.dtype)
     _expect(w, dev, "s_final", sf, ns, f, required=False)
-    L, dt = lib(), _DTYPE[v.dtype]
-    ws, nbytes = _own_workspace(L.m3_linattn_workspace_bytes(M3_WS_LINATTN_FWD, d, dt), workspace, dev)
-    args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay), _linattn_scale(scale, d.dstate), _ptr(s0),
-            _ptr(lengths), d, _ptr(y), _ptr(sf), _ptr(ws), nbytes)
-    with _Device(dev, stream) as s:
-        _check(L.m3_linattn_chunked_fwd(*args, s), w)
+    ws, nbytes = _own_workspace(need, workspace, dev)
+    args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
+            d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(y), _ptr(sf),
+            _ptr(ws), nbytes)
+    _run(lib().m3_linattn_chunked_fwd, w, args, dev, stream)
     return y, sf
 
 
@@ -654,15 +675,14 @@ def linattn_step_decode(q_t, k_t, v_t, log_decay, s, scale=None, y_out=None, str
     """One token of every lane: q_t, k_t (Bt,G,dk), v_t (Bt,H,dv); the state s
     (Bt,H,dk,dv) fp32 is updated in place; returns y_t (Bt,H,dv)."""
     w, f = "m3_linattn_step_decode", torch.float32
-    d, dev = _linattn_dims(w, q_t, k_t, v_t, False)
+    d, _, dev, dt = _linattn_dims(w, q_t, k_t, v_t, False)
     _expect(w, dev, "log_decay", log_decay, d.nheads, f)
     _expect(w, dev, "s", s, d.batch * d.nheads * d.dstate * d.headdim, f)
     y = torch.empty(v_t.shape, dtype=v_t.dtype, device=dev) if y_out is None else y_out
     _expect(w, dev, "y_t", y, v_t.numel(), v_t.dtype)
-    args = (_row_ptr(q_t), _row_ptr(k_t), _row_ptr(v_t), _DTYPE[v_t.dtype], _ptr(log_decay),
-            _linattn_scale(scale, d.dstate), d, _ptr(s), _ptr(y))
-    with _Device(dev, stream) as st:
-        _check(lib().m3_linattn_step_decode(*args, st), w)
+    args = (_row_ptr(q_t), _row_ptr(k_t), _row_ptr(v_t), dt, _ptr(log_decay),
+            d.dstate ** -0.5 if scale is None else float(scale), d, _ptr(s), _ptr(y))
+    _run(lib().m3_linattn_step_decode, w, args, dev, stream)
     return y
 
 
@@ -673,7 +693,7 @@ def linattn_chunked_bwd(q, k, v, log_decay, dy, scale=None, s0=None, ds_final=No
     and dtype (ds0 fp32).  dy (Bt,T,H,dv) contiguous; ds_final fp32 or None for
     zero.  ``out`` may hold preallocated tensors by name."""
     w, f = "m3_linattn_chunked_bwd", torch.float32
-    d, dev = _linattn_dims(w, q, k, v, True)
+    d, need, dev, dt = _linattn_dims(w, q, k, v, True, M3_WS_LINATTN_BWD)
     ns = d.batch * d.nheads * d.dstate * d.headdim
     _expect(w, dev, "log_decay", log_decay, d.nheads, f)
     _expect(w, dev, "dy", dy, v.numel(), v.dtype)
@@ -688,20 +708,28 @@ def linattn_chunked_bwd(q, k, v, log_decay, dy, scale=None, s0=None, ds_final=No
     for n in want:
         if n not in shapes:
             raise ValueError("%s: no gradient %r" % (w, n))
-        dt = f if n == "ds0" else v.dtype
-        out[n] = pre[n] if n in pre else torch.empty(shapes[n], dtype=dt, device=dev)
-        _expect(w, dev, n, out[n], ns if n == "ds0" else {"dq": q, "dk": k, "dv": v}[n].numel(), dt)
-    L, dt = lib(), _DTYPE[v.dtype]
-    ws, nbytes = _own_workspace(L.m3_linattn_workspace_bytes(M3_WS_LINATTN_BWD, d, dt), workspace, dev)
+        io = f if n == "ds0" else v.dtype
+        if n in pre:
+            out[n] = pre[n]
+            _expect(w, dev, n, out[n], ns if n == "ds0" else {"dq": q, "dk": k, "dv": v}[n].numel(), io)
+        else:
+            out[n] = torch.empty(shapes[n], dtype=io, device=dev)
+    ws, nbytes = _own_workspace(need, workspace, dev)
     g = LinattnGrads(*[_ptr(out.get(n)) for n in names])
-    args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay), _linattn_scale(scale, d.dstate), _ptr(s0),
-            _ptr(lengths), d, _ptr(dy), _ptr(ds_final), ctypes.byref(g), _ptr(ws), nbytes)
-    with _Device(dev, stream) as s:
-        _check(L.m3_linattn_chunked_bwd(*args, s), w)
+    args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
+            d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(dy), _ptr(ds_final),
+            ctypes.byref(g), _ptr(ws), nbytes)
+    _run(lib().m3_linattn_chunked_bwd, w, args, dev, stream)
     return out
 
 
-def _norm_dims(w, x, groups, weight, bias, gate, act):
+@functools.lru_cache(maxsize=512)
+def _norm_plan(B, L, C, groups, dtype, which):
+    d = NormDims(B, L, C, groups)
+    return d, int(lib().m3_group_norm_workspace_bytes(which, d, dtype))
+
+
+def _norm_dims(w, x, groups, weight, bias, gate, act, which):
     if x.dim() < 2:
         raise ValueError("%s: x is (Bt,...,C)" % w)
     if x.dtype not in _DTYPE:
@@ -715,7 +743,8 @@ def _norm_dims(w, x, groups, weight, bias, gate, act):
     for name, t in (("weight", weight), ("bias", bias)):
         _expect(w, dev, name, t, C, torch.float32, required=False)
     _expect(w, dev, "gate", gate, x.numel(), x.dtype, required=False)
-    return NormDims(B, L, C, int(groups)), dev
+    dt = _DTYPE[x.dtype]
+    return (*_norm_plan(B, L, C, int(groups), dt, which), dev, dt)
 
 
 def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps=1e-5, workspace=None, out=None,
@@ -730,7 +759,7 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps
     and rstd (Bt, groups) fp32; ``out`` may hold the three (mean, rstd None
     when not wanted)."""
     w, f = "m3_group_norm_fwd", torch.float32
-    d, dev = _norm_dims(w, x, groups, weight, bias, gate, act)
+    d, need, dev, dt = _norm_dims(w, x, groups, weight, bias, gate, act, M3_WS_NORM_FWD)
     if out is None:
         g = max(d.ngroups, 0)
         out = (torch.empty(x.shape, dtype=x.dtype, device=dev), torch.empty((d.batch, g), dtype=f, device=dev),
@@ -739,12 +768,10 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps
     _expect(w, dev, "y", y, x.numel(), x.dtype)
     _expect(w, dev, "mean", mean, d.batch * d.ngroups, f, required=False)
     _expect(w, dev, "rstd", rstd, d.batch * d.ngroups, f, required=False)
-    L, dt = lib(), _DTYPE[x.dtype]
-    ws, nbytes = _own_workspace(L.m3_group_norm_workspace_bytes(M3_WS_NORM_FWD, d, dt), workspace, dev)
+    ws, nbytes = _own_workspace(need, workspace, dev)
     args = (_ptr(x), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], float(eps), d, _ptr(y), _ptr(mean),
             _ptr(rstd), _ptr(ws), nbytes)
-    with _Device(dev, stream) as s:
-        _check(L.m3_group_norm_fwd(*args, s), w)
+    _run(lib().m3_group_norm_fwd, w, args, dev, stream)
     return y, mean, rstd
 
 
@@ -754,7 +781,7 @@ def group_norm_bwd(x, dy, mean, rstd, groups, weight=None, bias=None, gate=None,
     gradients named in ``want`` (by default dx, dweight, dbias, and dgate with
     a gate): dx, dgate in x's shape and dtype, dweight, dbias (C) fp32."""
     w, f = "m3_group_norm_bwd", torch.float32
-    d, dev = _norm_dims(w, x, groups, weight, bias, gate, act)
+    d, need, dev, dt = _norm_dims(w, x, groups, weight, bias, gate, act, M3_WS_NORM_BWD)
     _expect(w, dev, "dy", dy, x.numel(), x.dtype)
     _expect(w, dev, "mean", mean, d.batch * d.ngroups, f)
     _expect(w, dev, "rstd", rstd, d.batch * d.ngroups, f)
@@ -767,14 +794,15 @@ def group_norm_bwd(x, dy, mean, rstd, groups, weight=None, bias=None, gate=None,
         if n not in names or (n == "dgate" and gate is None):
             raise ValueError("%s: no gradient %r" % (w, n))
         wide = n in ("dx", "dgate")
-        shape, dt = (x.shape, x.dtype) if wide else ((d.channels,), f)
-        out[n] = pre[n] if n in pre else torch.empty(shape, dtype=dt, device=dev)
-        _expect(w, dev, n, out[n], x.numel() if wide else d.channels, dt)
-    L, dt = lib(), _DTYPE[x.dtype]
-    ws, nbytes = _own_workspace(L.m3_group_norm_workspace_bytes(M3_WS_NORM_BWD, d, dt), workspace, dev)
+        shape, io = (x.shape, x.dtype) if wide else ((d.channels,), f)
+        if n in pre:
+            out[n] = pre[n]
+            _expect(w, dev, n, out[n], x.numel() if wide else d.channels, io)
+        else:
+            out[n] = torch.empty(shape, dtype=io, device=dev)
+    ws, nbytes = _own_workspace(need, workspace, dev)
     args = (_ptr(x), _ptr(dy), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], _ptr(mean), _ptr(rstd), d,
             _ptr(out.get("dx")), _ptr(out.get("dweight")), _ptr(out.get("dbias")), _ptr(out.get("dgate")), _ptr(ws),
             nbytes)
-    with _Device(dev, stream) as s:
-        _check(L.m3_group_norm_bwd(*args, s), w)
+    _run(lib().m3_group_norm_bwd, w, args, dev, stream)
     return out

@@ -141,11 +141,11 @@ def test_binding_checks_linattn():
     # what the binding takes as it is: slices of a fused projection, one token of a longer tensor
     flat = z(2, 6, 100)
     a, b, c = flat[..., :16].unflatten(-1, (2, 8)), flat[..., 16:32].unflatten(-1, (2, 8)), flat[..., 36:100].unflatten(-1, (4, 16))
-    d, _ = m3._linattn_dims("w", a, b, c, True)
+    d = m3._linattn_dims("w", a, b, c, True)[0]
     assert (d.ld_q, d.ld_k, d.ld_v) == (100, 100, 100)
-    d, _ = m3._linattn_dims("w", q[:, 3], q[:, 3], v[:, 3], False)
+    d = m3._linattn_dims("w", q[:, 3], q[:, 3], v[:, 3], False)[0]
     assert (d.ld_q, d.ld_v, d.batch, d.ngroups) == (6 * 16, 6 * 64, 2, 2)
-    d, _ = m3._linattn_dims("w", q[:1, :1], q[:1, :1], v[:1, :1], True)
+    d = m3._linattn_dims("w", q[:1, :1], q[:1, :1], v[:1, :1], True)[0]
     assert (d.ld_q, d.ld_v) == (16, 64)
 
 
