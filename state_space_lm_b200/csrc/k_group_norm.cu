@@ -82,7 +82,9 @@ struct Raw<__nv_bfloat16, 8> {
 // VEC consecutive elements
 template <int VEC>
 __device__ __forceinline__ void ldv(const float *p, float *v) {
-    if (VEC == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
+    if (VEC % 4 == 0)
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) *reinterpret_cast<float4 *>(v + i) = *reinterpret_cast<const float4 *>(p + i);
     else
 #pragma unroll
         for (int i = 0; i < VEC; i++) v[i] = p[i];
@@ -153,115 +155,75 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int tw, float2 *sh) {
 __device__ __forceinline__ float row_sum(float v, int tw, float2 *sh) { return row_sum2(make_float2(v, 0.f), tw, sh).x; }
 
 // ------------------------------------------------------------------- row plan
-// A team of tw lanes (8 for 64 bf16 channels, a whole block for 4096) owns one
-// group's channels and walks rows with w and b in registers; neighbouring
-// teams own neighbouring groups, so a row is read as one contiguous piece.
-// Bound by the bytes.  Idle lanes (past the last whole set of G teams) take
-// part in the shuffles only.
+// A team of tw lanes (8 for 64 bf16 channels, a whole block for 4096) takes one
+// group's channels of a row; neighbouring teams take neighbouring groups, so a
+// row is read as one contiguous piece.  Bound by the bytes; the index
+// arithmetic is in 32 bits (a 64-bit division costs more than the norm of
+// eight elements does).
 constexpr int RT = 256;
 
-struct RowGeo {
-    int64_t team, slot, g;
-    int lane_in;
-    bool on;
-    int64_t nslots;
-};
-__device__ __forceinline__ RowGeo row_geo(const GnArgs &a, int tw) {
-    RowGeo r;
-    const int64_t t = (int64_t)blockIdx.x * RT + threadIdx.x;
-    r.team = t / tw;
-    r.lane_in = (int)(t % tw);
-    r.nslots = (int64_t)gridDim.x * (RT / tw) / a.G;
-    r.slot = r.team / a.G;
-    r.g = r.team % a.G;
-    r.on = r.slot < r.nslots;
-    return r;
-}
-
-// The next row's vectors are on their way while a row is worked on.
+// Forward: one team, one (row, group).  Few registers and many resident warps
+// hide the latencies; teams that walk rows with the next one on its way hold
+// half the warps and were slower (16384 x 1024, gated, 16 groups: 32 to 41 us).
 template <typename T, int VEC, int NV, int ACT, bool GATE>
 __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
     constexpr bool FAST = sizeof(T) == 2;
     __shared__ float2 sh[RT / 32];
-    const RowGeo r = row_geo(a, tw);
-    const int D = (int)(a.C / a.G), nvec = D / VEC;
+    const unsigned tsh = 31 - __clz(tw), G = (unsigned)a.G;
+    const unsigned team = blockIdx.x * (RT >> tsh) + (threadIdx.x >> tsh);     // below 2^32, see plan_of
+    const int li = threadIdx.x & (tw - 1);
+    const unsigned row = team / G, g = team - row * G;
+    const bool on = row < (unsigned)a.Bt;
+    const int D = (int)((unsigned)a.C / G), nvec = D / VEC;
     const float invD = 1.f / (float)D;
-    float w[NV][VEC], b[NV][VEC];
-    Raw<T, VEC> nx[NV], nz[NV];
-    const T *xp = static_cast<const T *>(a.x) + r.g * D, *zp = static_cast<const T *>(a.gate) + r.g * D;
-    auto fetch = [&](int64_t row) {
-        if (r.on && row < a.Bt) {
+    const int64_t base = (int64_t)row * a.C + g * D;
+    float x[NV][VEC];
+    Raw<T, VEC> z[NV];
+    float s = 0.f;
 #pragma unroll
-            for (int m = 0; m < NV; m++) {
-                const int v = m * tw + r.lane_in;
-                if (v < nvec) {
-                    nx[m].load(xp + row * a.C + v * VEC);
-                    if (GATE) nz[m].load(zp + row * a.C + v * VEC);
-                }
-            }
+    for (int m = 0; m < NV; m++) {
+        const int v = m * tw + li;
+#pragma unroll
+        for (int e = 0; e < VEC; e++) x[m][e] = 0.f;
+        if (on && v < nvec) {
+            ldv<VEC>(static_cast<const T *>(a.x) + base + v * VEC, x[m]);
+            if (GATE) z[m].load(static_cast<const T *>(a.gate) + base + v * VEC);
         }
-    };
-    fetch(r.slot);
 #pragma unroll
-    for (int m = 0; m < NV; m++)
+        for (int e = 0; e < VEC; e++) s += x[m][e];
+    }
+    const float mean = row_sum(s, tw, sh) * invD;
+    float q = 0.f;
+#pragma unroll
+    for (int m = 0; m < NV; m++) {
+        const bool in = m * tw + li < nvec;
 #pragma unroll
         for (int e = 0; e < VEC; e++) {
-            const int c = (m * tw + r.lane_in) * VEC + e;
-            const bool in = r.on && c < D;
-            w[m][e] = (in && a.w) ? a.w[r.g * D + c] : 1.f;
-            b[m][e] = (in && a.b) ? a.b[r.g * D + c] : 0.f;
+            x[m][e] -= mean;
+            if (in) q = fmaf(x[m][e], x[m][e], q);
         }
-    const int64_t turns = (a.Bt + r.nslots - 1) / r.nslots;    // the same for every lane: the shuffles need them all
-    for (int64_t k = 0; k < turns; k++) {
-        const int64_t row = r.slot + k * r.nslots;
-        const bool on = r.on && row < a.Bt;
-        const int64_t base = row * a.C + r.g * D;
-        float x[NV][VEC];
-        Raw<T, VEC> z[NV];
-        float s = 0.f;
+    }
+    const float rstd = rsqrtf(fmaf(row_sum(q, tw, sh), invD, a.eps));
+    if (on && li == 0) {
+        if (a.mean) a.mean[team] = mean;
+        if (a.rstd) a.rstd[team] = rstd;
+    }
 #pragma unroll
-        for (int m = 0; m < NV; m++) {
-            const bool in = on && m * tw + r.lane_in < nvec;
-            if (in) {
-                nx[m].get(x[m]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; e++) x[m][e] = 0.f;
-            }
-            z[m] = nz[m];
-#pragma unroll
-            for (int e = 0; e < VEC; e++) s += x[m][e];
-        }
-        fetch(row + r.nslots);
-        const float mean = row_sum(s, tw, sh) * invD;
-        float q = 0.f;
-#pragma unroll
-        for (int m = 0; m < NV; m++) {
-            const bool in = on && m * tw + r.lane_in < nvec;
+    for (int m = 0; m < NV; m++) {
+        const int v = m * tw + li;
+        if (on && v < nvec) {
+            float w[VEC], b[VEC], zf[VEC];
+            if (a.w) ldv<VEC>(a.w + g * D + v * VEC, w);
+            if (a.b) ldv<VEC>(a.b + g * D + v * VEC, b);
+            if (GATE) z[m].get(zf);
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                x[m][e] -= mean;
-                if (in) q = fmaf(x[m][e], x[m][e], q);
+                float n = x[m][e] * rstd;
+                if (a.w) n *= w[e];
+                if (a.b) n += b[e];
+                x[m][e] = GATE ? n * act_only<ACT, FAST>(zf[e], a.act) : act_only<ACT, FAST>(n, a.act);
             }
-        }
-        const float rstd = rsqrtf(fmaf(row_sum(q, tw, sh), invD, a.eps));
-        if (on && r.lane_in == 0) {
-            if (a.mean) a.mean[row * a.G + r.g] = mean;
-            if (a.rstd) a.rstd[row * a.G + r.g] = rstd;
-        }
-#pragma unroll
-        for (int m = 0; m < NV; m++) {
-            const int v = m * tw + r.lane_in;
-            if (on && v < nvec) {
-                float y[VEC], zf[VEC];
-                if (GATE) z[m].get(zf);
-#pragma unroll
-                for (int e = 0; e < VEC; e++) {
-                    const float u = fmaf(x[m][e] * rstd, w[m][e], b[m][e]);
-                    y[e] = GATE ? u * act_only<ACT, FAST>(zf[e], a.act) : act_only<ACT, FAST>(u, a.act);
-                }
-                stv<VEC>(static_cast<T *>(a.y) + base + v * VEC, y);
-            }
+            stv<VEC>(static_cast<T *>(a.y) + base + v * VEC, x[m]);
         }
     }
 }
@@ -275,25 +237,34 @@ __global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw, int fold) {
     constexpr bool FAST = sizeof(T) == 2;
     extern __shared__ float part[];                       // 2 C sums, when the block folds its slots
     __shared__ float2 sh[RT / 32];
-    const RowGeo r = row_geo(a, tw);
-    const int D = (int)(a.C / a.G), nvec = D / VEC;
+    struct { int slot, g, lane_in, nslots; bool on; } r;
+    const unsigned tsh = 31 - __clz(tw), G = (unsigned)a.G;
+    {
+        const unsigned team = blockIdx.x * (RT >> tsh) + (threadIdx.x >> tsh);
+        r.lane_in = threadIdx.x & (tw - 1);
+        r.nslots = (int)(gridDim.x * (RT >> tsh) / G);
+        r.slot = (int)(team / G);
+        r.g = (int)(team % G);
+        r.on = r.slot < r.nslots;                         // the rest: lanes past the last whole set of G teams
+    }
+    const int D = (int)((unsigned)a.C / G), nvec = D / VEC, Bt = (int)a.Bt;
     const float invD = 1.f / (float)D;
     float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
     Raw<T, VEC> nx[NV], ny[NV], nz[NV];
     float nmean = 0.f, nrstd = 0.f;
     const T *xp = static_cast<const T *>(a.x) + r.g * D, *zp = static_cast<const T *>(a.gate) + r.g * D;
     const T *yp = static_cast<const T *>(a.dy) + r.g * D;
-    auto fetch = [&](int64_t row) {
-        if (r.on && row < a.Bt) {
-            nmean = a.mean_in[row * a.G + r.g];
-            nrstd = a.rstd_in[row * a.G + r.g];
+    auto fetch = [&](int row) {
+        if (r.on && row < Bt) {
+            nmean = a.mean_in[(int64_t)row * a.G + r.g];
+            nrstd = a.rstd_in[(int64_t)row * a.G + r.g];
 #pragma unroll
             for (int m = 0; m < NV; m++) {
                 const int v = m * tw + r.lane_in;
                 if (v < nvec) {
-                    nx[m].load(xp + row * a.C + v * VEC);
-                    ny[m].load(yp + row * a.C + v * VEC);
-                    if (GATE) nz[m].load(zp + row * a.C + v * VEC);
+                    nx[m].load(xp + (int64_t)row * a.C + v * VEC);
+                    ny[m].load(yp + (int64_t)row * a.C + v * VEC);
+                    if (GATE) nz[m].load(zp + (int64_t)row * a.C + v * VEC);
                 }
             }
         }
@@ -309,11 +280,11 @@ __global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw, int fold) {
             b[m][e] = (in && a.b) ? a.b[r.g * D + c] : 0.f;
             dw[m][e] = db[m][e] = 0.f;
         }
-    const int64_t turns = (a.Bt + r.nslots - 1) / r.nslots;
-    for (int64_t k = 0; k < turns; k++) {
-        const int64_t row = r.slot + k * r.nslots;
-        const bool on = r.on && row < a.Bt;
-        const int64_t base = row * a.C + r.g * D;
+    const int turns = (Bt + r.nslots - 1) / r.nslots;     // the same for every lane: the sums over a team need them all
+    for (int k = 0; k < turns; k++) {
+        const int row = r.slot + k * r.nslots;
+        const bool on = r.on && row < Bt;
+        const int64_t base = (int64_t)row * a.C + r.g * D;
         const float mean = nmean, rstd = nrstd;
         float xh[NV][VEC], dn[NV][VEC];
         Raw<T, VEC> z[NV];
@@ -397,29 +368,22 @@ __global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw, int fold) {
         for (int c = threadIdx.x; c < 2 * a.C; c += RT) a.ws[(size_t)blockIdx.x * 2 * a.C + c] = part[c];
 }
 
-// dw, db from partial sums (n rows of 2 C): one block per 32 channels, its 8
+// dw, db from partial sums (n rows of 2 C): one block per 32 channels, its
 // warps take rows in turn, then add up in a fixed order.
 __device__ __forceinline__ void reduce_rows(const float *part, int64_t n, int64_t C, float *dw, float *db, int64_t blk) {
-    __shared__ float sh[8][32];
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+    __shared__ float sh[32][32];
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31, nw = blockDim.x >> 5;
     const int64_t c = blk * 32 + l;                       // of 2 C
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    float s0 = 0.f;
     if (c < 2 * C) {
-        int64_t r = w;
-        for (; r + 24 < n; r += 32) {
-            s0 += part[r * 2 * C + c];
-            s1 += part[(r + 8) * 2 * C + c];
-            s2 += part[(r + 16) * 2 * C + c];
-            s3 += part[(r + 24) * 2 * C + c];
-        }
-        for (; r < n; r += 8) s0 += part[r * 2 * C + c];
+#pragma unroll 8
+        for (int64_t r = w; r < n; r += nw) s0 += part[r * 2 * C + c];
     }
-    sh[w][l] = (s0 + s1) + (s2 + s3);
+    sh[w][l] = s0;
     __syncthreads();
     if (w == 0 && c < 2 * C) {
         float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) t += sh[i][l];
+        for (int i = 0; i < nw; i++) t += sh[i][l];
         if (c < C) {
             if (dw) dw[c] = t;
         } else if (db) {
@@ -428,7 +392,7 @@ __device__ __forceinline__ void reduce_rows(const float *part, int64_t n, int64_
     }
 }
 
-__global__ void __launch_bounds__(256) k_gn_reduce(const float *part, int64_t n, int64_t C, float *dw, float *db) {
+__global__ void __launch_bounds__(1024) k_gn_reduce(const float *part, int64_t n, int64_t C, float *dw, float *db) {
     reduce_rows(part, n, C, dw, db, blockIdx.x);
 }
 
@@ -440,22 +404,30 @@ __global__ void __launch_bounds__(256) k_gn_reduce(const float *part, int64_t n,
 constexpr int SQT = 256;
 
 struct SeqGeo {
-    int64_t bi, ch, base;
-    int64_t t0, t1;
-    int nvec, dvec, np, ph, v0;
+    int bi, ch, t0, t1;        // sequence, chunk, its tokens
+    int64_t base;              // of the sequence's first element
+    int nvec, dvec, np, ph, v0, vstep;
 };
-__device__ __forceinline__ SeqGeo seq_geo(const GnArgs &a, int vec, int64_t rows, int64_t nch) {
+__device__ __forceinline__ SeqGeo seq_geo(const GnArgs &a, int vec, int rows, int nch) {
     SeqGeo s;
-    s.bi = blockIdx.x / nch;
-    s.ch = blockIdx.x % nch;
+    const int C = (int)a.C, L = (int)a.L;
+    s.bi = (int)(blockIdx.x / (unsigned)nch);
+    s.ch = (int)blockIdx.x - s.bi * nch;
     s.base = s.bi * a.L * a.C;
     s.t0 = s.ch * rows;
-    s.t1 = s.t0 + rows < a.L ? s.t0 + rows : a.L;
-    s.nvec = (int)(a.C / vec);
-    s.dvec = (int)(a.C / a.G) / vec;
-    s.np = s.nvec < SQT ? SQT / s.nvec : 1;
-    s.ph = s.np > 1 ? (int)threadIdx.x / s.nvec : 0;
-    s.v0 = s.np > 1 ? (s.ph < s.np ? (int)threadIdx.x % s.nvec : s.nvec) : (int)threadIdx.x;   // nvec: idle
+    s.t1 = min(s.t0 + rows, L);
+    s.nvec = C / vec;
+    s.dvec = (int)((unsigned)C / (unsigned)a.G) / vec;
+    s.np = 1;
+    s.ph = 0;
+    s.v0 = threadIdx.x;
+    s.vstep = SQT;
+    if (s.nvec < SQT) {
+        s.np = (int)(SQT / (unsigned)s.nvec);
+        s.ph = (int)(threadIdx.x / (unsigned)s.nvec);
+        s.v0 = s.ph < s.np ? (int)threadIdx.x - s.ph * s.nvec : s.nvec;    // nvec: idle
+        s.vstep = s.nvec;
+    }
     return s;
 }
 
@@ -464,24 +436,24 @@ __device__ __forceinline__ SeqGeo seq_geo(const GnArgs &a, int vec, int64_t rows
 // first value (so a large mean cancels nothing); the threads' (n, mean, M2)
 // of a group are merged by the pairwise update of means.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int64_t rows, int64_t nch) {
+__global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int rows, int nch) {
     extern __shared__ float2 vstat[];                     // (np, nvec) pairs (mean, M2)
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
     const T *x = static_cast<const T *>(a.x) + s.base;
-    for (int v = s.v0; v < s.nvec; v += s.np > 1 ? s.nvec : SQT) {
-        const int64_t n = (s.t1 - s.t0 - s.ph + s.np - 1) / s.np;      // this thread's tokens
+    for (int v = s.v0; v < s.nvec; v += s.vstep) {
+        const int n = (int)((unsigned)(s.t1 - s.t0 - s.ph + s.np - 1) / (unsigned)s.np);   // this thread's tokens
         float K = 0.f, S = 0.f, Q = 0.f;
         if (n > 0) {
-            const T *p = x + (s.t0 + s.ph) * a.C + (int64_t)v * VEC;
+            const T *p = x + (int64_t)(s.t0 + s.ph) * a.C + v * VEC;
             const int64_t step = s.np * a.C;
             float sum[VEC], q[VEC];
             K = ldf(p, 0);
 #pragma unroll
             for (int e = 0; e < VEC; e++) sum[e] = q[e] = 0.f;
 #pragma unroll 4
-            for (int64_t t = 0; t < n; t++) {
+            for (int t = 0; t < n; t++, p += step) {
                 float y[VEC];
-                ldv<VEC>(p + t * step, y);
+                ldv<VEC>(p, y);
 #pragma unroll
                 for (int e = 0; e < VEC; e++) {
                     const float d = y[e] - K;
@@ -502,9 +474,9 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int64_t rows, in
     }
     __syncthreads();
     // one warp per group: the mean of the threads' means, then their spread
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31, nt = (int)(s.t1 - s.t0);
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31, nt = s.t1 - s.t0;
     const float tot = (float)nt * (float)s.dvec;          // tokens times vectors
-    float2 *out = reinterpret_cast<float2 *>(a.ws) + (s.bi * nch + s.ch) * a.G;
+    float2 *out = reinterpret_cast<float2 *>(a.ws) + (int64_t)blockIdx.x * a.G;
     for (int g = w; g < a.G; g += SQT / 32) {
         float m = 0.f;
         for (int ph = 0; ph < s.np; ph++) {
@@ -526,42 +498,53 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int64_t rows, in
     }
 }
 
-// Every CTA merges its sequence's chunks itself (a few KB from L2), a warp a
-// group, before it applies them: less than a launch of its own costs.
+// Every CTA merges its sequence's chunks itself (a few KB from L2) before it
+// applies them: less than a launch of its own costs.
 template <typename T, int VEC, int ACT, bool GATE>
-__global__ void __launch_bounds__(SQT) k_gn_seq_apply(GnArgs a, int64_t rows, int64_t nch) {
+__global__ void __launch_bounds__(SQT) k_gn_seq_apply(GnArgs a, int rows, int nch) {
     constexpr bool FAST = sizeof(T) == 2;
     extern __shared__ float2 gstat[];                     // G pairs (mean, rstd)
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
     {
+        // thread = (group of 32, every eighth chunk): sums of n d and of M2 + n d^2,
+        // d from the first chunk's mean, so that nothing of size mean^2 cancels
+        __shared__ float2 sh[8][32];
         const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-        const float D = (float)(a.C / a.G), n = (float)a.L * D, inv = 1.f / n;
-        for (int g = w; g < a.G; g += SQT / 32) {
-            const float2 *p = reinterpret_cast<const float2 *>(a.ws) + s.bi * nch * a.G + g;
-            float m = 0.f;
-            for (int64_t c = l; c < nch; c += 32) {
-                const float nc = (float)((c + 1) * rows < a.L ? rows : a.L - c * rows) * D;
-                m = fmaf(p[c * a.G].x, nc * inv, m);
+        const float D = (float)(a.C / a.G), n = (float)a.L * D;
+        const float nfull = (float)rows * D, nlast = (float)((int)a.L - (nch - 1) * rows) * D;
+        for (int g0 = 0; g0 < a.G; g0 += 32) {
+            const int g = g0 + l;
+            const float2 *p = reinterpret_cast<const float2 *>(a.ws) + (int64_t)s.bi * nch * a.G + g;
+            float K = 0.f, s1 = 0.f, s2 = 0.f;
+            if (g < a.G) {
+                K = p[0].x;
+#pragma unroll 8
+                for (int c = w; c < nch; c += 8) {
+                    const float2 q = p[c * (int)a.G];
+                    const float nc = c + 1 < nch ? nfull : nlast, d = q.x - K;
+                    s1 = fmaf(nc, d, s1);
+                    s2 += fmaf(nc * d, d, q.y);
+                }
             }
-            m = team_sum(m, 32);
-            float M2 = 0.f;
-            for (int64_t c = l; c < nch; c += 32) {
-                const float nc = (float)((c + 1) * rows < a.L ? rows : a.L - c * rows) * D;
-                const float2 q = p[c * a.G];
-                const float d = q.x - m;
-                M2 += fmaf(nc * d, d, q.y);
-            }
-            M2 = team_sum(M2, 32);
-            if (l == 0) {
-                const float rstd = rsqrtf(M2 / n + a.eps);
+            __syncthreads();
+            sh[w][l] = make_float2(s1, s2);
+            __syncthreads();
+            if (w == 0 && g < a.G) {
+                s1 = s2 = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    s1 += sh[i][l].x;
+                    s2 += sh[i][l].y;
+                }
+                const float dm = s1 / n, m = K + dm, rstd = rsqrtf(fmaxf(s2 - s1 * dm, 0.f) / n + a.eps);
                 gstat[g] = make_float2(m, rstd);
-                if (s.ch == 0 && a.mean) a.mean[s.bi * a.G + g] = m;
-                if (s.ch == 0 && a.rstd) a.rstd[s.bi * a.G + g] = rstd;
+                if (s.ch == 0 && a.mean) a.mean[(int64_t)s.bi * a.G + g] = m;
+                if (s.ch == 0 && a.rstd) a.rstd[(int64_t)s.bi * a.G + g] = rstd;
             }
         }
         __syncthreads();
     }
-    for (int v = s.v0; v < s.nvec; v += s.np > 1 ? s.nvec : SQT) {
+    for (int v = s.v0; v < s.nvec; v += s.vstep) {
         const float2 st = gstat[v / s.dvec];
         float w[VEC], b[VEC];
 #pragma unroll
@@ -569,9 +552,10 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_apply(GnArgs a, int64_t rows, in
             w[e] = a.w ? a.w[v * VEC + e] : 1.f;
             b[e] = a.b ? a.b[v * VEC + e] : 0.f;
         }
+        int64_t o = s.base + (int64_t)(s.t0 + s.ph) * a.C + v * VEC;
+        const int64_t step = s.np * a.C;
 #pragma unroll 4
-        for (int64_t t = s.t0 + s.ph; t < s.t1; t += s.np) {
-            const int64_t o = s.base + t * a.C + (int64_t)v * VEC;
+        for (int t = s.t0 + s.ph; t < s.t1; t += s.np, o += step) {
             float x[VEC], z[VEC];
             ldv<VEC>(static_cast<const T *>(a.x) + o, x);
             if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + o, z);
@@ -604,14 +588,14 @@ __device__ __forceinline__ float gn_du(float x, float dy, float z, float2 st, fl
 // Per (sequence, chunk, channel): sums of du xh and du over the chunk's
 // tokens, (sequence, chunk, 2, C); the gate's gradient is written on the way.
 template <typename T, int VEC, int ACT, bool GATE>
-__global__ void __launch_bounds__(SQT) k_gn_seq_bsums(GnArgs a, int64_t rows, int64_t nch) {
+__global__ void __launch_bounds__(SQT) k_gn_seq_bsums(GnArgs a, int rows, int nch) {
     constexpr bool FAST = sizeof(T) == 2;
     extern __shared__ float psum[];                       // (np - 1, 2, C): the other phases' sums
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
     float *out = a.ws + (size_t)blockIdx.x * 2 * a.C;
     float s1[VEC], s2[VEC];
-    for (int v = s.v0; v < s.nvec; v += s.np > 1 ? s.nvec : SQT) {
-        const int64_t gi = s.bi * a.G + v / s.dvec;
+    for (int v = s.v0; v < s.nvec; v += s.vstep) {
+        const int gi = s.bi * (int)a.G + v / s.dvec;
         const float2 st = make_float2(a.mean_in[gi], a.rstd_in[gi]);
         float w[VEC], b[VEC];
 #pragma unroll
@@ -620,9 +604,10 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_bsums(GnArgs a, int64_t rows, in
             b[e] = a.b ? a.b[v * VEC + e] : 0.f;
             s1[e] = s2[e] = 0.f;
         }
+        int64_t o = s.base + (int64_t)(s.t0 + s.ph) * a.C + v * VEC;
+        const int64_t step = s.np * a.C;
 #pragma unroll 4
-        for (int64_t t = s.t0 + s.ph; t < s.t1; t += s.np) {
-            const int64_t o = s.base + t * a.C + (int64_t)v * VEC;
+        for (int t = s.t0 + s.ph; t < s.t1; t += s.np, o += step) {
             float x[VEC], dy[VEC], z[VEC], dz[VEC];
             ldv<VEC>(static_cast<const T *>(a.x) + o, x);
             ldv<VEC>(static_cast<const T *>(a.dy) + o, dy);
@@ -669,12 +654,12 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_bsums(GnArgs a, int64_t rows, in
 // Per (sequence, group): the chunks' sums added up into (sequence, 2, C), and
 // from them mean(dn xh) and mean(dn).  One block a (sequence, group): warps
 // over chunks, lanes over the group's channels.
-__global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, int64_t nch, float *sums, float2 *mom) {
+__global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, int nch, float *sums, float2 *mom) {
     __shared__ float sh[2][8][32];
     __shared__ float red[2];
     const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-    const int64_t bi = blockIdx.x / a.G, g = blockIdx.x % a.G;
-    const int D = (int)(a.C / a.G);
+    const int bi = (int)(blockIdx.x / (unsigned)a.G), g = (int)blockIdx.x - bi * (int)a.G;
+    const int D = (int)((unsigned)a.C / (unsigned)a.G);
     float m2 = 0.f, m1 = 0.f;
     for (int c0 = 0; c0 < D; c0 += 32) {
         const int c = c0 + l;
@@ -682,9 +667,9 @@ __global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, int64_t nch, f
         if (c < D) {
             const float *p = a.ws + (size_t)bi * nch * 2 * a.C + g * D + c;
 #pragma unroll 4
-            for (int64_t k = w; k < nch; k += 8) {
-                s1 += p[k * 2 * a.C];
-                s2 += p[k * 2 * a.C + a.C];
+            for (int k = w; k < nch; k += 8) {
+                s1 += p[(int64_t)k * 2 * a.C];
+                s2 += p[(int64_t)k * 2 * a.C + a.C];
             }
         }
         __syncthreads();
@@ -696,7 +681,7 @@ __global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, int64_t nch, f
 #pragma unroll
             for (int i = 0; i < 8; i++) t += sh[w][i][l];
             if (c < D) {
-                sums[bi * 2 * a.C + w * a.C + g * D + c] = t;
+                sums[(int64_t)bi * 2 * a.C + w * a.C + g * D + c] = t;
                 const float wt = a.w ? a.w[g * D + c] : 1.f;
                 if (w == 0) m2 = fmaf(t, wt, m2);
                 else m1 = fmaf(t, wt, m1);
@@ -708,12 +693,12 @@ __global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, int64_t nch, f
         if (l == 0) red[w] = t / ((float)a.L * (float)D);
     }
     __syncthreads();
-    if (threadIdx.x == 0) mom[bi * a.G + g] = make_float2(red[0], red[1]);
+    if (threadIdx.x == 0) mom[blockIdx.x] = make_float2(red[0], red[1]);
 }
 
 // dx; the last blocks add up dw and db instead
 template <typename T, int VEC, int ACT, bool GATE>
-__global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int64_t rows, int64_t nch, const float *sums,
+__global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int rows, int nch, const float *sums,
                                                    const float2 *mom, unsigned dx_blocks) {
     constexpr bool FAST = sizeof(T) == 2;
     if (blockIdx.x >= dx_blocks) {
@@ -721,8 +706,8 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int64_t rows, int64
         return;
     }
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
-    for (int v = s.v0; v < s.nvec; v += s.np > 1 ? s.nvec : SQT) {
-        const int64_t gi = s.bi * a.G + v / s.dvec;
+    for (int v = s.v0; v < s.nvec; v += s.vstep) {
+        const int gi = s.bi * (int)a.G + v / s.dvec;
         const float2 st = make_float2(a.mean_in[gi], a.rstd_in[gi]), mm = mom[gi];
         float w[VEC], b[VEC];
 #pragma unroll
@@ -730,9 +715,10 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int64_t rows, int64
             w[e] = a.w ? a.w[v * VEC + e] : 1.f;
             b[e] = a.b ? a.b[v * VEC + e] : 0.f;
         }
+        int64_t o = s.base + (int64_t)(s.t0 + s.ph) * a.C + v * VEC;
+        const int64_t step = s.np * a.C;
 #pragma unroll 4
-        for (int64_t t = s.t0 + s.ph; t < s.t1; t += s.np) {
-            const int64_t o = s.base + t * a.C + (int64_t)v * VEC;
+        for (int t = s.t0 + s.ph; t < s.t1; t += s.np, o += step) {
             float x[VEC], dy[VEC], z[VEC];
             ldv<VEC>(static_cast<const T *>(a.x) + o, x);
             ldv<VEC>(static_cast<const T *>(a.dy) + o, dy);
@@ -784,12 +770,16 @@ Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd)
         const int64_t nv = ceil_div(nvec, p.tw);
         p.nv = 1;
         while (p.nv < nv) p.nv *= 2;
-        // about six CTAs per SM, at least two rows a team (weights are read
-        // once a team); always enough teams for one of each group
         const int64_t teams_cta = RT / p.tw, need = ceil_div(G, teams_cta);
-        int64_t blocks = ceil_div(Bt * G, teams_cta * 2);
-        const int64_t cap = 148 * (bwd ? 3 : 6);          // CTAs that fit: 80 and 40 registers a thread
-        if (blocks > cap) blocks = cap;
+        int64_t blocks = ceil_div(Bt * G, teams_cta);
+        if (!bwd) {
+            p.blocks = (unsigned)blocks;
+            return p;
+        }
+        // backward: the CTAs that are resident at once, at least two rows a
+        // team; always enough teams for one of each group
+        blocks = (blocks + 1) / 2;
+        if (blocks > 148 * 2) blocks = 148 * 2;
         if (blocks < need) blocks = need;
         p.blocks = (unsigned)blocks;
         p.nslots = blocks * teams_cta / G;
@@ -873,7 +863,7 @@ cudaError_t seq_fwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
     if (smem > 48 * 1024 &&
         (e = cudaFuncSetAttribute(k_gn_seq_stats<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
         return e;
-    k_gn_seq_stats<T, VEC><<<blocks, SQT, smem, s>>>(a, p.rows, p.nch);
+    k_gn_seq_stats<T, VEC><<<blocks, SQT, smem, s>>>(a, (int)p.rows, (int)p.nch);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int gsm = (int)(a.G * sizeof(float2));
@@ -887,7 +877,7 @@ cudaError_t seq_fwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
         else { GN_APPLY_SMEM(T, 1, ACT_ANY, false) }
     }
 #undef GN_APPLY_SMEM
-    GN_ACTS(k_gn_seq_apply, T, VEC, , <<<blocks, SQT, gsm, s>>>(a, p.rows, p.nch))
+    GN_ACTS(k_gn_seq_apply, T, VEC, , <<<blocks, SQT, gsm, s>>>(a, (int)p.rows, (int)p.nch))
     count_launch();
     return cudaGetLastError();
 }
@@ -897,17 +887,17 @@ cudaError_t seq_bwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
     const unsigned blocks = (unsigned)(a.Bt * p.nch);
     const int smem = (int)((seq_phases(a.C, VEC) - 1) * 2 * a.C * sizeof(float));   // below 16 KB: np C / VEC <= 256
     cudaError_t e;
-    GN_ACTS(k_gn_seq_bsums, T, VEC, , <<<blocks, SQT, smem, s>>>(a, p.rows, p.nch))
+    GN_ACTS(k_gn_seq_bsums, T, VEC, , <<<blocks, SQT, smem, s>>>(a, (int)p.rows, (int)p.nch))
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     float *sums = a.ws + (size_t)a.Bt * p.nch * 2 * a.C;
     float2 *mom = reinterpret_cast<float2 *>(sums + (size_t)a.Bt * 2 * a.C);
-    k_gn_seq_moments<<<(unsigned)(a.Bt * a.G), 256, 0, s>>>(a, p.nch, sums, mom);
+    k_gn_seq_moments<<<(unsigned)(a.Bt * a.G), 256, 0, s>>>(a, (int)p.nch, sums, mom);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const unsigned dxb = a.dx ? blocks : 0, rb = (a.dw || a.db) ? (unsigned)ceil_div(2 * a.C, 32) : 0;
     if (dxb + rb == 0) return cudaSuccess;
-    GN_ACTS(k_gn_seq_dx, T, VEC, , <<<dxb + rb, SQT, 0, s>>>(a, p.rows, p.nch, sums, mom, dxb))
+    GN_ACTS(k_gn_seq_dx, T, VEC, , <<<dxb + rb, SQT, 0, s>>>(a, (int)p.rows, (int)p.nch, sums, mom, dxb))
     count_launch();
     return cudaGetLastError();
 }
@@ -935,7 +925,7 @@ cudaError_t launch_gn_fwd(const GnArgs &a, m3_dtype dt, cudaStream_t s) {
 cudaError_t launch_gn_bwd(const GnArgs &a, m3_dtype dt, cudaStream_t s) {
     if (a.Bt == 0 || a.L == 0) {                          // nothing was summed: zeros
         if (!(a.dw || a.db)) return cudaSuccess;
-        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 256, 0, s>>>(nullptr, 0, a.C, a.dw, a.db);
+        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 1024, 0, s>>>(nullptr, 0, a.C, a.dw, a.db);
         count_launch();
         return cudaGetLastError();
     }
@@ -944,7 +934,7 @@ cudaError_t launch_gn_bwd(const GnArgs &a, m3_dtype dt, cudaStream_t s) {
         cudaError_t e =
             dt == M3_BF16 ? row_dispatch<__nv_bfloat16, 8>(a, p, true, s) : row_dispatch<float, 4>(a, p, true, s);
         if (e != cudaSuccess || !(a.dw || a.db)) return e;
-        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 256, 0, s>>>(a.ws, p.parts, a.C, a.dw, a.db);
+        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 1024, 0, s>>>(a.ws, p.parts, a.C, a.dw, a.db);
         count_launch();
         return cudaGetLastError();
     }

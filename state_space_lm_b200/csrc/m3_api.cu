@@ -662,6 +662,7 @@ m3_status check_norm(m3_dtype dtype, m3_act act, const m3_norm_dims &d) {
     if (d.batch < 0 || d.seqlen < 0 || d.channels < 1 || d.ngroups < 1 || d.channels % d.ngroups)
         return M3_ERR_INVALID_ARG;
     if (d.channels > 16384 || d.batch > (int64_t)1 << 24 || d.seqlen > (int64_t)1 << 30) return M3_ERR_UNSUPPORTED;
+    if (d.batch * d.ngroups > kMaxLanes) return M3_ERR_UNSUPPORTED;
     if (sat_product({d.batch, d.seqlen, d.channels}) > kMaxElems) return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }

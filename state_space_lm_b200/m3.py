@@ -564,10 +564,14 @@ class _Device:
         return False
 
 
+# the current stream's handle without building a Stream object (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _run(fn, where, args, dev, stream):
     """fn(*args, stream) on dev."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if stream is None and _raw_stream is not None and dev.index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(dev.index))
     else:
         with _Device(dev, stream) as s:
             rc = fn(*args, s)
@@ -631,9 +635,15 @@ def _linattn_dims(w, q, k, v, seq, which=None):
     return d, need, dev, dt
 
 
-def _own_workspace(need, workspace, dev):
+def _like(t):
+    """An output of t's shape and type, contiguous."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
+def _own_workspace(need, workspace, t):
+    dev = t.device
     if workspace is None:
-        return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
+        return (t.new_empty(need, dtype=torch.uint8) if need else None), need
     if workspace.device != dev:
         raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
     return workspace, workspace.numel() * workspace.element_size()
@@ -658,12 +668,13 @@ def linattn_chunked_fwd(q, k, v, log_decay, scale=None, s0=None, lengths=None, w
     _expect(w, dev, "s0", s0, ns, f, required=False)
     _expect(w, dev, "lengths", lengths, d.batch, torch.int32, required=False)
     if out is None:
-        out = (torch.empty(v.shape, dtype=v.dtype, device=dev),
-               torch.empty((d.batch, d.nheads, d.dstate, d.headdim), dtype=f, device=dev))
-    y, sf = out
-    _expect(w, dev, "y", y, v.numel(), v.dtype)
-    _expect(w, dev, "s_final", sf, ns, f, required=False)
-    ws, nbytes = _own_workspace(need, workspace, dev)
+        y = _like(v)
+        sf = v.new_empty((d.batch, d.nheads, d.dstate, d.headdim), dtype=f) if s0 is None else torch.empty_like(s0)
+    else:
+        y, sf = out
+        _expect(w, dev, "y", y, v.numel(), v.dtype)
+        _expect(w, dev, "s_final", sf, ns, f, required=False)
+    ws, nbytes = _own_workspace(need, workspace, v)
     args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(y), _ptr(sf),
             _ptr(ws), nbytes)
@@ -678,8 +689,11 @@ def linattn_step_decode(q_t, k_t, v_t, log_decay, s, scale=None, y_out=None, str
     d, _, dev, dt = _linattn_dims(w, q_t, k_t, v_t, False)
     _expect(w, dev, "log_decay", log_decay, d.nheads, f)
     _expect(w, dev, "s", s, d.batch * d.nheads * d.dstate * d.headdim, f)
-    y = torch.empty(v_t.shape, dtype=v_t.dtype, device=dev) if y_out is None else y_out
-    _expect(w, dev, "y_t", y, v_t.numel(), v_t.dtype)
+    if y_out is None:
+        y = _like(v_t)
+    else:
+        y = y_out
+        _expect(w, dev, "y_t", y, v_t.numel(), v_t.dtype)
     args = (_row_ptr(q_t), _row_ptr(k_t), _row_ptr(v_t), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), d, _ptr(s), _ptr(y))
     _run(lib().m3_linattn_step_decode, w, args, dev, stream)
@@ -713,8 +727,8 @@ def linattn_chunked_bwd(q, k, v, log_decay, dy, scale=None, s0=None, ds_final=No
             out[n] = pre[n]
             _expect(w, dev, n, out[n], ns if n == "ds0" else {"dq": q, "dk": k, "dv": v}[n].numel(), io)
         else:
-            out[n] = torch.empty(shapes[n], dtype=io, device=dev)
-    ws, nbytes = _own_workspace(need, workspace, dev)
+            out[n] = _like({"dq": q, "dk": k, "dv": v}[n]) if n != "ds0" else v.new_empty(shapes[n], dtype=io)
+    ws, nbytes = _own_workspace(need, workspace, v)
     g = LinattnGrads(*[_ptr(out.get(n)) for n in names])
     args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(dy), _ptr(ds_final),
@@ -761,14 +775,14 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps
     w, f = "m3_group_norm_fwd", torch.float32
     d, need, dev, dt = _norm_dims(w, x, groups, weight, bias, gate, act, M3_WS_NORM_FWD)
     if out is None:
-        g = max(d.ngroups, 0)
-        out = (torch.empty(x.shape, dtype=x.dtype, device=dev), torch.empty((d.batch, g), dtype=f, device=dev),
-               torch.empty((d.batch, g), dtype=f, device=dev))
-    y, mean, rstd = out
-    _expect(w, dev, "y", y, x.numel(), x.dtype)
-    _expect(w, dev, "mean", mean, d.batch * d.ngroups, f, required=False)
-    _expect(w, dev, "rstd", rstd, d.batch * d.ngroups, f, required=False)
-    ws, nbytes = _own_workspace(need, workspace, dev)
+        y, mean = _like(x), x.new_empty((d.batch, max(d.ngroups, 0)), dtype=f)
+        rstd = torch.empty_like(mean)
+    else:
+        y, mean, rstd = out
+        _expect(w, dev, "y", y, x.numel(), x.dtype)
+        _expect(w, dev, "mean", mean, d.batch * d.ngroups, f, required=False)
+        _expect(w, dev, "rstd", rstd, d.batch * d.ngroups, f, required=False)
+    ws, nbytes = _own_workspace(need, workspace, x)
     args = (_ptr(x), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], float(eps), d, _ptr(y), _ptr(mean),
             _ptr(rstd), _ptr(ws), nbytes)
     _run(lib().m3_group_norm_fwd, w, args, dev, stream)
@@ -799,8 +813,9 @@ def group_norm_bwd(x, dy, mean, rstd, groups, weight=None, bias=None, gate=None,
             out[n] = pre[n]
             _expect(w, dev, n, out[n], x.numel() if wide else d.channels, io)
         else:
-            out[n] = torch.empty(shape, dtype=io, device=dev)
-    ws, nbytes = _own_workspace(need, workspace, dev)
+            of = x if wide else weight if n == "dweight" else bias
+            out[n] = x.new_empty(shape, dtype=io) if of is None else _like(of)
+    ws, nbytes = _own_workspace(need, workspace, x)
     args = (_ptr(x), _ptr(dy), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], _ptr(mean), _ptr(rstd), d,
             _ptr(out.get("dx")), _ptr(out.get("dweight")), _ptr(out.get("dbias")), _ptr(out.get("dgate")), _ptr(ws),
             nbytes)
