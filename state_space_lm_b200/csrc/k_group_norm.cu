@@ -16,6 +16,17 @@ namespace {
 
 enum { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2, ACT_RELU = 3, ACT_ANY = -1 };
 
+__device__ __forceinline__ float ex2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // act(u) and act'(u); ACT_ANY takes the activation at run time (the variants
 // without vectors).  FAST: the exponentials of 16-bit outputs use the
 // hardware approximation (2^-21 relative, against a rounding of 2^-8).
@@ -23,14 +34,13 @@ template <int ACT, bool FAST>
 __device__ __forceinline__ void act_both(float u, int act, float &f, float &df) {
     const int A = ACT == ACT_ANY ? act : ACT;
     if (A == ACT_SILU) {
-        const float e = FAST ? __expf(-u) : expf(-u);
-        const float s = FAST ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+        const float s = FAST ? rcp_fast(1.f + ex2_fast(u * -1.4426950408889634f)) : 1.f / (1.f + expf(-u));
         f = u * s;
         df = fmaf(f, 1.f - s, s);
     } else if (A == ACT_GELU) {
         const float p = 0.5f * (1.f + erff(u * 0.70710678118654752f));
         f = u * p;
-        df = fmaf(u * 0.39894228040143268f, FAST ? __expf(-0.5f * u * u) : expf(-0.5f * u * u), p);
+        df = fmaf(u * 0.39894228040143268f, FAST ? ex2_fast(u * u * -0.72134752044448170f) : expf(-0.5f * u * u), p);
     } else if (A == ACT_RELU) {
         f = u > 0.f ? u : (u == u ? 0.f : u);            // a NaN stays a NaN
         df = u > 0.f ? 1.f : 0.f;
@@ -135,12 +145,14 @@ __device__ __forceinline__ float team_sum(float v, int tw) {
 // shared memory (the whole block takes part; `sh` holds a value per warp).
 __device__ __forceinline__ float2 row_sum2(float2 v, int tw, float2 *sh) {
     const int in = tw < 32 ? tw : 32;
-    for (int o = in >> 1; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < in) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
     if (tw > 32) {
-        const int w = threadIdx.x >> 5, nw = tw >> 5, w0 = w / nw * nw;
+        const int w = threadIdx.x >> 5, nw = tw >> 5, w0 = w & ~(nw - 1);
         __syncthreads();
         if ((threadIdx.x & 31) == 0) sh[w] = v;
         __syncthreads();
@@ -152,7 +164,21 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int tw, float2 *sh) {
     }
     return v;
 }
-__device__ __forceinline__ float row_sum(float v, int tw, float2 *sh) { return row_sum2(make_float2(v, 0.f), tw, sh).x; }
+__device__ __forceinline__ float row_sum(float v, int tw, float2 *sh) {
+    const int in = tw < 32 ? tw : 32;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < in) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tw > 32) {
+        const int w = threadIdx.x >> 5, nw = tw >> 5, w0 = w & ~(nw - 1);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) sh[w].x = v;
+        __syncthreads();
+        v = 0.f;
+        for (int i = 0; i < nw; i++) v += sh[w0 + i].x;
+    }
+    return v;
+}
 
 // ------------------------------------------------------------------- row plan
 // A team of tw lanes (8 for 64 bf16 channels, a whole block for 4096) takes one
@@ -436,7 +462,7 @@ __device__ __forceinline__ SeqGeo seq_geo(const GnArgs &a, int vec, int rows, in
 // first value (so a large mean cancels nothing); the threads' (n, mean, M2)
 // of a group are merged by the pairwise update of means.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int rows, int nch) {
+__global__ void __launch_bounds__(SQT, 2) k_gn_seq_stats(GnArgs a, int rows, int nch) {
     extern __shared__ float2 vstat[];                     // (np, nvec) pairs (mean, M2)
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
     const T *x = static_cast<const T *>(a.x) + s.base;
@@ -450,7 +476,7 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int rows, int nc
             K = ldf(p, 0);
 #pragma unroll
             for (int e = 0; e < VEC; e++) sum[e] = q[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
             for (int t = 0; t < n; t++, p += step) {
                 float y[VEC];
                 ldv<VEC>(p, y);
@@ -473,35 +499,54 @@ __global__ void __launch_bounds__(SQT) k_gn_seq_stats(GnArgs a, int rows, int nc
         vstat[s.ph * s.nvec + v] = make_float2(K, Q);
     }
     __syncthreads();
-    // one warp per group: the mean of the threads' means, then their spread
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31, nt = s.t1 - s.t0;
-    const float tot = (float)nt * (float)s.dvec;          // tokens times vectors
-    float2 *out = reinterpret_cast<float2 *>(a.ws) + (int64_t)blockIdx.x * a.G;
-    for (int g = w; g < a.G; g += SQT / 32) {
-        float m = 0.f;
-        for (int ph = 0; ph < s.np; ph++) {
-            const float n = (float)((nt - ph + s.np - 1) / s.np);
-            for (int v = l; v < s.dvec; v += 32) m = fmaf(vstat[ph * s.nvec + g * s.dvec + v].x, n, m);
+    // the phases of a vector merged by its first thread (n tokens each, one
+    // more in the first phases), then a warp per group: the mean of the
+    // vectors' means, and their spread
+    const int nt = s.t1 - s.t0;
+    if (s.np > 1) {
+        if (s.ph == 0) {
+            const int q = (int)((unsigned)nt / (unsigned)s.np), more = nt - q * s.np;
+            const float inv = 1.f / (float)nt;
+            float m = 0.f, M2 = 0.f;
+            for (int ph = 0; ph < s.np; ph++) m = fmaf(vstat[ph * s.nvec + s.v0].x, (float)(q + (ph < more)) * inv, m);
+            for (int ph = 0; ph < s.np; ph++) {
+                const float2 p = vstat[ph * s.nvec + s.v0];
+                const float d = p.x - m;
+                M2 += fmaf((float)((q + (ph < more)) * VEC) * d, d, p.y);
+            }
+            vstat[s.v0] = make_float2(m, M2);
         }
-        m = team_sum(m, 32) / tot;
-        float M2 = 0.f;
-        for (int ph = 0; ph < s.np; ph++) {
-            const float n = (float)((nt - ph + s.np - 1) / s.np * VEC);
-            for (int v = l; v < s.dvec; v += 32) {
-                const float2 p = vstat[ph * s.nvec + g * s.dvec + v];
+        __syncthreads();
+    }
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+    const float inv = 1.f / (float)s.dvec, n = (float)(nt * VEC);
+    float2 *out = reinterpret_cast<float2 *>(a.ws) + (int64_t)blockIdx.x * a.G;
+    // lanes of a warp: `per` of one group, so that narrow groups share a warp
+    int per = 1;
+    while (per < 32 && per < s.dvec) per *= 2;
+    const int gs = 32 / per, gi = l / per, li = l & (per - 1);
+    for (int g0 = w * gs; g0 < (int)a.G; g0 += SQT / 32 * gs) {
+        const int g = g0 + gi;
+        const bool on = g < (int)a.G;
+        float m = 0.f, M2 = 0.f;
+        if (on)
+            for (int v = li; v < s.dvec; v += per) m += vstat[g * s.dvec + v].x;
+        m = team_sum(m, per) * inv;
+        if (on)
+            for (int v = li; v < s.dvec; v += per) {
+                const float2 p = vstat[g * s.dvec + v];
                 const float d = p.x - m;
                 M2 += fmaf(n * d, d, p.y);
             }
-        }
-        M2 = team_sum(M2, 32);
-        if (l == 0) out[g] = make_float2(m, M2);
+        M2 = team_sum(M2, per);
+        if (on && li == 0) out[g] = make_float2(m, M2);
     }
 }
 
 // Every CTA merges its sequence's chunks itself (a few KB from L2) before it
 // applies them: less than a launch of its own costs.
 template <typename T, int VEC, int ACT, bool GATE>
-__global__ void __launch_bounds__(SQT) k_gn_seq_apply(GnArgs a, int rows, int nch) {
+__global__ void __launch_bounds__(SQT, 2) k_gn_seq_apply(GnArgs a, int rows, int nch) {
     constexpr bool FAST = sizeof(T) == 2;
     extern __shared__ float2 gstat[];                     // G pairs (mean, rstd)
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
@@ -588,7 +633,7 @@ __device__ __forceinline__ float gn_du(float x, float dy, float z, float2 st, fl
 // Per (sequence, chunk, channel): sums of du xh and du over the chunk's
 // tokens, (sequence, chunk, 2, C); the gate's gradient is written on the way.
 template <typename T, int VEC, int ACT, bool GATE>
-__global__ void __launch_bounds__(SQT) k_gn_seq_bsums(GnArgs a, int rows, int nch) {
+__global__ void __launch_bounds__(SQT, 2) k_gn_seq_bsums(GnArgs a, int rows, int nch) {
     constexpr bool FAST = sizeof(T) == 2;
     extern __shared__ float psum[];                       // (np - 1, 2, C): the other phases' sums
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
@@ -698,7 +743,7 @@ __global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, int nch, float
 
 // dx; the last blocks add up dw and db instead
 template <typename T, int VEC, int ACT, bool GATE>
-__global__ void __launch_bounds__(SQT) k_gn_seq_dx(GnArgs a, int rows, int nch, const float *sums,
+__global__ void __launch_bounds__(SQT, 2) k_gn_seq_dx(GnArgs a, int rows, int nch, const float *sums,
                                                    const float2 *mom, unsigned dx_blocks) {
     constexpr bool FAST = sizeof(T) == 2;
     if (blockIdx.x >= dx_blocks) {
@@ -790,8 +835,9 @@ Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd)
         }
         return p;
     }
-    // chunks of tokens: about four CTAs per SM, at least 4 tokens each
-    int64_t nch = ceil_div(148 * 4, Bt > 0 ? Bt : 1);
+    // chunks of tokens: the two CTAs per SM that are resident at once, at
+    // least 4 tokens each
+    int64_t nch = 148 * 2 / (Bt > 0 ? Bt : 1);
     if (nch > ceil_div(L, 4)) nch = ceil_div(L, 4);
     if (nch < 1) nch = 1;
     p.rows = ceil_div(L, nch);
