@@ -188,68 +188,93 @@ __device__ __forceinline__ float row_sum(float v, int tw, float2 *sh) {
 // eight elements does).
 constexpr int RT = 256;
 
-// Forward: one team, one (row, group).  Few registers and many resident warps
-// hide the latencies; teams that walk rows with the next one on its way hold
-// half the warps and were slower (16384 x 1024, gated, 16 groups: 32 to 41 us).
-template <typename T, int VEC, int NV, int ACT, bool GATE>
+// Forward: one team, R rows of one group at once.  Few registers and many
+// resident warps hide the latencies; teams that walk rows with the next one on
+// its way hold half the warps and were slower (16384 x 1024, gated, 16 groups:
+// 32 to 41 us).
+template <typename T, int VEC, int NV, int ACT, bool GATE, int R = (VEC > 1 && NV == 1 ? 2 : 1)>
 __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
     constexpr bool FAST = sizeof(T) == 2;
     __shared__ float2 sh[RT / 32];
     const unsigned tsh = 31 - __clz(tw), G = (unsigned)a.G;
     const unsigned team = blockIdx.x * (RT >> tsh) + (threadIdx.x >> tsh);     // below 2^32, see plan_of
     const int li = threadIdx.x & (tw - 1);
-    const unsigned row = team / G, g = team - row * G;
-    const bool on = row < (unsigned)a.Bt;
+    const unsigned row0 = team / G * R, g = team - team / G * G;
     const int D = (int)((unsigned)a.C / G), nvec = D / VEC;
     const float invD = 1.f / (float)D;
-    const int64_t base = (int64_t)row * a.C + g * D;
-    float x[NV][VEC];
-    Raw<T, VEC> z[NV];
-    float s = 0.f;
+    const int64_t base = (int64_t)row0 * a.C + g * D;
+    float x[R][NV][VEC], mean[R], rstd[R];
+    Raw<T, VEC> xr[R][NV], z[R][NV];
+#pragma unroll
+    for (int u = 0; u < R; u++)
+#pragma unroll
+        for (int m = 0; m < NV; m++) {
+            const int v = m * tw + li;
+            if (row0 + u < (unsigned)a.Bt && v < nvec) {
+                xr[u][m].load(static_cast<const T *>(a.x) + base + u * a.C + v * VEC);
+                if (GATE) z[u][m].load(static_cast<const T *>(a.gate) + base + u * a.C + v * VEC);
+            }
+        }
+#pragma unroll
+    for (int u = 0; u < R; u++) {
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < NV; m++) {
+            if (row0 + u < (unsigned)a.Bt && m * tw + li < nvec) {
+                xr[u][m].get(x[u][m]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; e++) x[u][m][e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; e++) s += x[u][m][e];
+        }
+        mean[u] = s;
+    }
+#pragma unroll
+    for (int u = 0; u < R; u++) mean[u] = row_sum(mean[u], tw, sh) * invD;
+#pragma unroll
+    for (int u = 0; u < R; u++) {
+        float q = 0.f;
+#pragma unroll
+        for (int m = 0; m < NV; m++) {
+            const bool in = m * tw + li < nvec;
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                x[u][m][e] -= mean[u];
+                if (in) q = fmaf(x[u][m][e], x[u][m][e], q);
+            }
+        }
+        rstd[u] = q;
+    }
+#pragma unroll
+    for (int u = 0; u < R; u++) rstd[u] = rsqrtf(fmaf(row_sum(rstd[u], tw, sh), invD, a.eps));
+#pragma unroll
+    for (int u = 0; u < R; u++)
+        if (row0 + u < (unsigned)a.Bt && li == 0) {
+            if (a.mean) a.mean[(int64_t)(row0 + u) * G + g] = mean[u];
+            if (a.rstd) a.rstd[(int64_t)(row0 + u) * G + g] = rstd[u];
+        }
 #pragma unroll
     for (int m = 0; m < NV; m++) {
         const int v = m * tw + li;
-#pragma unroll
-        for (int e = 0; e < VEC; e++) x[m][e] = 0.f;
-        if (on && v < nvec) {
-            ldv<VEC>(static_cast<const T *>(a.x) + base + v * VEC, x[m]);
-            if (GATE) z[m].load(static_cast<const T *>(a.gate) + base + v * VEC);
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; e++) s += x[m][e];
-    }
-    const float mean = row_sum(s, tw, sh) * invD;
-    float q = 0.f;
-#pragma unroll
-    for (int m = 0; m < NV; m++) {
-        const bool in = m * tw + li < nvec;
-#pragma unroll
-        for (int e = 0; e < VEC; e++) {
-            x[m][e] -= mean;
-            if (in) q = fmaf(x[m][e], x[m][e], q);
-        }
-    }
-    const float rstd = rsqrtf(fmaf(row_sum(q, tw, sh), invD, a.eps));
-    if (on && li == 0) {
-        if (a.mean) a.mean[team] = mean;
-        if (a.rstd) a.rstd[team] = rstd;
-    }
-#pragma unroll
-    for (int m = 0; m < NV; m++) {
-        const int v = m * tw + li;
-        if (on && v < nvec) {
+        if (v < nvec) {
             float w[VEC], b[VEC], zf[VEC];
             if (a.w) ldv<VEC>(a.w + g * D + v * VEC, w);
             if (a.b) ldv<VEC>(a.b + g * D + v * VEC, b);
-            if (GATE) z[m].get(zf);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                float n = x[m][e] * rstd;
-                if (a.w) n *= w[e];
-                if (a.b) n += b[e];
-                x[m][e] = GATE ? n * act_only<ACT, FAST>(zf[e], a.act) : act_only<ACT, FAST>(n, a.act);
+            for (int u = 0; u < R; u++) {
+                if (row0 + u >= (unsigned)a.Bt) continue;
+                if (GATE) z[u][m].get(zf);
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    float n = x[u][m][e] * rstd[u];
+                    if (a.w) n *= w[e];
+                    if (a.b) n += b[e];
+                    x[u][m][e] = GATE ? n * act_only<ACT, FAST>(zf[e], a.act) : act_only<ACT, FAST>(n, a.act);
+                }
+                stv<VEC>(static_cast<T *>(a.y) + base + u * a.C + v * VEC, x[u][m]);
             }
-            stv<VEC>(static_cast<T *>(a.y) + base + v * VEC, x[m]);
         }
     }
 }
@@ -599,17 +624,30 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_apply(GnArgs a, int rows, int
         }
         int64_t o = s.base + (int64_t)(s.t0 + s.ph) * a.C + v * VEC;
         const int64_t step = s.np * a.C;
-#pragma unroll 4
-        for (int t = s.t0 + s.ph; t < s.t1; t += s.np, o += step) {
-            float x[VEC], z[VEC];
-            ldv<VEC>(static_cast<const T *>(a.x) + o, x);
-            if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + o, z);
+        // four tokens' loads go out together (y may be anywhere: the compiler
+        // keeps loads behind stores)
+        constexpr int U = 4;
+        for (int t = s.t0 + s.ph; t < s.t1; t += U * s.np, o += U * step) {
+            Raw<T, VEC> xr[U], zr[U];
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const float u = fmaf((x[e] - st.x) * st.y, w[e], b[e]);
-                x[e] = GATE ? u * act_only<ACT, FAST>(z[e], a.act) : act_only<ACT, FAST>(u, a.act);
-            }
-            stv<VEC>(static_cast<T *>(a.y) + o, x);
+            for (int u = 0; u < U; u++)
+                if (t + u * s.np < s.t1) {
+                    xr[u].load(static_cast<const T *>(a.x) + o + u * step);
+                    if (GATE) zr[u].load(static_cast<const T *>(a.gate) + o + u * step);
+                }
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (t + u * s.np < s.t1) {
+                    float x[VEC], z[VEC];
+                    xr[u].get(x);
+                    if (GATE) zr[u].get(z);
+#pragma unroll
+                    for (int e = 0; e < VEC; e++) {
+                        const float n = fmaf((x[e] - st.x) * st.y, w[e], b[e]);
+                        x[e] = GATE ? n * act_only<ACT, FAST>(z[e], a.act) : act_only<ACT, FAST>(n, a.act);
+                    }
+                    stv<VEC>(static_cast<T *>(a.y) + o + u * step, x);
+                }
         }
     }
 }
@@ -762,19 +800,31 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_dx(GnArgs a, int rows, int nc
         }
         int64_t o = s.base + (int64_t)(s.t0 + s.ph) * a.C + v * VEC;
         const int64_t step = s.np * a.C;
-#pragma unroll 4
-        for (int t = s.t0 + s.ph; t < s.t1; t += s.np, o += step) {
-            float x[VEC], dy[VEC], z[VEC];
-            ldv<VEC>(static_cast<const T *>(a.x) + o, x);
-            ldv<VEC>(static_cast<const T *>(a.dy) + o, dy);
-            if (GATE) ldv<VEC>(static_cast<const T *>(a.gate) + o, z);
+        constexpr int U = GATE ? 2 : 4;                   // tokens whose loads go out together
+        for (int t = s.t0 + s.ph; t < s.t1; t += U * s.np, o += U * step) {
+            Raw<T, VEC> xr[U], yr[U], zr[U];
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                float xh, dz;
-                const float du = gn_du<ACT, GATE, FAST>(x[e], dy[e], z[e], st, w[e], b[e], a.act, xh, dz);
-                x[e] = (fmaf(du, w[e], -mm.y) - xh * mm.x) * st.y;
-            }
-            stv<VEC>(static_cast<T *>(a.dx) + o, x);
+            for (int u = 0; u < U; u++)
+                if (t + u * s.np < s.t1) {
+                    xr[u].load(static_cast<const T *>(a.x) + o + u * step);
+                    yr[u].load(static_cast<const T *>(a.dy) + o + u * step);
+                    if (GATE) zr[u].load(static_cast<const T *>(a.gate) + o + u * step);
+                }
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (t + u * s.np < s.t1) {
+                    float x[VEC], dy[VEC], z[VEC];
+                    xr[u].get(x);
+                    yr[u].get(dy);
+                    if (GATE) zr[u].get(z);
+#pragma unroll
+                    for (int e = 0; e < VEC; e++) {
+                        float xh, dz;
+                        const float du = gn_du<ACT, GATE, FAST>(x[e], dy[e], z[e], st, w[e], b[e], a.act, xh, dz);
+                        x[e] = (fmaf(du, w[e], -mm.y) - xh * mm.x) * st.y;
+                    }
+                    stv<VEC>(static_cast<T *>(a.dx) + o + u * step, x);
+                }
         }
     }
 }
@@ -816,7 +866,8 @@ Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd)
         p.nv = 1;
         while (p.nv < nv) p.nv *= 2;
         const int64_t teams_cta = RT / p.tw, need = ceil_div(G, teams_cta);
-        int64_t blocks = ceil_div(Bt * G, teams_cta);
+        const int64_t rows = !bwd && p.vec > 1 && p.nv == 1 ? 2 : 1;   // rows a team takes at once
+        int64_t blocks = ceil_div(ceil_div(Bt, rows) * G, teams_cta);
         if (!bwd) {
             p.blocks = (unsigned)blocks;
             return p;
