@@ -234,54 +234,60 @@ __global__ void __launch_bounds__(256) k_head_sum(const float *in, T *out, int64
 // One token of every lane: S <- S + (S (g - 1) + k v^T), y = scale S^T q.
 // One CTA per lane.  The state is read once and written once in VEC-wide
 // pieces: thread = (row of R, piece of a row), so a warp's accesses are
-// contiguous; the y sums over rows meet in shared memory.  Bound by the
-// state's bytes.
+// contiguous; the y sums over rows meet in shared memory.  The first rows of
+// the state are on their way before anything else is read (a lane of 128 x 64
+// then has its whole 32 KB in flight).  Bound by the state's bytes.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) k_lin_step(LinStepArgs a) {
     __shared__ float qs[256], ks[256], vs[256];
     __shared__ float red[256 * VEC];
     const int tid = threadIdx.x;
-    const int64_t lane = blockIdx.x, b = lane / a.H, h = lane % a.H, hg = h / (a.H / a.G);
+    const unsigned lane = blockIdx.x, H = (unsigned)a.H, b = lane / H, h = lane - b * H;
     const int dk = (int)a.dk, dv = (int)a.dv;
+    const int cols = dv / VEC, R = 256 / cols;            // pieces of a row, rows at a time
+    const int r0 = (int)((unsigned)tid / (unsigned)cols), c = tid - r0 * cols;
+    constexpr int U = 8;
+    float *S = a.s + (size_t)lane * dk * dv + VEC * c;
+    float x[U][VEC], acc[VEC];
+    auto fetch = [&](int rr) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int r = rr + u * R;
+            if (r < dk) {
+                if (VEC == 4) *reinterpret_cast<float4 *>(x[u]) = *reinterpret_cast<const float4 *>(S + r * dv);
+                else x[u][0] = S[r * dv];
+            }
+        }
+    };
+    if (r0 < R) fetch(r0);
+    const int hg = (int)(h / (unsigned)(a.H / a.G));
     const T *q = static_cast<const T *>(a.q) + b * a.ldq + hg * dk;
     const T *k = static_cast<const T *>(a.k) + b * a.ldk + hg * dk;
-    const T *v = static_cast<const T *>(a.v) + b * a.ldv + h * dv;
+    const T *v = static_cast<const T *>(a.v) + b * a.ldv + (int)h * dv;
     if (tid < dk) {
         qs[tid] = ldf(q, tid) * a.scale;
         ks[tid] = ldf(k, tid);
     }
     if (tid < dv) vs[tid] = ldf(v, tid);
     const float gm1 = expm1f(a.log_decay[h]);
-    const int cols = dv / VEC, R = 256 / cols;            // pieces of a row, rows at a time
-    const int c = tid % cols, r0 = tid / cols;
-    float *S = a.s + (size_t)lane * dk * dv;
-    float acc[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; e++) acc[e] = 0.f;
     __syncthreads();
     if (r0 < R) {
-        constexpr int U = 8;
         for (int rr = r0; rr < dk; rr += U * R) {
-            float x[U][VEC];
+            if (rr > r0) fetch(rr);
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 const int r = rr + u * R;
                 if (r < dk) {
-                    if (VEC == 4) *reinterpret_cast<float4 *>(x[u]) = *reinterpret_cast<const float4 *>(S + r * dv + 4 * c);
-                    else x[u][0] = S[r * dv + c];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int r = rr + u * R;
-                if (r < dk) {
+                    const float kr = ks[r], qr = qs[r];
 #pragma unroll
                     for (int e = 0; e < VEC; e++) {
-                        x[u][e] += fmaf(x[u][e], gm1, ks[r] * vs[VEC * c + e]);
-                        acc[e] = fmaf(qs[r], x[u][e], acc[e]);
+                        x[u][e] += fmaf(x[u][e], gm1, kr * vs[VEC * c + e]);
+                        acc[e] = fmaf(qr, x[u][e], acc[e]);
                     }
-                    if (VEC == 4) *reinterpret_cast<float4 *>(S + r * dv + 4 * c) = *reinterpret_cast<float4 *>(x[u]);
-                    else S[r * dv + c] = x[u][0];
+                    if (VEC == 4) *reinterpret_cast<float4 *>(S + r * dv) = *reinterpret_cast<float4 *>(x[u]);
+                    else S[r * dv] = x[u][0];
                 }
             }
         }
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(256) k_lin_step(LinStepArgs a) {
     if (tid < dv) {
         float s = 0.f;
         for (int r = 0; r < R; r++) s += red[r * dv + tid];
-        stf(static_cast<T *>(a.y), lane * dv + tid, s);
+        stf(static_cast<T *>(a.y), (int64_t)lane * dv + tid, s);
     }
 }
 
@@ -330,16 +336,17 @@ cudaError_t launch_mix_simt_d(const MixArgs &a, cudaStream_t s) {
 }  // namespace
 
 // Split the time axis when the lanes' column tiles leave SMs idle: enough
-// segments for about four CTAs per SM, at least 128 tokens each (a segment
+// segments for about four CTAs per SM, at least 64 tokens each (a segment
 // costs a state written and read, and its tokens' b and c twice), at most 64
-// segments and 64 MB of states.
+// segments and 64 MB of states.  (3 x 333 tokens, 5 heads of 37 x 29: 64 us in
+// one piece of each lane.)
 void mix_simt_plan(MixArgs &a) {
     a.nseg = 1;
     a.seg_len = a.T > 0 ? a.T : 1;
     const int64_t lanes = a.Bt * a.H, ctas = lanes * ((a.dc + SP - 1) / SP);
-    if (lanes == 0 || ctas >= 296 || a.T < 512) return;
+    if (lanes == 0 || ctas >= 296 || a.T < 192) return;
     int64_t ns = 592 / ctas;
-    if (ns > a.T / 128) ns = a.T / 128;
+    if (ns > a.T / 64) ns = a.T / 64;
     if (ns > 64) ns = 64;
     const int64_t most = ((int64_t)64 << 20) / (lanes * a.da * a.dc * 4) + 1;
     if (ns > most) ns = most;
