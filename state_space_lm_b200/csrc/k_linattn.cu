@@ -41,11 +41,7 @@ __global__ void __launch_bounds__(ST) k_mix_simt(MixArgs g) {
     const int64_t len = lane_length(g.lengths, bi, g.T);
     const int64_t t0 = seg_begin(seg, g.nseg, g.seg_len, g.reverse);
     const int64_t n = seg_tokens(seg, g.nseg, g.seg_len, g.reverse, len);
-    const double lg = (double)g.log_decay[h];
-    if (tid <= SC) {
-        sm.pw[tid] = decay_pow(lg, tid);
-        sm.pm1[tid] = decay_pow_m1(lg, tid);
-    }
+    if (tid <= SC) decay_pow_f32(g.log_decay[h], tid, sm.pw[tid], sm.pm1[tid]);
     const int64_t row0 = bi * g.T;
     const T *A = static_cast<const T *>(g.a) + (int64_t)(h / g.ra) * g.da;
     const T *B = static_cast<const T *>(g.b) + (int64_t)(h / g.rb) * g.da;
@@ -136,8 +132,9 @@ __global__ void __launch_bounds__(ST) k_mix_simt(MixArgs g) {
             float own[RS];
 #pragma unroll
             for (int i = 0; i < RS; i++) own[i] = 0.f;
-            for (int j = 0; j < L; j++) {
-                const float cw = sm.c[j][l] * (sm.pw[g.reverse ? L - j : L - 1 - j] * g.scale_w);
+#pragma unroll 4
+            for (int j = 0; j < SC; j++) {                // rows behind the block's tokens are zeros
+                const float cw = sm.c[j][l] * (sm.pw[max(0, g.reverse ? L - j : L - 1 - j)] * g.scale_w);
 #pragma unroll
                 for (int i = 0; i < RS; i += 4) {
                     const float4 x = *reinterpret_cast<const float4 *>(&sm.b[j][w * RS + i]);
@@ -338,8 +335,8 @@ cudaError_t launch_mix_simt_d(const MixArgs &a, cudaStream_t s) {
 // Split the time axis when the lanes' column tiles leave SMs idle: enough
 // segments for about four CTAs per SM, at least 64 tokens each (a segment
 // costs a state written and read, and its tokens' b and c twice), at most 64
-// segments and 64 MB of states.  (3 x 333 tokens, 5 heads of 37 x 29: 64 us in
-// one piece of each lane.)
+// segments and 64 MB of states.  (3 x 333 tokens, 5 heads of 37 x 29, fp32:
+// 64 us in one piece of each lane, 31 us in five.)
 void mix_simt_plan(MixArgs &a) {
     a.nseg = 1;
     a.seg_len = a.T > 0 ? a.T : 1;

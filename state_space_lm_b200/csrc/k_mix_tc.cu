@@ -42,30 +42,38 @@ namespace m3 {
 namespace mixtc {
 using namespace ptx;
 
-constexpr int Q = 64, DC = 64, DA = 128;               // chunk, columns of a tile, widest a and b rows
+constexpr int Q = 64, DC = 64, DA = 128;               // chunk, columns of a tile, widest a, b and c rows
 constexpr int W_TMA = 0, W_S = 1, W_D = 2, W_Y23 = 3, W_CW = 4, W_SC = 8, W_ST = 12, W_Y = 20, NWARPS = 24;
 constexpr int THREADS = NWARPS * 32;
 
-// ---- shared memory (bytes from a 1024-aligned base), all tiles 128B-swizzled
-constexpr int NST = 3;                                  // stages of A, B, C
+// ---- shared memory (bytes from a 1024-aligned base), all tiles 128B-swizzled.
+// KD, the width that a and b rows are padded to (64 or 128): with 64 the
+// tensor cores read and the state warps keep half, and more stages fit.
+constexpr int SZ_T = Q * DC * 2, SZ_C = SZ_T;           // one 64 x 64 bf16 tile
+template <int KD>
+struct Lay {
+    static constexpr int NST = KD == 64 ? 5 : 3;        // stages of A, B, C
+    static constexpr int SZ_AB = Q * KD * 2, SZ_STAGE = 2 * SZ_AB + SZ_C;
+    static constexpr int SZ_M = KD * DC * 2;
+    static constexpr int OFF_STAGE = 0;
+    static constexpr int OFF_CW = OFF_STAGE + NST * SZ_STAGE;   // 2 x 3 pieces
+    static constexpr int OFF_P = OFF_CW + 2 * 3 * SZ_T;         // 2
+    static constexpr int OFF_M = OFF_P + 2 * SZ_T;              // 2
+    static constexpr int OFF_Y = OFF_M + 2 * SZ_M;              // 1
+    static constexpr int OFF_PW = OFF_Y + SZ_T;                 // fp32 g^0 .. g^64, then g^n - 1
+    static constexpr int OFF_BAR = OFF_PW + 2 * 72 * 4;
+    static constexpr int OFF_MISC = OFF_BAR + 40 * 8;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+constexpr int NPW = 72, MAXST = 5;
 constexpr int PFD = 3;                                  // chunks that the L2 prefetch runs ahead of the loads
-constexpr int SZ_AB = Q * DA * 2, SZ_C = Q * DC * 2, SZ_STAGE = 2 * SZ_AB + SZ_C;
-constexpr int SZ_T = Q * DC * 2;                        // one 64 x 64 bf16 tile
-constexpr int SZ_M = DA * DC * 2;
-constexpr int OFF_STAGE = 0;
-constexpr int OFF_CW = OFF_STAGE + NST * SZ_STAGE;      // 2 x 3 pieces
-constexpr int OFF_P = OFF_CW + 2 * 3 * SZ_T;            // 2
-constexpr int OFF_M = OFF_P + 2 * SZ_T;                 // 2
-constexpr int OFF_Y = OFF_M + 2 * SZ_M;                 // 1
-constexpr int OFF_PW = OFF_Y + SZ_T;                    // fp32 g^0 .. g^64, then g^n - 1
-constexpr int NPW = 72;
-constexpr int OFF_BAR = OFF_PW + 2 * NPW * 4;
 enum {
     B_FULL = 0,                    // NST: a stage has arrived
-    B_EMPTY = B_FULL + NST,        // NST: its readers are done
+    B_EMPTY = B_FULL + MAXST,      // NST: its readers are done
     // 2 of each from here on.  "Full" of an accumulator also says that the
     // operands it was made from may be overwritten: P and M (Y)
-    B_CWFULL = B_EMPTY + NST,      // Cw in shared memory
+    B_CWFULL = B_EMPTY + MAXST,      // Cw in shared memory
     B_CWEMPTY = B_CWFULL + 2,
     B_PFULL = B_CWEMPTY + 2,       // masked scores in shared memory
     B_MFULL = B_PFULL + 2,         // the entering state in shared memory
@@ -79,9 +87,7 @@ enum {
     B_DRAIN = B_ZERO + 1,          // 3: every UMMA of an issuing warp is done
     NBAR = B_DRAIN + 3
 };
-constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-constexpr int SMEM = OFF_MISC + 16 + 1024;
-static_assert(SMEM <= 227 * 1024, "shared memory budget");
+static_assert(NBAR <= 40, "barriers");
 
 constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_D = 64, COL_Y2 = 256, COL_Y3 = 384;   // 64, 3 x 64, 2 x 64, 2 x 64
 
@@ -106,8 +112,13 @@ __device__ __forceinline__ uint32_t round2(f32x2 v) {
     return pack_bf16(a, b);
 }
 
-template <bool SO>
+template <bool SO, int KD>
 __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ Batch P) {
+    using L_ = Lay<KD>;
+    constexpr int NST = L_::NST, SZ_AB = L_::SZ_AB, SZ_STAGE = L_::SZ_STAGE, SZ_M = L_::SZ_M;
+    constexpr int OFF_STAGE = L_::OFF_STAGE, OFF_CW = L_::OFF_CW, OFF_P = L_::OFF_P, OFF_M = L_::OFF_M;
+    constexpr int OFF_Y = L_::OFF_Y, OFF_PW = L_::OFF_PW, OFF_BAR = L_::OFF_BAR, OFF_MISC = L_::OFF_MISC;
+    constexpr int NX = KD / 64;                         // 64-column halves of an A or B tile
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(sm);
@@ -139,9 +150,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         const uint32_t s0 = sbase + OFF_STAGE + st * SZ_STAGE, fb = bar(B_FULL + st);
         mbar_expect_tx(fb, SO ? SZ_AB + SZ_C : SZ_STAGE);
 #pragma unroll
-        for (int x = 0; x < 2; x++) {
-            if (!SO) tma_load4(s0 + x * (SZ_AB / 2), &P.ma[pi], 64 * x, ha, t, (int)b32, fb);
-            tma_load4(s0 + SZ_AB + x * (SZ_AB / 2), &P.mb[pi], 64 * x, hb, t, (int)b32, fb);
+        for (int x = 0; x < NX; x++) {
+            if (!SO) tma_load4(s0 + x * SZ_T, &P.ma[pi], 64 * x, ha, t, (int)b32, fb);
+            tma_load4(s0 + SZ_AB + x * SZ_T, &P.mb[pi], 64 * x, hb, t, (int)b32, fb);
         }
         tma_load4(s0 + 2 * SZ_AB, &P.mc[pi], p0, hc, t, (int)b32, fb);
     };
@@ -218,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 }
         }
     } else if (warp < W_CW) {
-        constexpr uint32_t id_kk = idesc(64, 64, 0, 0), id_kmn = idesc(64, 64, 0, 1), id_st = idesc(128, 192, 1, 1);
+        constexpr uint32_t id_kk = idesc(64, 64, 0, 0), id_kmn = idesc(64, 64, 0, 1), id_st = idesc(KD, 192, 1, 1);
         // Descriptor steps (16-byte units): a K-step of 16 is 32 bytes of a
         // K-major row (the second 64 columns lie half a tile further), and two
         // groups of 8 rows (MN) of an MN-major one.  The issue loops are
@@ -229,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         constexpr uint64_t MN = 2048 >> 4;
         const uint64_t d_k0 = sdesc(sbase + OFF_STAGE, 16, 1024), d_mn0 = sdesc(sbase + OFF_STAGE, Q * 128, 1024);
         const uint64_t d_cw0 = sdesc(sbase + OFF_CW, SZ_T, 1024), d_p0 = sdesc(sbase + OFF_P, 16, 1024);
-        const uint64_t d_m0 = sdesc(sbase + OFF_M, DA * 128, 1024);
+        const uint64_t d_m0 = sdesc(sbase + OFF_M, KD * 128, 1024);
         constexpr uint64_t ST = SZ_STAGE >> 4, AB = SZ_AB >> 4, TT = SZ_T >> 4, MM = SZ_M >> 4;
         int st = 0, k3 = 0;                             // stage, turn of the ring
         if (warp == W_S && !SO) {
@@ -242,10 +253,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     const uint64_t da = d_k0 + st * ST, db = da + AB;
                     const uint32_t d = tmem + COL_S;
 #pragma unroll 1
-                    for (int x = 0; x < 2; x++)
+                    for (int x = 0; x < NX; x++)
 #pragma unroll
                         for (int kk = 0; kk < 4; kk++)
-                            umma(d, da + x * (AB / 2) + kk * 2, db + x * (AB / 2) + kk * 2, id_kk, x + kk > 0);
+                            umma(d, da + x * TT + kk * 2, db + x * TT + kk * 2, id_kk, x + kk > 0);
                     umma_commit(bar(B_SFULL));
                 }
                 __syncwarp();
@@ -283,10 +294,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     const uint64_t da = d_k0 + st * ST, dm = d_m0 + pb * MM;
                     const uint32_t d = tmem + COL_Y3 + pb * 64;
 #pragma unroll 1
-                    for (int x = 0; x < 2; x++)
+                    for (int x = 0; x < NX; x++)
 #pragma unroll
                         for (int kk = 0; kk < 4; kk++)
-                            umma(d, da + x * (AB / 2) + kk * 2, dm + (4 * x + kk) * MN, id_kmn, x + kk > 0);
+                            umma(d, da + x * TT + kk * 2, dm + (4 * x + kk) * MN, id_kmn, x + kk > 0);
                 }
                 __syncwarp();
                 if (!wait(B_PFULL + pb, k2, 118)) break;
@@ -330,8 +341,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     if (row >= L) {
                         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4 *>(ct + o) = z;
-                        *reinterpret_cast<uint4 *>(ct + o - SZ_AB) = z;
-                        *reinterpret_cast<uint4 *>(ct + o - SZ_AB / 2) = z;
+#pragma unroll
+                        for (int x = 1; x <= NX; x++) *reinterpret_cast<uint4 *>(ct + o - x * SZ_T) = z;
                     }
                 fence_async_smem();
                 arrive(B_ZERO);
@@ -430,7 +441,80 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 }
             }
         }
-    } else if (warp < W_Y) {
+    } else if (KD == 64 && warp < W_Y) {
+        // ---- the state of 64 rows (an M = 64 accumulator): two rows, 32 of
+        // the tile's columns in pairs, fp32
+        const int q = warp & 3, c0 = 32 * ((warp - W_ST) >> 2);
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + COL_D + c0;
+        const size_t elems = (size_t)g.da * g.dc;
+        float *slots = g.ws + (size_t)lane * (g.nseg - 1) * elems;
+        const int ra = 16 * q + (l32 >> 2), pc = p0 + c0 + 2 * (l32 & 3);
+        f32x2 M[8];                                     // pair e: row ra + 8 (e & 1), columns 8 (e / 2) + 0, 1
+        // where pair e lies in a state of global memory; a quad's four pairs
+        // are 32 bytes of a row
+        auto inside = [&](int e) { return ra + 8 * (e & 1) < g.da && pc + 8 * (e >> 1) < g.dc; };
+        auto at = [&](int e, int odd, bool tr) {
+            const size_t n = ra + 8 * (e & 1), p = pc + 8 * (e >> 1) + odd;
+            return tr ? p * g.da + n : n * g.dc + p;
+        };
+        {
+            const float *src = (SO || (seg == 0 && !g.m0)) ? nullptr
+                               : (seg == 0 ? g.m0 + lane * elems : slots + (size_t)(seg - 1) * elems);
+            const bool tr = seg == 0 && g.m_trans;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                M[e] = src && inside(e) ? pair(src[at(e, 0, tr)], src[at(e, 1, tr)]) : 0ull;
+        }
+        const int mr = 16 * q + (l32 & 15), mc = l32 >> 4;
+        uint32_t mo[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) mo[i] = sbase + OFF_M + mr * 128 + (((c0 / 8 + 2 * i + mc) ^ (mr & 7)) << 4);
+        auto publish = [&](int buf) {                   // the rounded copy that D3 reads
+            stmatrix4(mo[0] + buf * SZ_M, round2(M[0]), round2(M[1]), round2(M[2]), round2(M[3]));
+            stmatrix4(mo[1] + buf * SZ_M, round2(M[4]), round2(M[5]), round2(M[6]), round2(M[7]));
+            fence_async_smem();
+            arrive(B_MFULL + buf);
+        };
+        if (!SO && nch > 0) publish(0);
+        for (int c = 0; c < nch; c++) {
+            const int pb = c & 1;
+            const float d1 = pm1[chunk_n(c)];
+            const f32x2 dm1 = pair(d1, d1);
+            if (!wait(B_DFULL, c, 114)) break;
+            tc_fence_after();
+            float hi[16], mid[16], lo[16];
+            tmem_ld16x256b_x4(tl, hi);
+            tmem_ld16x256b_x4(tl + 64, mid);
+            tmem_ld16x256b_x4(tl + 128, lo);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const f32x2 s = add2(add2(pair(lo[2 * e], lo[2 * e + 1]), pair(mid[2 * e], mid[2 * e + 1])),
+                                     pair(hi[2 * e], hi[2 * e + 1]));
+                M[e] = add2(fma2(M[e], dm1, M[e]), s);
+            }
+            tc_fence_before();
+            arrive(B_DEMPTY);
+            if (!SO && c + 1 < nch) {
+                // buffer (c+1) & 1 was last read by D3 of chunk c - 1
+                if (c > 0 && !wait(B_YFULL + (pb ^ 1), (c - 1) >> 1, 115)) break;
+                publish(pb ^ 1);
+            }
+        }
+        float *dst = SO ? slots + (size_t)seg * elems
+                        : (seg == g.nseg - 1 && g.m_out ? g.m_out + lane * elems : nullptr);
+        if (dst && !*abort_flag) {
+            const bool tr = !SO && g.m_trans;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                if (inside(e)) {
+                    float a, b2;
+                    unpair(M[e], a, b2);
+                    dst[at(e, 0, tr)] = a;
+                    dst[at(e, 1, tr)] = b2;
+                }
+        }
+    } else if (KD == 128 && warp < W_Y) {
         // ---- the state: this thread's row, 32 of the tile's columns, fp32
         const int q = warp & 3, n = 32 * q + l32, ch = (warp - W_ST) >> 2, c0 = 32 * ch;
         const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + COL_D + c0;
@@ -672,16 +756,20 @@ bool mix_tc_sizes(const MixArgs &g, m3_dtype dt) {
     return true;
 }
 
-// Segments of the problems of one launch (the same count for all).  A CTA
+static int padded(const MixArgs &g) { return g.da <= 64 ? 64 : 128; }
+
+// Segments of the problems of one launch (those padded to the same width; the
+// same count for all).  A CTA
 // holds an SM, so k CTAs take ceil(k / 148) waves of (chunks of a segment);
 // the state pass over the leading segments costs about 0.6 of a full chunk per
 // chunk.  The count with the least time in those units, at least 4 chunks a
 // segment, at most 64 segments and 64 MB of states.
-void mix_tc_plan(MixArgs *g, int n) {
+static void plan_width(MixArgs *g, int n, int kd) {
     using namespace mixtc;
     const int64_t nq = (g[0].T + Q - 1) / Q;
     int64_t ctas = 0, state = 0;
     for (int i = 0; i < n; i++) {
+        if (padded(g[i]) != kd) continue;
         ctas += g[i].Bt * g[i].H * ((g[i].dc + DC - 1) / DC);
         state += g[i].Bt * g[i].H * g[i].da * g[i].dc * 4;
         g[i].nseg = 1;
@@ -699,71 +787,86 @@ void mix_tc_plan(MixArgs *g, int n) {
         const double cost = ((double)waves(ctas * k) + 0.6 * (double)waves(ctas * (k - 1))) * (double)len;
         if (cost < best - 1e-9) {
             best = cost;
-            for (int i = 0; i < n; i++) {
-                g[i].nseg = (int)k;
-                g[i].seg_len = len * Q;
-            }
+            for (int i = 0; i < n; i++)
+                if (padded(g[i]) == kd) {
+                    g[i].nseg = (int)k;
+                    g[i].seg_len = len * Q;
+                }
         }
     }
+}
+void mix_tc_plan(MixArgs *g, int n) {
+    plan_width(g, n, 64);
+    plan_width(g, n, 128);
 }
 
 // What a launch needs of its device, looked up once per device: the kernels'
 // shared-memory size set, the error word's address.
-static cudaError_t device_setup(int **err) {
+template <int KD>
+static cudaError_t set_smem() {
     using namespace mixtc;
+    const cudaError_t e = cudaFuncSetAttribute(k_mix_tc<true, KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<KD>::SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(k_mix_tc<false, KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<KD>::SMEM);
+}
+static cudaError_t device_setup(int **err) {
     static std::atomic<int *> known[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && (*err = known[dev].load(std::memory_order_acquire))) return cudaSuccess;
-    if ((e = cudaFuncSetAttribute(k_mix_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(k_mix_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess ||
-        (e = cudaGetSymbolAddress(reinterpret_cast<void **>(err), g_error)) != cudaSuccess)
+    if ((e = set_smem<64>()) != cudaSuccess || (e = set_smem<128>()) != cudaSuccess ||
+        (e = cudaGetSymbolAddress(reinterpret_cast<void **>(err), mixtc::g_error)) != cudaSuccess)
         return e;
     if (dev < 64) known[dev].store(*err, std::memory_order_release);
     return cudaSuccess;
 }
 
-cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
+template <bool SO>
+static cudaError_t launch_pass(mixtc::Batch &P, int kd, cudaStream_t s) {
     using namespace mixtc;
-    if (n < 1 || n > MAXP) return cudaErrorInvalidValue;
-    Batch P;
-    P.n = n;
-    cudaError_t e = device_setup(&P.err);
-    if (e != cudaSuccess) return e;
-    bool split = false;
-    for (int i = 0; i < n; i++) {
-        const MixArgs &a = g[i];
-        if (!rows_map(&P.ma[i], a.a, a.da, a.H / a.ra, a.T, a.Bt, a.lda, Q) ||
-            !rows_map(&P.mb[i], a.b, a.da, a.H / a.rb, a.T, a.Bt, a.ldb, Q) ||
-            !rows_map(&P.mc[i], a.c, a.dc, a.H / a.rc, a.T, a.Bt, a.ldc, Q))
-            return cudaErrorInvalidValue;
-        if (a.y && !a.y_f32 && !rows_map(&P.my[i], a.y, a.dc, a.H, a.T, a.Bt, a.H * a.dc, 16)) return cudaErrorInvalidValue;
-        P.g[i] = a;
-        split |= a.nseg > 1;
-    }
-    if (split) {
-        unsigned k = 0;
-        for (int i = 0; i < n; i++) {
-            P.first[i] = k;
-            k += (unsigned)(g[i].Bt * g[i].H * (g[i].nseg - 1) * ((g[i].dc + DC - 1) / DC));
-        }
-        P.first[n] = k;
-        k_mix_tc<true><<<k, THREADS, SMEM, s>>>(P);
-        count_launch();
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        for (int i = 0; i < n; i++)
-            if (g[i].nseg > 1 && (e = launch_mix_combine(g[i], s)) != cudaSuccess) return e;
-    }
     unsigned k = 0;
-    for (int i = 0; i < n; i++) {
+    for (int i = 0; i < P.n; i++) {
         P.first[i] = k;
-        k += (unsigned)(g[i].Bt * g[i].H * g[i].nseg * ((g[i].dc + DC - 1) / DC));
+        k += (unsigned)(P.g[i].Bt * P.g[i].H * (P.g[i].nseg - (SO ? 1 : 0)) * ((P.g[i].dc + DC - 1) / DC));
     }
-    P.first[n] = k;
-    k_mix_tc<false><<<k, THREADS, SMEM, s>>>(P);
+    P.first[P.n] = k;
+    if (kd == 64) k_mix_tc<SO, 64><<<k, THREADS, Lay<64>::SMEM, s>>>(P);
+    else k_mix_tc<SO, 128><<<k, THREADS, Lay<128>::SMEM, s>>>(P);
     count_launch();
     return cudaGetLastError();
+}
+
+cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
+    using namespace mixtc;
+    Batch P;
+    cudaError_t e = device_setup(&P.err);
+    if (e != cudaSuccess) return e;
+    for (int kd : {64, 128}) {
+        P.n = 0;
+        bool split = false;
+        for (int i = 0; i < n; i++) {
+            const MixArgs &a = g[i];
+            if (padded(a) != kd) continue;
+            if (P.n == MAXP) return cudaErrorInvalidValue;
+            const int k = P.n++;
+            if (!rows_map(&P.ma[k], a.a, a.da, a.H / a.ra, a.T, a.Bt, a.lda, Q) ||
+                !rows_map(&P.mb[k], a.b, a.da, a.H / a.rb, a.T, a.Bt, a.ldb, Q) ||
+                !rows_map(&P.mc[k], a.c, a.dc, a.H / a.rc, a.T, a.Bt, a.ldc, Q) ||
+                (a.y && !a.y_f32 && !rows_map(&P.my[k], a.y, a.dc, a.H, a.T, a.Bt, a.H * a.dc, 16)))
+                return cudaErrorInvalidValue;
+            P.g[k] = a;
+            split |= a.nseg > 1;
+        }
+        if (P.n == 0) continue;
+        if (split) {
+            if ((e = launch_pass<true>(P, kd, s)) != cudaSuccess) return e;
+            for (int i = 0; i < P.n; i++)
+                if (P.g[i].nseg > 1 && (e = launch_mix_combine(P.g[i], s)) != cudaSuccess) return e;
+        }
+        if ((e = launch_pass<false>(P, kd, s)) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 int mix_tc_error_and_clear(cudaStream_t s) {

@@ -67,16 +67,14 @@ __device__ __forceinline__ int64_t lane_length(const int32_t *lengths, int64_t b
     const int64_t n = lengths[b];
     return n < 0 ? 0 : (n > T ? T : n);
 }
-// g^n and g^n - 1 for whole n >= 0, from 64 bits: the powers are needed to
-// full fp32 accuracy, and a state multiplied by g^n must not inherit the
-// rounding of a g near 1 (it is updated as M + M (g^n - 1)).  g^0 is 1 for a
-// decay of zero too (log_decay = -inf).
-__device__ __forceinline__ float decay_pow(double lg, int64_t n) { return n == 0 ? 1.f : (float)exp(lg * (double)n); }
+// g^n - 1 for whole n >= 0, from 64 bits.  A state multiplied by g^n must not
+// inherit the rounding of a g^n near 1: it is updated as M + M (g^n - 1).  g^0
+// is 1 for a decay of zero too (log_decay = -inf).
 __device__ __forceinline__ float decay_pow_m1(double lg, int64_t n) {
     return n == 0 ? 0.f : (float)expm1(lg * (double)n);
 }
 
-// The same from fp32 arithmetic for n <= 64, within a few roundings: the
+// g^n and g^n - 1 from fp32 arithmetic for n <= 64, within a few roundings: the
 // product's own rounding is put back in (its derivative is the power itself).
 // (A double exp is 2 KB of code that every CTA of a short kernel waits for.)
 __device__ __forceinline__ void decay_pow_f32(float lg, int n, float &p, float &pm1) {
