@@ -215,16 +215,36 @@ __global__ void __launch_bounds__(256) k_mix_combine(MixArgs g) {
 }
 
 // out[row, group, :] = sum over the group's heads of in[row, head, :], in
-// fp32 and a fixed order, rounded once.  Bound by reading `in`.
-template <typename T>
-__global__ void __launch_bounds__(256) k_head_sum(const float *in, T *out, int64_t n, int rep, int64_t d) {
+// fp32 and a fixed order, rounded once; one or two tensors (blockIdx.y).  Bound
+// by reading `in`: VEC elements a thread, a head's loads in flight together.
+struct HeadSum {
+    const float *in[2];
+    void *out[2];
+    int64_t n;                                            // vectors of an output
+    int rep, d;
+};
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) k_head_sum(HeadSum a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    const int64_t e = i % d, rg = i / d;
-    const float *p = in + rg * rep * d + e;
-    float s = 0.f;
-    for (int r = 0; r < rep; r++) s += p[r * d];
-    stf(out, i, s);
+    if (i >= a.n) return;
+    const int64_t rg = i * VEC / a.d;
+    const int e = (int)(i * VEC - rg * a.d);
+    const float *p = a.in[blockIdx.y] + rg * a.rep * a.d + e;
+    float s[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; k++) s[k] = 0.f;
+#pragma unroll 4
+    for (int r = 0; r < a.rep; r++, p += a.d) {
+        if (VEC == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p);
+            s[0] += v.x; s[VEC - 3] += v.y; s[VEC - 2] += v.z; s[VEC - 1] += v.w;
+        } else {
+            s[0] += p[0];
+        }
+    }
+    T *o = static_cast<T *>(a.out[blockIdx.y]) + i * VEC;
+#pragma unroll
+    for (int k = 0; k < VEC; k++) stf(o, k, s[k]);
 }
 
 // -------------------------------------------------------------- k_lin_step
@@ -364,15 +384,26 @@ cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_head_sum(const float *in, void *out, m3_dtype dt, int64_t rows, int64_t H, int64_t G, int64_t d,
-                            cudaStream_t s) {
-    const int64_t n = rows * G * d;
-    if (n == 0) return cudaSuccess;
-    const unsigned blocks = (unsigned)((n + 255) / 256);
-    if (dt == M3_BF16)
-        k_head_sum<__nv_bfloat16><<<blocks, 256, 0, s>>>(in, static_cast<__nv_bfloat16 *>(out), n, (int)(H / G), d);
-    else
-        k_head_sum<float><<<blocks, 256, 0, s>>>(in, static_cast<float *>(out), n, (int)(H / G), d);
+cudaError_t launch_head_sum(const float *const in[2], void *const out[2], int count, m3_dtype dt, int64_t rows, int64_t H,
+                            int64_t G, int64_t d, cudaStream_t s) {
+    const bool v4 = d % 4 == 0;
+    HeadSum a;
+    for (int i = 0; i < 2; i++) {
+        a.in[i] = in[i];
+        a.out[i] = out[i];
+    }
+    a.n = rows * G * d / (v4 ? 4 : 1);
+    a.rep = (int)(H / G);
+    a.d = (int)d;
+    if (a.n == 0) return cudaSuccess;
+    const dim3 grid((unsigned)((a.n + 255) / 256), count);
+    if (dt == M3_BF16) {
+        if (v4) k_head_sum<__nv_bfloat16, 4><<<grid, 256, 0, s>>>(a);
+        else k_head_sum<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(a);
+    } else {
+        if (v4) k_head_sum<float, 4><<<grid, 256, 0, s>>>(a);
+        else k_head_sum<float, 1><<<grid, 256, 0, s>>>(a);
+    }
     count_launch();
     return cudaGetLastError();
 }

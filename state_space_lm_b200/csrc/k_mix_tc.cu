@@ -759,11 +759,13 @@ bool mix_tc_sizes(const MixArgs &g, m3_dtype dt) {
 static int padded(const MixArgs &g) { return g.da <= 64 ? 64 : 128; }
 
 // Segments of the problems of one launch (those padded to the same width; the
-// same count for all).  A CTA
-// holds an SM, so k CTAs take ceil(k / 148) waves of (chunks of a segment);
-// the state pass over the leading segments costs about 0.6 of a full chunk per
-// chunk.  The count with the least time in those units, at least 4 chunks a
-// segment, at most 64 segments and 64 MB of states.
+// same count for all).  A CTA holds an SM, so k CTAs take ceil(k / 148) waves.
+// A wave takes its chunks and about 4 chunks' time more (set-up, the first
+// loads, the last chunk's way through the roles: 5 us); the state pass over
+// the leading segments takes half a chunk's time per chunk.  The count with the
+// least time in those units, at least 4 chunks a segment, at most 64 segments
+// and 64 MB of states.  (1 x 32768 tokens, 32 heads: 357 us with 32 segments,
+// which a rule without the fixed part takes.)
 static void plan_width(MixArgs *g, int n, int kd) {
     using namespace mixtc;
     const int64_t nq = (g[0].T + Q - 1) / Q;
@@ -778,13 +780,13 @@ static void plan_width(MixArgs *g, int n, int kd) {
     if (ctas == 0 || ctas >= 148 || nq < 8) return;
     const int64_t most = ((int64_t)64 << 20) / state;
     auto waves = [](int64_t k) { return (k + 147) / 148; };
-    double best = (double)waves(ctas) * (double)nq;
+    double best = (double)waves(ctas) * (double)(nq + 4);
     for (int64_t ns = 2; ns <= 64; ns++) {
         const int64_t len = (nq + ns - 1) / ns;
         if (len < 4) break;
         const int64_t k = (nq + len - 1) / len;
         if (k < 2 || k - 1 > most) continue;
-        const double cost = ((double)waves(ctas * k) + 0.6 * (double)waves(ctas * (k - 1))) * (double)len;
+        const double cost = (double)waves(ctas * k) * (double)(len + 4) + (double)waves(ctas * (k - 1)) * (0.5 * (double)len + 4);
         if (cost < best - 1e-9) {
             best = cost;
             for (int i = 0; i < n; i++)

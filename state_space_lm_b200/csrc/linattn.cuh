@@ -98,9 +98,9 @@ cudaError_t launch_mix_tc(const MixArgs *a, int n, cudaStream_t s);
 int mix_tc_error_and_clear(cudaStream_t s);
 // chains the segments' states between the two passes
 cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s);
-// sums an fp32 (Bt, T, H, d) tensor over the heads of each of G groups
-cudaError_t launch_head_sum(const float *in, void *out, m3_dtype dt, int64_t rows, int64_t H, int64_t G, int64_t d,
-                            cudaStream_t s);
+// sums one or two fp32 (Bt, T, H, d) tensors over the heads of each of G groups
+cudaError_t launch_head_sum(const float *const in[2], void *const out[2], int count, m3_dtype dt, int64_t rows, int64_t H,
+                            int64_t G, int64_t d, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinStepArgs &a, m3_dtype dt, cudaStream_t s);
 
 }  // namespace m3

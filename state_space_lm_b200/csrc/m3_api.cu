@@ -613,7 +613,8 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
     const size_t hb = head_bytes(d, o);
     const bool shared = hb > 0;
     char *heads = static_cast<char *>(workspace) + p.bytes;
-    struct { const void *in; void *out; } sums[2] = {};
+    const float *sum_in[2] = {};
+    void *sum_out[2] = {};
     int ns = 0;
     auto fill = [&](int i, const void *a, const void *b, const void *c, const float *m0, void *y) -> MixArgs & {
         MixArgs &m = p.m[i];
@@ -629,9 +630,9 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
     };
     auto summed = [&](void *out) -> void * {
         if (!shared) return out;
-        void *in = heads + ns * hb;
-        sums[ns].in = in;
-        sums[ns++].out = out;
+        float *in = reinterpret_cast<float *>(heads + ns * hb);
+        sum_in[ns] = in;
+        sum_out[ns++] = out;
         return in;
     };
     if (want[0]) fill(0, dy, v, k, s0, summed(g.dq));
@@ -646,9 +647,8 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
     const cudaStream_t s = (cudaStream_t)stream;
     return launch_unless_injected([&]() -> cudaError_t {
         cudaError_t e = launch_mixes(p, dtype, workspace, s);
-        for (int j = 0; j < ns && e == cudaSuccess; j++)
-            e = launch_head_sum(static_cast<const float *>(sums[j].in), sums[j].out, dtype, d.batch * d.seqlen,
-                                d.nheads, o.G, d.dstate, s);
+        if (e == cudaSuccess && ns > 0)
+            e = launch_head_sum(sum_in, sum_out, ns, dtype, d.batch * d.seqlen, d.nheads, o.G, d.dstate, s);
         return e;
     });
 }
