@@ -10,6 +10,7 @@
 // over many tokens, or wide groups): a pass for the sums, a pass that applies
 // them; the second read of x comes from L2 while the tensors fit there.
 #include "group_norm.cuh"
+#include "launch.cuh"
 
 namespace m3 {
 namespace {
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
 template <typename T, int VEC, int NV, int ACT, bool GATE>
 __global__ void __launch_bounds__(RT) k_gn_row_bwd(GnArgs a, int tw, int fold) {
     constexpr bool FAST = sizeof(T) == 2;
+    pdl_trigger();
     extern __shared__ float part[];                       // 2 C sums, when the block folds its slots
     __shared__ float2 sh[RT / 32];
     struct { int slot, g, lane_in, nslots; bool on; } r;
@@ -444,6 +446,7 @@ __device__ __forceinline__ void reduce_rows(const float *part, int64_t n, int64_
 }
 
 __global__ void __launch_bounds__(1024) k_gn_reduce(const float *part, int64_t n, int64_t C, float *dw, float *db) {
+    pdl_wait();
     reduce_rows(part, n, C, dw, db, blockIdx.x);
 }
 
@@ -488,6 +491,7 @@ __device__ __forceinline__ SeqGeo seq_geo(const GnArgs &a, int vec, int rows, in
 // of a group are merged by the pairwise update of means.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(SQT, 2) k_gn_seq_stats(GnArgs a, int rows, int nch) {
+    pdl_trigger();
     extern __shared__ float2 vstat[];                     // (np, nvec) pairs (mean, M2)
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
     const T *x = static_cast<const T *>(a.x) + s.base;
@@ -579,6 +583,7 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_apply(GnArgs a, int rows, int
         // thread = (group of 32, every eighth chunk): sums of n d and of M2 + n d^2,
         // d from the first chunk's mean, so that nothing of size mean^2 cancels
         __shared__ float2 sh[8][32];
+        pdl_wait();
         const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
         const float D = (float)(a.C / a.G), n = (float)a.L * D;
         const float nfull = (float)rows * D, nlast = (float)((int)a.L - (nch - 1) * rows) * D;
@@ -673,6 +678,7 @@ __device__ __forceinline__ float gn_du(float x, float dy, float z, float2 st, fl
 template <typename T, int VEC, int ACT, bool GATE>
 __global__ void __launch_bounds__(SQT, 2) k_gn_seq_bsums(GnArgs a, int rows, int nch) {
     constexpr bool FAST = sizeof(T) == 2;
+    pdl_trigger();
     extern __shared__ float psum[];                       // (np - 1, 2, C): the other phases' sums
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
     float *out = a.ws + (size_t)blockIdx.x * 2 * a.C;
@@ -740,6 +746,8 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_bsums(GnArgs a, int rows, int
 __global__ void __launch_bounds__(256) k_gn_seq_moments(GnArgs a, int nch, float *sums, float2 *mom) {
     __shared__ float sh[2][8][32];
     __shared__ float red[2];
+    pdl_trigger();
+    pdl_wait();
     const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
     const int bi = (int)(blockIdx.x / (unsigned)a.G), g = (int)blockIdx.x - bi * (int)a.G;
     const int D = (int)((unsigned)a.C / (unsigned)a.G);
@@ -784,6 +792,7 @@ template <typename T, int VEC, int ACT, bool GATE>
 __global__ void __launch_bounds__(SQT, 2) k_gn_seq_dx(GnArgs a, int rows, int nch, const float *sums,
                                                    const float2 *mom, unsigned dx_blocks) {
     constexpr bool FAST = sizeof(T) == 2;
+    pdl_wait();
     if (blockIdx.x >= dx_blocks) {
         reduce_rows(sums, a.Bt, a.C, a.dw, a.db, blockIdx.x - dx_blocks);
         return;
@@ -898,21 +907,21 @@ Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd)
 
 // the (activation, gate) variant of a kernel template: without vectors the
 // activation is a run-time choice (a quarter of the variants)
-#define GN_ACTS(K, T, VEC, NV, ...)                                                   \
-    if constexpr (VEC == 1) {                                                                 \
-        if (a.gate) K<T, 1 NV, ACT_ANY, true> __VA_ARGS__;                            \
-        else K<T, 1 NV, ACT_ANY, false> __VA_ARGS__;                                  \
+#define GN_ACTS(CALL, K, T, VEC, NV)                                                  \
+    if constexpr (VEC == 1) {                                                         \
+        if (a.gate) { CALL((K<T, 1 NV, ACT_ANY, true>)); }                            \
+        else { CALL((K<T, 1 NV, ACT_ANY, false>)); }                                  \
     } else {                                                                          \
         constexpr int V = VEC == 1 ? (sizeof(T) == 2 ? 8 : 4) : VEC;                  \
         switch (a.act * 2 + (a.gate ? 1 : 0)) {                                       \
-            case 0: K<T, V NV, ACT_NONE, false> __VA_ARGS__; break;                   \
-            case 1: K<T, V NV, ACT_NONE, true> __VA_ARGS__; break;                    \
-            case 2: K<T, V NV, ACT_SILU, false> __VA_ARGS__; break;                   \
-            case 3: K<T, V NV, ACT_SILU, true> __VA_ARGS__; break;                    \
-            case 4: K<T, V NV, ACT_GELU, false> __VA_ARGS__; break;                   \
-            case 5: K<T, V NV, ACT_GELU, true> __VA_ARGS__; break;                    \
-            case 6: K<T, V NV, ACT_RELU, false> __VA_ARGS__; break;                   \
-            default: K<T, V NV, ACT_RELU, true> __VA_ARGS__; break;                   \
+            case 0: CALL((K<T, V NV, ACT_NONE, false>)); break;                       \
+            case 1: CALL((K<T, V NV, ACT_NONE, true>)); break;                        \
+            case 2: CALL((K<T, V NV, ACT_SILU, false>)); break;                       \
+            case 3: CALL((K<T, V NV, ACT_SILU, true>)); break;                        \
+            case 4: CALL((K<T, V NV, ACT_GELU, false>)); break;                       \
+            case 5: CALL((K<T, V NV, ACT_GELU, true>)); break;                        \
+            case 6: CALL((K<T, V NV, ACT_RELU, false>)); break;                       \
+            default: CALL((K<T, V NV, ACT_RELU, true>)); break;                       \
         }                                                                             \
     }
 #define GN_COMMA_NV(n) , n
@@ -921,9 +930,13 @@ template <typename T, int VEC, int NV>
 cudaError_t row_launch(const GnArgs &a, const Plan &p, bool bwd, cudaStream_t s) {
     if (bwd) {
         const int smem = p.fold ? (int)(2 * a.C * sizeof(float)) : 0;      // C <= 4096 there
-        GN_ACTS(k_gn_row_bwd, T, VEC, GN_COMMA_NV(NV), <<<p.blocks, RT, smem, s>>>(a, p.tw, p.fold))
+#define GN_CALL(K) K<<<p.blocks, RT, smem, s>>>(a, p.tw, p.fold)
+        GN_ACTS(GN_CALL, k_gn_row_bwd, T, VEC, GN_COMMA_NV(NV))
+#undef GN_CALL
     } else {
-        GN_ACTS(k_gn_row_fwd, T, VEC, GN_COMMA_NV(NV), <<<p.blocks, RT, 0, s>>>(a, p.tw))
+#define GN_CALL(K) K<<<p.blocks, RT, 0, s>>>(a, p.tw)
+        GN_ACTS(GN_CALL, k_gn_row_fwd, T, VEC, GN_COMMA_NV(NV))
+#undef GN_CALL
     }
     count_launch();
     return cudaGetLastError();
@@ -963,20 +976,15 @@ cudaError_t seq_fwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
     k_gn_seq_stats<T, VEC><<<blocks, SQT, smem, s>>>(a, (int)p.rows, (int)p.nch);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int gsm = (int)(a.G * sizeof(float2));
-#define GN_APPLY_SMEM(T, V, A, Z)                                                                          \
-    if (gsm > 48 * 1024 &&                                                                                 \
-        (e = cudaFuncSetAttribute(k_gn_seq_apply<T, V, A, Z>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
-                                  gsm)) != cudaSuccess)                                                    \
-        return e;
-    if (VEC == 1) {                                       // G > 6144 only without vectors
-        if (a.gate) { GN_APPLY_SMEM(T, 1, ACT_ANY, true) }
-        else { GN_APPLY_SMEM(T, 1, ACT_ANY, false) }
-    }
-#undef GN_APPLY_SMEM
-    GN_ACTS(k_gn_seq_apply, T, VEC, , <<<blocks, SQT, gsm, s>>>(a, (int)p.rows, (int)p.nch))
-    count_launch();
-    return cudaGetLastError();
+    const int gsm = (int)(a.G * sizeof(float2));          // above 48 KB only without vectors (G > 6144)
+#define GN_CALL(K)                                                                                               \
+    if (gsm > 48 * 1024 &&                                                                                       \
+        (e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, gsm)) != cudaSuccess)          \
+        return e;                                                                                                \
+    e = launch_after(K, dim3(blocks), SQT, gsm, s, a, (int)p.rows, (int)p.nch)
+    GN_ACTS(GN_CALL, k_gn_seq_apply, T, VEC, )
+#undef GN_CALL
+    return e;
 }
 
 template <typename T, int VEC>
@@ -984,19 +992,22 @@ cudaError_t seq_bwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
     const unsigned blocks = (unsigned)(a.Bt * p.nch);
     const int smem = (int)((seq_phases(a.C, VEC) - 1) * 2 * a.C * sizeof(float));   // below 16 KB: np C / VEC <= 256
     cudaError_t e;
-    GN_ACTS(k_gn_seq_bsums, T, VEC, , <<<blocks, SQT, smem, s>>>(a, (int)p.rows, (int)p.nch))
+#define GN_CALL(K) K<<<blocks, SQT, smem, s>>>(a, (int)p.rows, (int)p.nch)
+    GN_ACTS(GN_CALL, k_gn_seq_bsums, T, VEC, )
+#undef GN_CALL
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     float *sums = a.ws + (size_t)a.Bt * p.nch * 2 * a.C;
     float2 *mom = reinterpret_cast<float2 *>(sums + (size_t)a.Bt * 2 * a.C);
-    k_gn_seq_moments<<<(unsigned)(a.Bt * a.G), 256, 0, s>>>(a, (int)p.nch, sums, mom);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(k_gn_seq_moments, dim3((unsigned)(a.Bt * a.G)), 256, 0, s, a, (int)p.nch, sums, mom)) !=
+        cudaSuccess)
+        return e;
     const unsigned dxb = a.dx ? blocks : 0, rb = (a.dw || a.db) ? (unsigned)ceil_div(2 * a.C, 32) : 0;
     if (dxb + rb == 0) return cudaSuccess;
-    GN_ACTS(k_gn_seq_dx, T, VEC, , <<<dxb + rb, SQT, 0, s>>>(a, (int)p.rows, (int)p.nch, sums, mom, dxb))
-    count_launch();
-    return cudaGetLastError();
+#define GN_CALL(K) e = launch_after(K, dim3(dxb + rb), SQT, 0, s, a, (int)p.rows, (int)p.nch, sums, mom, dxb)
+    GN_ACTS(GN_CALL, k_gn_seq_dx, T, VEC, )
+#undef GN_CALL
+    return e;
 }
 
 }  // namespace
@@ -1031,9 +1042,7 @@ cudaError_t launch_gn_bwd(const GnArgs &a, m3_dtype dt, cudaStream_t s) {
         cudaError_t e =
             dt == M3_BF16 ? row_dispatch<__nv_bfloat16, 8>(a, p, true, s) : row_dispatch<float, 4>(a, p, true, s);
         if (e != cudaSuccess || !(a.dw || a.db)) return e;
-        k_gn_reduce<<<(unsigned)ceil_div(2 * a.C, 32), 1024, 0, s>>>(a.ws, p.parts, a.C, a.dw, a.db);
-        count_launch();
-        return cudaGetLastError();
+        return launch_after(k_gn_reduce, dim3((unsigned)ceil_div(2 * a.C, 32)), 1024, 0, s, a.ws, p.parts, a.C, a.dw, a.db);
     }
     if (dt == M3_BF16) return p.vec == 8 ? seq_bwd<__nv_bfloat16, 8>(a, p, s) : seq_bwd<__nv_bfloat16, 1>(a, p, s);
     return p.vec == 4 ? seq_bwd<float, 4>(a, p, s) : seq_bwd<float, 1>(a, p, s);

@@ -1,6 +1,7 @@
 // k_linattn.cu -- linear attention with a decay for each head: the fp32
 // kernel for every size and type, the combine of a split time axis, the sum
 // of per-head gradients over shared heads, and the single-token step.
+#include "launch.cuh"
 #include "linattn.cuh"
 
 namespace m3 {
@@ -226,6 +227,7 @@ struct HeadSum {
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) k_head_sum(HeadSum a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    pdl_wait();
     if (i >= a.n) return;
     const int64_t rg = i * VEC / a.d;
     const int e = (int)(i * VEC - rg * a.d);
@@ -397,15 +399,10 @@ cudaError_t launch_head_sum(const float *const in[2], void *const out[2], int co
     a.d = (int)d;
     if (a.n == 0) return cudaSuccess;
     const dim3 grid((unsigned)((a.n + 255) / 256), count);
-    if (dt == M3_BF16) {
-        if (v4) k_head_sum<__nv_bfloat16, 4><<<grid, 256, 0, s>>>(a);
-        else k_head_sum<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(a);
-    } else {
-        if (v4) k_head_sum<float, 4><<<grid, 256, 0, s>>>(a);
-        else k_head_sum<float, 1><<<grid, 256, 0, s>>>(a);
-    }
-    count_launch();
-    return cudaGetLastError();
+    if (dt == M3_BF16)
+        return v4 ? launch_after(k_head_sum<__nv_bfloat16, 4>, grid, 256, 0, s, a)
+                  : launch_after(k_head_sum<__nv_bfloat16, 1>, grid, 256, 0, s, a);
+    return v4 ? launch_after(k_head_sum<float, 4>, grid, 256, 0, s, a) : launch_after(k_head_sum<float, 1>, grid, 256, 0, s, a);
 }
 
 cudaError_t launch_linattn_step(const LinStepArgs &a, m3_dtype dt, cudaStream_t s) {
