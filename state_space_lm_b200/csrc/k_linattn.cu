@@ -355,7 +355,7 @@ cudaError_t launch_mix_simt_d(const MixArgs &a, cudaStream_t s) {
 }  // namespace
 
 // Split the time axis when the lanes' column tiles leave SMs idle: enough
-// segments for about four CTAs per SM, at least 64 tokens each (a segment
+// segments for about four CTAs per SM, at least 32 tokens each (a segment
 // costs a state written and read, and its tokens' b and c twice), at most 64
 // segments and 64 MB of states.  (3 x 333 tokens, 5 heads of 37 x 29, fp32:
 // 64 us in one piece of each lane, 31 us in five.)
@@ -363,9 +363,9 @@ void mix_simt_plan(MixArgs &a) {
     a.nseg = 1;
     a.seg_len = a.T > 0 ? a.T : 1;
     const int64_t lanes = a.Bt * a.H, ctas = lanes * ((a.dc + SP - 1) / SP);
-    if (lanes == 0 || ctas >= 296 || a.T < 192) return;
+    if (lanes == 0 || ctas >= 296 || a.T < 96) return;
     int64_t ns = 592 / ctas;
-    if (ns > a.T / 64) ns = a.T / 64;
+    if (ns > a.T / 32) ns = a.T / 32;
     if (ns > 64) ns = 64;
     const int64_t most = ((int64_t)64 << 20) / (lanes * a.da * a.dc * 4) + 1;
     if (ns > most) ns = most;
