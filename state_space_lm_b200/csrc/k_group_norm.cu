@@ -57,6 +57,29 @@ __device__ __forceinline__ float act_only(float u, int act) {
     return f;
 }
 
+// fma of two values in one instruction (register pairs)
+__device__ __forceinline__ void fma_pair(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+// o = a * b + c over VEC values; b and c may be one value each
+template <int VEC>
+__device__ __forceinline__ void fmav(float *o, const float *a, const float *b, const float *c) {
+    if (VEC == 1) o[0] = fmaf(a[0], b[0], c[0]);
+    else
+#pragma unroll
+        for (int i = 0; i + 1 < VEC; i += 2) fma_pair(o[i], o[i + 1], a[i], a[i + 1], b[i], b[i + 1], c[i], c[i + 1]);
+}
+template <int VEC>
+__device__ __forceinline__ void fmav(float *o, const float *a, float b, float c) {
+    if (VEC == 1) o[0] = fmaf(a[0], b, c);
+    else
+#pragma unroll
+        for (int i = 0; i + 1 < VEC; i += 2) fma_pair(o[i], o[i + 1], a[i], a[i + 1], b, b, c, c);
+}
+
 // VEC consecutive elements as they lie in memory: loaded early, unpacked late.
 template <typename T, int VEC>
 struct Raw {
@@ -227,8 +250,10 @@ __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
 #pragma unroll
                 for (int e = 0; e < VEC; e++) x[u][m][e] = 0.f;
             }
+            float t[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < VEC; e++) s += x[u][m][e];
+            for (int e = 0; e < VEC; e++) t[e & 1] += x[u][m][e];
+            s += t[0] + t[1];
         }
         mean[u] = s;
     }
@@ -239,11 +264,17 @@ __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
         float q = 0.f;
 #pragma unroll
         for (int m = 0; m < NV; m++) {
-            const bool in = m * tw + li < nvec;
+            fmav<VEC>(x[u][m], x[u][m], 1.f, -mean[u]);
+            if (m * tw + li < nvec) {
+                if (VEC == 1) {
+                    q = fmaf(x[u][m][0], x[u][m][0], q);
+                } else {
+                    float t0 = 0.f, t1 = 0.f;
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                x[u][m][e] -= mean[u];
-                if (in) q = fmaf(x[u][m][e], x[u][m][e], q);
+                    for (int e = 0; e + 1 < VEC; e += 2)
+                        fma_pair(t0, t1, x[u][m][e], x[u][m][e + 1], x[u][m][e], x[u][m][e + 1], t0, t1);
+                    q += t0 + t1;
+                }
             }
         }
         rstd[u] = q;
@@ -261,19 +292,23 @@ __global__ void __launch_bounds__(RT) k_gn_row_fwd(GnArgs a, int tw) {
         const int v = m * tw + li;
         if (v < nvec) {
             float w[VEC], b[VEC], zf[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                w[e] = 1.f;
+                b[e] = 0.f;
+            }
             if (a.w) ldv<VEC>(a.w + g * D + v * VEC, w);
             if (a.b) ldv<VEC>(a.b + g * D + v * VEC, b);
 #pragma unroll
             for (int u = 0; u < R; u++) {
                 if (row0 + u >= (unsigned)a.Bt) continue;
                 if (GATE) z[u][m].get(zf);
+                fmav<VEC>(x[u][m], x[u][m], rstd[u], 0.f);
+                fmav<VEC>(x[u][m], x[u][m], w, b);
 #pragma unroll
-                for (int e = 0; e < VEC; e++) {
-                    float n = x[u][m][e] * rstd[u];
-                    if (a.w) n *= w[e];
-                    if (a.b) n += b[e];
-                    x[u][m][e] = GATE ? n * act_only<ACT, FAST>(zf[e], a.act) : act_only<ACT, FAST>(n, a.act);
-                }
+                for (int e = 0; e < VEC; e++)
+                    x[u][m][e] = GATE ? x[u][m][e] * act_only<ACT, FAST>(zf[e], a.act)
+                                      : act_only<ACT, FAST>(x[u][m][e], a.act);
                 stv<VEC>(static_cast<T *>(a.y) + base + u * a.C + v * VEC, x[u][m]);
             }
         }
@@ -579,6 +614,22 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_apply(GnArgs a, int rows, int
     constexpr bool FAST = sizeof(T) == 2;
     extern __shared__ float2 gstat[];                     // G pairs (mean, rstd)
     const SeqGeo s = seq_geo(a, VEC, rows, nch);
+    // U tokens' loads go out together (y may be anywhere: the compiler keeps
+    // loads behind stores), the first of them before the merge
+    constexpr int U = GATE ? 4 : 8;
+    Raw<T, VEC> xr[U], zr[U];
+    const int64_t step = s.np * a.C;
+    auto fetch = [&](int t, int64_t o) {
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (t + u * s.np < s.t1) {
+                xr[u].load(static_cast<const T *>(a.x) + o + u * step);
+                if (GATE) zr[u].load(static_cast<const T *>(a.gate) + o + u * step);
+            }
+    };
+    const int64_t o0 = s.base + (int64_t)(s.t0 + s.ph) * a.C;
+    bool ready = s.v0 < s.nvec;
+    if (ready) fetch(s.t0 + s.ph, o0 + s.v0 * VEC);
     {
         // thread = (group of 32, every eighth chunk): sums of n d and of M2 + n d^2,
         // d from the first chunk's mean, so that nothing of size mean^2 cancels
@@ -624,33 +675,24 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_apply(GnArgs a, int rows, int
         float w[VEC], b[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; e++) {
-            w[e] = a.w ? a.w[v * VEC + e] : 1.f;
+            w[e] = (a.w ? a.w[v * VEC + e] : 1.f) * st.y;
             b[e] = a.b ? a.b[v * VEC + e] : 0.f;
         }
-        int64_t o = s.base + (int64_t)(s.t0 + s.ph) * a.C + v * VEC;
-        const int64_t step = s.np * a.C;
-        // four tokens' loads go out together (y may be anywhere: the compiler
-        // keeps loads behind stores)
-        constexpr int U = 4;
+        int64_t o = o0 + v * VEC;
         for (int t = s.t0 + s.ph; t < s.t1; t += U * s.np, o += U * step) {
-            Raw<T, VEC> xr[U], zr[U];
-#pragma unroll
-            for (int u = 0; u < U; u++)
-                if (t + u * s.np < s.t1) {
-                    xr[u].load(static_cast<const T *>(a.x) + o + u * step);
-                    if (GATE) zr[u].load(static_cast<const T *>(a.gate) + o + u * step);
-                }
+            if (!ready) fetch(t, o);
+            ready = false;
 #pragma unroll
             for (int u = 0; u < U; u++)
                 if (t + u * s.np < s.t1) {
                     float x[VEC], z[VEC];
                     xr[u].get(x);
                     if (GATE) zr[u].get(z);
+                    fmav<VEC>(x, x, 1.f, -st.x);          // the difference first: a large mean cancels nothing
+                    fmav<VEC>(x, x, w, b);
 #pragma unroll
-                    for (int e = 0; e < VEC; e++) {
-                        const float n = fmaf((x[e] - st.x) * st.y, w[e], b[e]);
-                        x[e] = GATE ? n * act_only<ACT, FAST>(z[e], a.act) : act_only<ACT, FAST>(n, a.act);
-                    }
+                    for (int e = 0; e < VEC; e++)
+                        x[e] = GATE ? x[e] * act_only<ACT, FAST>(z[e], a.act) : act_only<ACT, FAST>(x[e], a.act);
                     stv<VEC>(static_cast<T *>(a.y) + o + u * step, x);
                 }
         }

@@ -729,7 +729,7 @@ def linattn_chunked_bwd(q, k, v, log_decay, dy, scale=None, s0=None, ds_final=No
         else:
             out[n] = _like({"dq": q, "dk": k, "dv": v}[n]) if n != "ds0" else v.new_empty(shapes[n], dtype=io)
     ws, nbytes = _own_workspace(need, workspace, v)
-    g = LinattnGrads(*[_ptr(out.get(n)) for n in names])
+    g = LinattnGrads(*[_ptr(out[n]) if n in out else None for n in names])
     args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(dy), _ptr(ds_final),
             ctypes.byref(g), _ptr(ws), nbytes)
