@@ -8,6 +8,7 @@ names).  The initial states and the final states take part in autograd too,
 so a sequence can be split into pieces whose states are chained.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import m3
 
@@ -75,9 +76,11 @@ class LinearAttention(torch.autograd.Function):
         y, sf = m3.linattn_chunked_fwd(q, k, v, log_decay, scale=scale, s0=s0, lengths=lengths)
         ctx.save_for_backward(q, k, v, log_decay, s0, lengths)
         ctx.scale = scale
+        ctx.set_materialize_grads(False)
         return y, sf
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, ds):
         q, k, v, log_decay, s0, lengths = ctx.saved_tensors
         need = dict(zip(("dq", "dk", "dv"), ctx.needs_input_grad[:3]), ds0=ctx.needs_input_grad[5])
@@ -105,6 +108,7 @@ class GroupNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, bias, gate, mean, rstd = ctx.saved_tensors
         n = ctx.needs_input_grad

@@ -568,8 +568,14 @@ class _Device:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _run(fn, where, args, dev, stream):
-    """fn(*args, stream) on dev."""
+def _run(fn, where, args, dev, stream, made=()):
+    """fn(*args, stream) on dev.  made: tensors that this call allocated, on
+    the current stream; the allocator has to know of the caller's stream before
+    it gives their memory to someone else."""
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
     if stream is None and _raw_stream is not None and dev.index == torch.cuda.current_device():
         rc = fn(*args, _raw_stream(dev.index))
     else:
@@ -678,7 +684,8 @@ def linattn_chunked_fwd(q, k, v, log_decay, scale=None, s0=None, lengths=None, w
     args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(y), _ptr(sf),
             _ptr(ws), nbytes)
-    _run(lib().m3_linattn_chunked_fwd, w, args, dev, stream)
+    _run(lib().m3_linattn_chunked_fwd, w, args, dev, stream, (None if workspace is not None else ws,
+                                                              *((y, sf) if out is None else ())))
     return y, sf
 
 
@@ -696,7 +703,7 @@ def linattn_step_decode(q_t, k_t, v_t, log_decay, s, scale=None, y_out=None, str
         _expect(w, dev, "y_t", y, v_t.numel(), v_t.dtype)
     args = (_row_ptr(q_t), _row_ptr(k_t), _row_ptr(v_t), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), d, _ptr(s), _ptr(y))
-    _run(lib().m3_linattn_step_decode, w, args, dev, stream)
+    _run(lib().m3_linattn_step_decode, w, args, dev, stream, (y,) if y_out is None else ())
     return y
 
 
@@ -733,7 +740,8 @@ def linattn_chunked_bwd(q, k, v, log_decay, dy, scale=None, s0=None, ds_final=No
     args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(dy), _ptr(ds_final),
             ctypes.byref(g), _ptr(ws), nbytes)
-    _run(lib().m3_linattn_chunked_bwd, w, args, dev, stream)
+    _run(lib().m3_linattn_chunked_bwd, w, args, dev, stream, (None if workspace is not None else ws,
+                                                              *(t for n, t in out.items() if n not in pre)))
     return out
 
 
@@ -785,7 +793,8 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps
     ws, nbytes = _own_workspace(need, workspace, x)
     args = (_ptr(x), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], float(eps), d, _ptr(y), _ptr(mean),
             _ptr(rstd), _ptr(ws), nbytes)
-    _run(lib().m3_group_norm_fwd, w, args, dev, stream)
+    _run(lib().m3_group_norm_fwd, w, args, dev, stream, (None if workspace is not None else ws,
+                                                         *((y, mean, rstd) if out is None else ())))
     return y, mean, rstd
 
 
@@ -819,5 +828,6 @@ def group_norm_bwd(x, dy, mean, rstd, groups, weight=None, bias=None, gate=None,
     args = (_ptr(x), _ptr(dy), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], _ptr(mean), _ptr(rstd), d,
             _ptr(out.get("dx")), _ptr(out.get("dweight")), _ptr(out.get("dbias")), _ptr(out.get("dgate")), _ptr(ws),
             nbytes)
-    _run(lib().m3_group_norm_bwd, w, args, dev, stream)
+    _run(lib().m3_group_norm_bwd, w, args, dev, stream, (None if workspace is not None else ws,
+                                                         *(t for n, t in out.items() if n not in pre)))
     return out
