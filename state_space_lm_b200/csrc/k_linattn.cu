@@ -201,18 +201,43 @@ __global__ void __launch_bounds__(256) k_mix_combine(MixArgs g) {
     for (int j = threadIdx.x; j < g.nseg - 1; j += 256)
         dm1[j] = decay_pow_m1(lg, seg_tokens(j, g.nseg, g.seg_len, g.reverse, len));
     __syncthreads();
-    const size_t elems = (size_t)g.da * g.dc, i = (size_t)blockIdx.y * 256 + threadIdx.x;
+    const size_t elems = (size_t)g.dar * g.dcr, i = (size_t)blockIdx.y * 256 + threadIdx.x;
     if (i >= elems) return;
     float M = 0.f;
     if (g.m0) {
-        const size_t r = i / g.dc, p = i % g.dc;
-        M = g.m0[lane * elems + (g.m_trans ? p * g.da + r : i)];
+        const size_t r = i / g.dcr, p = i % g.dcr;
+        M = g.m0[lane * elems + (g.m_trans ? p * g.dar + r : i)];
     }
     float *sl = g.ws + (size_t)lane * (g.nseg - 1) * elems + i;
     for (int j = 0; j < g.nseg - 1; j++) {
         M = fmaf(M, dm1[j], M) + sl[j * elems];
         sl[j * elems] = M;
     }
+}
+
+// One thread, one 16-byte piece of a padded row.
+__global__ void __launch_bounds__(256) k_pad_rows(PadArgs a) {
+    const int k = blockIdx.y;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.n[k]) return;
+    const int d = a.d[k], w = (d + 7) / 8, heads = a.heads[k];
+    int64_t rh, row;
+    if (a.n[k] < (int64_t)1 << 31) {                      // 64-bit divisions would cost more than the copy
+        rh = (unsigned)i / (unsigned)w;
+        row = (unsigned)rh / (unsigned)heads;
+    } else {
+        rh = i / w;
+        row = rh / heads;
+    }
+    const int c = (int)(i - rh * w) * 8, h = (int)(rh - row * heads);
+    const uint16_t *p = static_cast<const uint16_t *>(a.src[k]) + row * a.ld[k] + (int64_t)h * d + c;
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const uint32_t lo = c + 2 * e < d ? p[2 * e] : 0, hi = c + 2 * e + 1 < d ? p[2 * e + 1] : 0;
+        o[e] = lo | hi << 16;
+    }
+    static_cast<uint4 *>(a.dst[k])[i] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // out[row, group, :] = sum over the group's heads of in[row, head, :], in
@@ -229,8 +254,9 @@ __global__ void __launch_bounds__(256) k_head_sum(HeadSum a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     pdl_wait();
     if (i >= a.n) return;
-    const int64_t rg = i * VEC / a.d;
-    const int e = (int)(i * VEC - rg * a.d);
+    const int w = a.d / VEC;                              // vectors of a row
+    const int64_t rg = a.n < (int64_t)1 << 31 ? (unsigned)i / (unsigned)w : i / w;
+    const int e = (int)(i - rg * w) * VEC;
     const float *p = a.in[blockIdx.y] + rg * a.rep * a.d + e;
     float s[VEC];
 #pragma unroll
@@ -381,7 +407,7 @@ cudaError_t launch_mix_simt(const MixArgs &a, m3_dtype dt, cudaStream_t s) {
 }
 
 cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s) {
-    k_mix_combine<<<dim3((unsigned)(a.Bt * a.H), (unsigned)((a.da * a.dc + 255) / 256)), 256, 0, s>>>(a);
+    k_mix_combine<<<dim3((unsigned)(a.Bt * a.H), (unsigned)((a.dar * a.dcr + 255) / 256)), 256, 0, s>>>(a);
     count_launch();
     return cudaGetLastError();
 }
@@ -403,6 +429,16 @@ cudaError_t launch_head_sum(const float *const in[2], void *const out[2], int co
         return v4 ? launch_after(k_head_sum<__nv_bfloat16, 4>, grid, 256, 0, s, a)
                   : launch_after(k_head_sum<__nv_bfloat16, 1>, grid, 256, 0, s, a);
     return v4 ? launch_after(k_head_sum<float, 4>, grid, 256, 0, s, a) : launch_after(k_head_sum<float, 1>, grid, 256, 0, s, a);
+}
+
+cudaError_t launch_pad_rows(const PadArgs &a, cudaStream_t s) {
+    int64_t most = 0;
+    for (int i = 0; i < a.count; i++)
+        if (a.n[i] > most) most = a.n[i];
+    if (most == 0) return cudaSuccess;
+    k_pad_rows<<<dim3((unsigned)((most + 255) / 256), a.count), 256, 0, s>>>(a);
+    count_launch();
+    return cudaGetLastError();
 }
 
 cudaError_t launch_linattn_step(const LinStepArgs &a, m3_dtype dt, cudaStream_t s) {

@@ -446,16 +446,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         // the tile's columns in pairs, fp32
         const int q = warp & 3, c0 = 32 * ((warp - W_ST) >> 2);
         const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + COL_D + c0;
-        const size_t elems = (size_t)g.da * g.dc;
+        const size_t elems = (size_t)g.dar * g.dcr;
         float *slots = g.ws + (size_t)lane * (g.nseg - 1) * elems;
         const int ra = 16 * q + (l32 >> 2), pc = p0 + c0 + 2 * (l32 & 3);
         f32x2 M[8];                                     // pair e: row ra + 8 (e & 1), columns 8 (e / 2) + 0, 1
         // where pair e lies in a state of global memory; a quad's four pairs
         // are 32 bytes of a row
-        auto inside = [&](int e) { return ra + 8 * (e & 1) < g.da && pc + 8 * (e >> 1) < g.dc; };
+        auto inside = [&](int e, int odd) { return ra + 8 * (e & 1) < g.dar && pc + 8 * (e >> 1) + odd < g.dcr; };
         auto at = [&](int e, int odd, bool tr) {
             const size_t n = ra + 8 * (e & 1), p = pc + 8 * (e >> 1) + odd;
-            return tr ? p * g.da + n : n * g.dc + p;
+            return tr ? p * g.dar + n : n * g.dcr + p;
         };
         {
             const float *src = (SO || (seg == 0 && !g.m0)) ? nullptr
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             const bool tr = seg == 0 && g.m_trans;
 #pragma unroll
             for (int e = 0; e < 8; e++)
-                M[e] = src && inside(e) ? pair(src[at(e, 0, tr)], src[at(e, 1, tr)]) : 0ull;
+                M[e] = pair(src && inside(e, 0) ? src[at(e, 0, tr)] : 0.f, src && inside(e, 1) ? src[at(e, 1, tr)] : 0.f);
         }
         const int mr = 16 * q + (l32 & 15), mc = l32 >> 4;
         uint32_t mo[2];
@@ -506,21 +506,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         if (dst && !*abort_flag) {
             const bool tr = !SO && g.m_trans;
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                if (inside(e)) {
-                    float a, b2;
-                    unpair(M[e], a, b2);
-                    dst[at(e, 0, tr)] = a;
-                    dst[at(e, 1, tr)] = b2;
-                }
+            for (int e = 0; e < 8; e++) {
+                float a, b2;
+                unpair(M[e], a, b2);
+                if (inside(e, 0)) dst[at(e, 0, tr)] = a;
+                if (inside(e, 1)) dst[at(e, 1, tr)] = b2;
+            }
         }
     } else if (KD == 128 && warp < W_Y) {
         // ---- the state: this thread's row, 32 of the tile's columns, fp32
         const int q = warp & 3, n = 32 * q + l32, ch = (warp - W_ST) >> 2, c0 = 32 * ch;
         const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + COL_D + c0;
-        const size_t elems = (size_t)g.da * g.dc;
+        const size_t elems = (size_t)g.dar * g.dcr;
         float *slots = g.ws + (size_t)lane * (g.nseg - 1) * elems;
-        const bool mine = n < g.da;
+        const bool mine = n < g.dar;
         f32x2 M[16];
         // fp32 states go to and from global memory by way of this warp's 32 rows
         // of the M buffers, as fp32 rows of 128 bytes (16-byte pieces XOR row):
@@ -528,25 +527,30 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         uint8_t *stg = sm + OFF_M + (q * 2 + ch) * 4096;
         auto piece = [&](int row, int k) { return reinterpret_cast<float4 *>(stg + row * 128 + ((k ^ (row & 7)) << 4)); };
         const int wr = l32 >> 3, wk = l32 & 7;          // row of four, 16-byte piece
-        const bool in = p0 + c0 + 4 * wk < g.dc;        // dc is a multiple of 8
+        const bool in = p0 + c0 + 4 * wk < g.dcr;
+        // element by element where the state is transposed or its rows are no
+        // whole 16-byte pieces
+        auto at = [&](int p, bool tr) { return tr ? (size_t)(p0 + c0 + p) * g.dar + n : (size_t)n * g.dcr + p0 + c0 + p; };
+        const bool pieces = g.dcr % 4 == 0;
         {
             const float *src = (SO || (seg == 0 && !g.m0)) ? nullptr
                                : (seg == 0 ? g.m0 + lane * elems : slots + (size_t)(seg - 1) * elems);
 #pragma unroll
             for (int p = 0; p < 16; p++) M[p] = 0ull;
-            if (src && seg == 0 && g.m_trans) {
+            const bool tr = seg == 0 && g.m_trans;
+            if (src && (tr || !pieces)) {
                 if (mine) {
 #pragma unroll
                     for (int p = 0; p < 32; p += 2)
-                        if (p0 + c0 + p < g.dc)
-                            M[p / 2] = pair(src[(size_t)(p0 + c0 + p) * g.da + n], src[(size_t)(p0 + c0 + p + 1) * g.da + n]);
+                        M[p / 2] = pair(p0 + c0 + p < g.dcr ? src[at(p, tr)] : 0.f,
+                                        p0 + c0 + p + 1 < g.dcr ? src[at(p + 1, tr)] : 0.f);
                 }
             } else if (src) {
 #pragma unroll 4
                 for (int r = wr; r < 32; r += 4) {
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (in && 32 * q + r < g.da)
-                        v = *reinterpret_cast<const float4 *>(src + (size_t)(32 * q + r) * g.dc + p0 + c0 + 4 * wk);
+                    if (in && 32 * q + r < g.dar)
+                        v = *reinterpret_cast<const float4 *>(src + (size_t)(32 * q + r) * g.dcr + p0 + c0 + 4 * wk);
                     *piece(r, wk) = v;
                 }
                 __syncwarp();
@@ -603,17 +607,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                         : (seg == g.nseg - 1 && g.m_out ? g.m_out + lane * elems : nullptr);
         bool out = dst && !*abort_flag;
         // the last chunk's D3 still reads the buffers
-        if (out && !SO && !g.m_trans && nch > 0) out = wait(B_YFULL + ((nch - 1) & 1), (nch - 1) >> 1, 121);
-        if (out && !SO && g.m_trans) {
+        const bool tro = !SO && g.m_trans, single = tro || !pieces;
+        if (out && !SO && !single && nch > 0) out = wait(B_YFULL + ((nch - 1) & 1), (nch - 1) >> 1, 121);
+        if (out && single) {
             if (mine) {
 #pragma unroll
-                for (int p = 0; p < 32; p += 2)
-                    if (p0 + c0 + p < g.dc) {
-                        float a, b2;
-                        unpair(M[p / 2], a, b2);
-                        dst[(size_t)(p0 + c0 + p) * g.da + n] = a;
-                        dst[(size_t)(p0 + c0 + p + 1) * g.da + n] = b2;
-                    }
+                for (int p = 0; p < 32; p += 2) {
+                    float a, b2;
+                    unpair(M[p / 2], a, b2);
+                    if (p0 + c0 + p < g.dcr) dst[at(p, tro)] = a;
+                    if (p0 + c0 + p + 1 < g.dcr) dst[at(p + 1, tro)] = b2;
+                }
             }
         } else if (out) {
 #pragma unroll
@@ -626,8 +630,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             __syncwarp();
 #pragma unroll 4
             for (int r = wr; r < 32; r += 4)
-                if (in && 32 * q + r < g.da)
-                    *reinterpret_cast<float4 *>(dst + (size_t)(32 * q + r) * g.dc + p0 + c0 + 4 * wk) = *piece(r, wk);
+                if (in && 32 * q + r < g.dar)
+                    *reinterpret_cast<float4 *>(dst + (size_t)(32 * q + r) * g.dcr + p0 + c0 + 4 * wk) = *piece(r, wk);
         }
     } else if (!SO && g.y) {
         // ---- the answers
@@ -640,8 +644,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
 #pragma unroll
         for (int i = 0; i < 4; i++) yo[i] = ybase + mr * 128 + (((2 * i + mc) ^ (mr & 7)) << 4);
         const float si = g.scale_i;
-        const bool f32 = g.y_f32;
-        float *yf = static_cast<float *>(g.y) + ((b * g.T + t_beg) * g.H + h) * g.dc + p0 + cq;
+        // y goes out by TMA, or straight from the registers: in fp32, and where
+        // its rows are no whole 16-byte pieces (then also in single elements,
+        // where they are no whole pairs)
+        const bool direct = g.y_f32 || g.dcr != g.dc, f32 = g.y_f32, even = g.dcr % 2 == 0;
+        const int64_t y0 = ((b * g.T + t_beg) * g.H + h) * g.dcr + p0 + cq;
         for (int c = 0; c < nch; c++) {
             const int pb = c & 1, L = chunk_n(c), t = chunk_t(c);
             if (!wait(B_YFULL + pb, c >> 1, 116)) break;
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             const float fa = ra < L ? pw[rev ? L - 1 - ra : ra + 1] * si : 0.f;
             const float fb = rb < L ? pw[rev ? L - 1 - rb : rb + 1] * si : 0.f;
             const f32x2 fa2 = pair(fa, fa), fb2 = pair(fb, fb);
-            if (!f32) {
+            if (!direct) {
                 if (l32 == 0) tma_store_wait_read();    // the rows of the chunk before are on their way
                 __syncwarp();
             }
@@ -668,16 +675,34 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     for (int e = 0; e < 8; e++)
                         if (((e & 1) ? rb : ra) >= L) o[e] = 0ull;
                 }
-                if (!f32) {
+                if (!direct) {
                     stmatrix4(yo[2 * hf], round2(o[0]), round2(o[1]), round2(o[2]), round2(o[3]));
                     stmatrix4(yo[2 * hf + 1], round2(o[4]), round2(o[5]), round2(o[6]), round2(o[7]));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
-                        const int row = (e & 1) ? rb : ra, col = 32 * hf + 8 * (e >> 1);
-                        // dc is a multiple of 8: a pair is inside or outside
-                        if (p0 + col + cq < g.dc && t_beg + t + row < g.T)
-                            *reinterpret_cast<f32x2 *>(yf + (int64_t)(t + row) * g.H * g.dc + col) = o[e];
+                        const int row = (e & 1) ? rb : ra, col = 32 * hf + 8 * (e >> 1), left = g.dcr - (p0 + col + cq);
+                        if (left <= 0 || t_beg + t + row >= g.T) continue;
+                        const int64_t at = y0 + (int64_t)(t + row) * g.H * g.dcr + col;
+                        float a, b2;
+                        unpair(o[e], a, b2);
+                        if (f32) {
+                            float *y = static_cast<float *>(g.y) + at;
+                            if (even) {
+                                *reinterpret_cast<f32x2 *>(y) = o[e];
+                            } else {
+                                y[0] = a;
+                                if (left > 1) y[1] = b2;
+                            }
+                        } else {
+                            __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(g.y) + at;
+                            if (even) {
+                                *reinterpret_cast<uint32_t *>(y) = pack_bf16(a, b2);
+                            } else {
+                                y[0] = __float2bfloat16_rn(a);
+                                if (left > 1) y[1] = __float2bfloat16_rn(b2);
+                            }
+                        }
                     }
                 }
             }
@@ -686,17 +711,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             __syncwarp();
             if (l32 == 0) {
                 mbar_arrive(bar(B_YEMPTY + pb));
-                if (!f32 && t_beg + t + 16 * q < g.T)
+                if (!direct && t_beg + t + 16 * q < g.T)
                     tma_store4(&P.my[pi], p0, (int)h, (int)t_beg + t + 16 * q, (int)b, ybase);
             }
             __syncwarp();
         }
         // rows behind the sequence in the segment's chunks that were not walked: zeros
         const int64_t e = t_beg + g.seg_len < g.T ? t_beg + g.seg_len : g.T;
-        const int cols = g.dc - p0 < DC ? g.dc - p0 : DC, es = f32 ? 4 : 2, nv = cols * es / 16;
+        const int cols = g.dcr - p0 < DC ? g.dcr - p0 : DC;
         for (int64_t t = t_beg + (int64_t)nch * Q + wy; t < e; t += 4) {
-            uint8_t *row = static_cast<uint8_t *>(g.y) + (((b * g.T + t) * g.H + h) * g.dc + p0) * es;
-            for (int v = l32; v < nv; v += 32) reinterpret_cast<uint4 *>(row)[v] = make_uint4(0u, 0u, 0u, 0u);
+            const int64_t row = ((b * g.T + t) * g.H + h) * g.dcr + p0;
+            for (int p = l32; p < cols; p += 32) {
+                if (f32) static_cast<float *>(g.y)[row + p] = 0.f;
+                else static_cast<__nv_bfloat16 *>(g.y)[row + p] = __float2bfloat16_rn(0.f);
+            }
         }
         if (l32 == 0) tma_store_wait_all();
     } else if (!SO) {
@@ -774,7 +802,7 @@ static void plan_width(MixArgs *g, int n, int kd) {
     for (int i = 0; i < n; i++) {
         if (padded(g[i]) != kd) continue;
         ctas += g[i].Bt * g[i].H * ((g[i].dc + DC - 1) / DC);
-        state += g[i].Bt * g[i].H * g[i].da * g[i].dc * 4;
+        state += g[i].Bt * g[i].H * g[i].dar * g[i].dcr * 4;
         g[i].nseg = 1;
         g[i].seg_len = (nq > 0 ? nq : 1) * Q;
     }
@@ -856,7 +884,7 @@ cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
             if (!rows_map(&P.ma[k], a.a, a.da, a.H / a.ra, a.T, a.Bt, a.lda, Q) ||
                 !rows_map(&P.mb[k], a.b, a.da, a.H / a.rb, a.T, a.Bt, a.ldb, Q) ||
                 !rows_map(&P.mc[k], a.c, a.dc, a.H / a.rc, a.T, a.Bt, a.ldc, Q) ||
-                (a.y && !a.y_f32 && !rows_map(&P.my[k], a.y, a.dc, a.H, a.T, a.Bt, a.H * a.dc, 16)))
+                (a.y && !a.y_f32 && a.dcr == a.dc && !rows_map(&P.my[k], a.y, a.dc, a.H, a.T, a.Bt, a.H * a.dc, 16)))
                 return cudaErrorInvalidValue;
             P.g[k] = a;
             split |= a.nseg > 1;

@@ -25,20 +25,21 @@ struct MixArgs {
     const void *a, *b, *c;
     int64_t lda, ldb, ldc;       // elements between the rows of consecutive tokens
     int ra, rb, rc;              // lanes' heads that share one head of a, b, c
-    int da, dc;                  // width of a and b rows, of c rows
+    int da, dc;                  // width of a and b rows, of c rows, in memory
+    int dar, dcr;                // the same without padding: widths of the states and of y
     const float *log_decay;      // (H), natural logarithm
     const int32_t *lengths;      // (Bt) tokens of each sequence, or NULL for T
     const float *m0;             // state the walk starts from, or NULL for zero
     float *m_out;                // state after the walk, or NULL
-    int m_trans;                 // m0, m_out hold the state transposed, (dc, da) instead of (da, dc)
-    void *y;                     // (Bt, T, H, dc), or NULL when only m_out is wanted
+    int m_trans;                 // m0, m_out hold the state transposed, (dcr, dar) instead of (dar, dcr)
+    void *y;                     // (Bt, T, H, dcr), or NULL when only m_out is wanted
     int y_f32;                   // y in fp32 (else the input type)
     int64_t Bt, T, H;
     int reverse;
     float scale_p, scale_i, scale_w;
     int nseg;                    // segments of the time axis, in walking order
     int64_t seg_len;             // tokens of a segment
-    float *ws;                   // (nseg - 1) states of da * dc floats for each lane
+    float *ws;                   // (nseg - 1) states of dar * dcr floats for each lane
 };
 
 struct LinStepArgs {
@@ -98,6 +99,16 @@ cudaError_t launch_mix_tc(const MixArgs *a, int n, cudaStream_t s);
 int mix_tc_error_and_clear(cudaStream_t s);
 // chains the segments' states between the two passes
 cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s);
+// Rows whose width or stride TMA cannot address, copied into rows padded with
+// zeros to a multiple of 8 columns: up to four tensors in one launch.
+struct PadArgs {
+    const void *src[4];          // (rows, heads, d) bf16, ld elements from row to row
+    void *dst[4];                // (rows, heads, (d + 7) / 8 * 8), contiguous, 16-byte aligned
+    int64_t ld[4], n[4];         // n: 8-column pieces of dst
+    int heads[4], d[4];
+    int count;
+};
+cudaError_t launch_pad_rows(const PadArgs &a, cudaStream_t s);
 // sums one or two fp32 (Bt, T, H, d) tensors over the heads of each of G groups
 cudaError_t launch_head_sum(const float *const in[2], void *const out[2], int count, m3_dtype dt, int64_t rows, int64_t H,
                             int64_t G, int64_t d, cudaStream_t s);

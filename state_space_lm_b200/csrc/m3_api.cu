@@ -463,7 +463,7 @@ void plan_mixes(LinPlan &p, m3_dtype dtype, bool aligned) {
         MixArgs &m = p.m[i];
         if (!p.tc) mix_simt_plan(m);
         p.states[i] = p.bytes;
-        p.bytes += align256((size_t)(m.Bt * m.H) * (size_t)(m.nseg - 1) * m.da * m.dc * sizeof(float));
+        p.bytes += align256((size_t)(m.Bt * m.H) * (size_t)(m.nseg - 1) * m.dar * m.dcr * sizeof(float));
     }
 }
 cudaError_t launch_mixes(LinPlan &p, m3_dtype dtype, void *workspace, cudaStream_t s) {
@@ -477,44 +477,95 @@ cudaError_t launch_mixes(LinPlan &p, m3_dtype dtype, void *workspace, cudaStream
     return cudaSuccess;
 }
 
+// bf16 rows that TMA cannot address, for their width or their stride, are
+// copied into padded ones first (in the workspace): the tensor cores still pay,
+// 8 x 2048 tokens of 16 heads of 120 x 60 took 1.1 ms in fp32 arithmetic.
+struct LinPads {
+    bool on;
+    int64_t dk, dv;            // padded widths
+    size_t q, k, v, dy, bytes; // offsets from the first of them, and their end
+};
+LinPads pads_of(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
+    LinPads p{};
+    p.dk = d.dstate;
+    p.dv = d.headdim;
+    if (dtype != M3_BF16 || d.dstate > 128 || d.headdim > 128 || d.seqlen < 1) return p;
+    // what the tensor-core path takes (mix_tc_sizes), with room for the padding
+    if (d.batch * d.nheads > (int64_t)1 << 28 || sat_product({d.seqlen, d.nheads, 128}) > (int64_t)1 << 37) return p;
+    p.on = d.dstate % 8 || d.headdim % 8 || o.ldq % 8 || o.ldk % 8 || o.ldv % 8;
+    if (!p.on) return p;
+    p.dk = (d.dstate + 7) / 8 * 8;
+    p.dv = (d.headdim + 7) / 8 * 8;
+    const size_t rows = (size_t)(d.batch * d.seqlen);
+    p.k = align256(rows * o.G * p.dk * 2);
+    p.v = 2 * p.k;
+    p.dy = p.v + align256(rows * d.nheads * p.dv * 2);
+    p.bytes = p.dy + align256(rows * d.nheads * p.dv * 2);
+    return p;
+}
+
 // One mix of the problem, without its pointers.
-MixArgs mix_of(const m3_linattn_dims &d, int64_t da, int64_t dc, m3_dtype dtype) {
+MixArgs mix_of(const m3_linattn_dims &d, int64_t da, int64_t dc, int64_t dar, int64_t dcr, m3_dtype dtype) {
     MixArgs m{};
     m.Bt = d.batch; m.H = d.nheads; m.T = d.seqlen;
     m.da = (int)da; m.dc = (int)dc;
+    m.dar = (int)dar; m.dcr = (int)dcr;
     m.ra = m.rb = m.rc = 1;
     m.y_f32 = dtype == M3_F32;
     return m;
 }
-LinPlan fwd_mix(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
+LinPlan fwd_mix(const m3_linattn_dims &d, const LinGeo &o, const LinPads &pd, m3_dtype dtype) {
     LinPlan p;
     p.n = 1;
-    MixArgs &m = p.m[0] = mix_of(d, d.dstate, d.headdim, dtype);
-    m.lda = o.ldq; m.ldb = o.ldk; m.ldc = o.ldv;
+    MixArgs &m = p.m[0] = mix_of(d, pd.dk, pd.dv, d.dstate, d.headdim, dtype);
+    m.lda = pd.on ? o.G * pd.dk : o.ldq;
+    m.ldb = pd.on ? o.G * pd.dk : o.ldk;
+    m.ldc = pd.on ? d.nheads * pd.dv : o.ldv;
     m.ra = m.rb = (int)(d.nheads / o.G);
     return p;
 }
 // dq = mix(dy, v, k) forwards, dk = mix(v, dy, q) and dv = mix(k, q, dy)
 // backwards.
-LinPlan bwd_mixes(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
+LinPlan bwd_mixes(const m3_linattn_dims &d, const LinGeo &o, const LinPads &pd, m3_dtype dtype) {
     LinPlan p;
     p.n = 3;
     const int rep = (int)(d.nheads / o.G);
-    const int64_t ldd = d.nheads * d.headdim;
-    MixArgs &dq = p.m[0] = mix_of(d, d.headdim, d.dstate, dtype);
-    dq.lda = ldd; dq.ldb = o.ldv; dq.ldc = o.ldk; dq.rc = rep;
+    const int64_t ldd = d.nheads * pd.dv, ldq = pd.on ? o.G * pd.dk : o.ldq, ldk = pd.on ? o.G * pd.dk : o.ldk;
+    const int64_t ldv = pd.on ? ldd : o.ldv;
+    MixArgs &dq = p.m[0] = mix_of(d, pd.dv, pd.dk, d.headdim, d.dstate, dtype);
+    dq.lda = ldd; dq.ldb = ldv; dq.ldc = ldk; dq.rc = rep;
     MixArgs &dk = p.m[1] = dq;
-    dk.lda = o.ldv; dk.ldb = ldd; dk.ldc = o.ldq;
+    dk.lda = ldv; dk.ldb = ldd; dk.ldc = ldq;
     dk.reverse = 1;
     for (MixArgs *m : {&dq, &dk}) {
         m->m_trans = 1;
         if (rep > 1) m->y_f32 = 1;
     }
-    MixArgs &dv = p.m[2] = mix_of(d, d.dstate, d.headdim, dtype);
-    dv.lda = o.ldk; dv.ldb = o.ldq; dv.ldc = ldd;
+    MixArgs &dv = p.m[2] = mix_of(d, pd.dk, pd.dv, d.dstate, d.headdim, dtype);
+    dv.lda = ldk; dv.ldb = ldq; dv.ldc = ldd;
     dv.ra = dv.rb = rep;
     dv.reverse = 1;
     return p;
+}
+// The copies of q, k, v (and dy), and the mixes' pointers turned to them.
+PadArgs pad_rows(const m3_linattn_dims &d, const LinGeo &o, const LinPads &pd, char *at, const void *&q, const void *&k,
+                 const void *&v, const void **dy) {
+    PadArgs a{};
+    auto add = [&](const void *&src, size_t off, int64_t ld, int64_t heads, int64_t w, int64_t wp) {
+        const int i = a.count++;
+        a.src[i] = src;
+        a.dst[i] = at + off;
+        a.ld[i] = ld;
+        a.n[i] = d.batch * d.seqlen * heads * (wp / 8);
+        a.heads[i] = (int)heads;
+        a.d[i] = (int)w;
+        src = at + off;
+    };
+    add(q, pd.q, o.ldq, o.G, d.dstate, pd.dk);
+    add(k, pd.k, o.ldk, o.G, d.dstate, pd.dk);
+    add(v, pd.v, o.ldv, d.nheads, d.headdim, pd.dv);
+    if (dy) add(*dy, pd.dy, d.nheads * d.headdim, d.nheads, d.headdim, pd.dv);
+    return a;
 }
 // bytes of one gradient of shared heads, per head in fp32
 size_t head_bytes(const m3_linattn_dims &d, const LinGeo &o) {
@@ -530,14 +581,15 @@ size_t m3_linattn_workspace_bytes(int which, m3_linattn_dims d, m3_dtype dtype) 
     if (check_dtype(dtype) != M3_OK || check_linattn_dims(d, true, o) != M3_OK) return 0;
     if (which != M3_WS_LINATTN_FWD && which != M3_WS_LINATTN_BWD) return 0;
     const bool bwd = which == M3_WS_LINATTN_BWD;
+    const LinPads pd = pads_of(d, o, dtype);
     size_t most = 0;
     for (bool aligned : {false, true}) {
-        LinPlan p = bwd ? bwd_mixes(d, o, dtype) : fwd_mix(d, o, dtype);
+        if (pd.on && !aligned) continue;
+        LinPlan p = bwd ? bwd_mixes(d, o, pd, dtype) : fwd_mix(d, o, pd, dtype);
         plan_mixes(p, dtype, aligned);
         if (p.bytes > most) most = p.bytes;
-        if (!p.tc && aligned) break;
     }
-    return most + (bwd ? 2 * head_bytes(d, o) : 0);
+    return most + (bwd ? 2 * head_bytes(d, o) + pd.bytes : pd.on ? pd.dy : 0);
 }
 
 m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3_dtype dtype, const float *log_decay,
@@ -556,7 +608,12 @@ m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3
     const size_t need = m3_linattn_workspace_bytes(M3_WS_LINATTN_FWD, d, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
     if (d.batch == 0) return M3_OK;
-    LinPlan p = fwd_mix(d, o, dtype);
+    const LinPads pd = pads_of(d, o, dtype);
+    LinPlan p = fwd_mix(d, o, pd, dtype);
+    plan_mixes(p, dtype, pd.on || tma_aligned(q, k, v));
+    PadArgs pads{};
+    if (pd.on && !p.tc) return M3_ERR_UNSUPPORTED;          // does not happen: pads_of has seen to it
+    if (pd.on) pads = pad_rows(d, o, pd, static_cast<char *>(workspace) + p.bytes, q, k, v, nullptr);
     MixArgs &m = p.m[0];
     m.a = q; m.b = k; m.c = v;
     m.log_decay = log_decay; m.lengths = lengths;
@@ -564,8 +621,10 @@ m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3
     m.y = y;
     m.scale_p = m.scale_i = scale;
     m.scale_w = 1.f;
-    plan_mixes(p, dtype, tma_aligned(q, k, v));
-    return launch_unless_injected([&] { return launch_mixes(p, dtype, workspace, (cudaStream_t)stream); });
+    return launch_unless_injected([&]() -> cudaError_t {
+        const cudaError_t e = launch_pad_rows(pads, (cudaStream_t)stream);
+        return e != cudaSuccess ? e : launch_mixes(p, dtype, workspace, (cudaStream_t)stream);
+    });
 }
 
 m3_status m3_linattn_step_decode(const void *q_t, const void *k_t, const void *v_t, m3_dtype dtype,
@@ -608,11 +667,15 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
     if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
     const bool want[3] = {g.dq != nullptr, g.dk != nullptr, g.dv || g.ds0};
     if (d.batch == 0 || !(want[0] || want[1] || want[2])) return M3_OK;
-    LinPlan p = bwd_mixes(d, o, dtype);
-    plan_mixes(p, dtype, tma_aligned(q, k, v));
+    const LinPads pd = pads_of(d, o, dtype);
+    LinPlan p = bwd_mixes(d, o, pd, dtype);
+    plan_mixes(p, dtype, pd.on || tma_aligned(q, k, v));
     const size_t hb = head_bytes(d, o);
     const bool shared = hb > 0;
     char *heads = static_cast<char *>(workspace) + p.bytes;
+    PadArgs pads{};
+    if (pd.on && !p.tc) return M3_ERR_UNSUPPORTED;          // does not happen: pads_of has seen to it
+    if (pd.on) pads = pad_rows(d, o, pd, heads + 2 * hb, q, k, v, &dy);
     const float *sum_in[2] = {};
     void *sum_out[2] = {};
     int ns = 0;
@@ -646,7 +709,8 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
         }
     const cudaStream_t s = (cudaStream_t)stream;
     return launch_unless_injected([&]() -> cudaError_t {
-        cudaError_t e = launch_mixes(p, dtype, workspace, s);
+        cudaError_t e = launch_pad_rows(pads, s);
+        if (e == cudaSuccess) e = launch_mixes(p, dtype, workspace, s);
         if (e == cudaSuccess && ns > 0)
             e = launch_head_sum(sum_in, sum_out, ns, dtype, d.batch * d.seqlen, d.nheads, o.G, d.dstate, s);
         return e;
