@@ -776,8 +776,10 @@ static bool rows_map(CUtensorMap *m, const void *base, int64_t d, int64_t heads,
 
 }  // namespace mixtc
 
+// Sequences of up to 16 tokens are one block of the fp32 kernel: as fast as
+// this kernel's set-up, and without its roundings.
 bool mix_tc_sizes(const MixArgs &g, m3_dtype dt) {
-    if (dt != M3_BF16 || g.da > mixtc::DA || g.dc > mixtc::DA || g.da % 8 || g.dc % 8 || g.T < 1) return false;
+    if (dt != M3_BF16 || g.da > mixtc::DA || g.dc > mixtc::DA || g.da % 8 || g.dc % 8 || g.T <= 16) return false;
     if (g.Bt * g.H > (int64_t)1 << 28) return false;      // three problems of two column tiles share a 1-D grid
     // a TMA stride is a multiple of 16 bytes below 2^40
     for (int64_t ld : {g.lda, g.ldb, g.ldc})
