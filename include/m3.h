@@ -322,10 +322,10 @@ size_t m3_workspace_bytes(int which, m3_dims d, m3_dtype dtype);
  * bases of q, k and v need only the alignment of their type; everything else
  * is contiguous and 16-byte aligned.
  *
- * bf16 inputs with dstate and headdim <= 128 and more than 16 tokens run on the
- * tensor cores (widths or row strides that are no multiples of 8 by way of padded copies in the
- * workspace; other bases than 16-byte aligned ones do not); everything else
- * runs in fp32 arithmetic.  A
+ * bf16 inputs with dstate and headdim <= 128 run on the tensor cores (widths or
+ * row strides that are no multiples of 8 by way of padded copies in the
+ * workspace; other bases than 16-byte aligned ones do not, nor do few sequences
+ * of up to 16 tokens); everything else runs in fp32 arithmetic.  A
  * non-finite q, k or v reaches the rows that depend on it, and may reach
  * earlier rows of its own 64-token chunk; one behind a sequence's length
  * reaches nothing. */

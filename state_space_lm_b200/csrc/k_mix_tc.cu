@@ -20,14 +20,14 @@
 // bf16 pieces, hi + mid + lo = w c exactly, side by side in D4's columns.
 //
 // One CTA owns one lane, one tile of 64 columns of c and one segment of the
-// time axis, and walks its chunks.  24 warps: 0 TMA, 1-3 UMMA issue (D1; D4; D3 and D2),
-// 4-7 Cw, 8-11 scores, 12-19 state, 20-23 outputs.  Three issuing warps, not
-// one: a section of waits, fence, issue and commit takes a warp 400 to 700
-// cycles, four of them in a row more than anything else in a chunk.  The hand-overs are buffered
-// in TMEM or shared memory, so the roles work on different chunks;
-// the chain from chunk to chunk is only the state's update.  A split time
-// axis takes two passes: B and C alone for every segment's own state, the
-// combine of linattn.cuh, then all segments at once.
+// time axis, and walks its chunks.  24 warps: 0 TMA, 1-3 UMMA issue (D1; D4; D3
+// and D2), 4-7 Cw, 8-11 scores, 12-19 state, 20-23 outputs.  Three issuing
+// warps, not one: a section of waits, fence, issue and commit takes a warp 400
+// to 700 cycles, four of them in a row more than anything else in a chunk.  The
+// hand-overs are buffered in TMEM or shared memory, so the roles work on
+// different chunks; the chain from chunk to chunk is only the state's update.
+// A split time axis takes two passes: B and C alone for every segment's own
+// state, the combine of linattn.cuh, then all segments at once.
 //
 // The problems of a call (three in the backward) share one launch.  Every
 // wait is bounded: past ~1 s the kernel records the site, stops issuing work,
@@ -776,10 +776,14 @@ static bool rows_map(CUtensorMap *m, const void *base, int64_t d, int64_t heads,
 
 }  // namespace mixtc
 
-// Sequences of up to 16 tokens are one block of the fp32 kernel: as fast as
-// this kernel's set-up, and without its roundings.
+// Up to 256 lanes of up to 16 tokens are one block each of the fp32 kernel, which
+// takes about as long and has no operand rounding.  128 x 64 states, 16 tokens
+// there against 17 here, forward and backward: 16 lanes 6.9 and 16.5 us against
+// 7.0 and 13.2, 256 lanes 17.6 and 48.8 against 14.3 and 54.1; 1024 lanes'
+// forward is 61 us there against 49 here (with the calls' host time).
 bool mix_tc_sizes(const MixArgs &g, m3_dtype dt) {
-    if (dt != M3_BF16 || g.da > mixtc::DA || g.dc > mixtc::DA || g.da % 8 || g.dc % 8 || g.T <= 16) return false;
+    if (dt != M3_BF16 || g.da > mixtc::DA || g.dc > mixtc::DA || g.da % 8 || g.dc % 8 || g.T < 1) return false;
+    if (g.T <= 16 && g.Bt * g.H <= 256) return false;
     if (g.Bt * g.H > (int64_t)1 << 28) return false;      // three problems of two column tiles share a 1-D grid
     // a TMA stride is a multiple of 16 bytes below 2^40
     for (int64_t ld : {g.lda, g.ldb, g.ldc})

@@ -489,7 +489,8 @@ LinPads pads_of(const m3_linattn_dims &d, const LinGeo &o, m3_dtype dtype) {
     LinPads p{};
     p.dk = d.dstate;
     p.dv = d.headdim;
-    if (dtype != M3_BF16 || d.dstate > 128 || d.headdim > 128 || d.seqlen <= 16) return p;
+    if (dtype != M3_BF16 || d.dstate > 128 || d.headdim > 128 || d.seqlen < 1) return p;
+    if (d.seqlen <= 16 && d.batch * d.nheads <= 256) return p;
     // what the tensor-core path takes (mix_tc_sizes), with room for the padding
     if (d.batch * d.nheads > (int64_t)1 << 28 || sat_product({d.seqlen, d.nheads, 128}) > (int64_t)1 << 37) return p;
     p.on = d.dstate % 8 || d.headdim % 8 || o.ldq % 8 || o.ldk % 8 || o.ldv % 8;

@@ -141,6 +141,31 @@ def test_ragged_batches_with_garbage_behind_the_lengths(shape, dtype):
     assert torch.equal(y, y2) and torch.equal(sf, sf2)
 
 
+@pytest.mark.parametrize("shape", [(129, 1, 2, 2, 64, 64), (20, 16, 16, 4, 128, 64), (65, 7, 4, 1, 36, 20),
+                                   (128, 16, 2, 2, 64, 64), (300, 3, 1, 1, 8, 72)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_many_short_sequences(shape):
+    """Both sides of the rule that gives up to 256 lanes of up to 16 tokens to
+    the fp32 kernel and more of them to the tensor cores."""
+    d = inputs(*shape, "bf16", ragged=True)
+    check_forward(d)
+    check_backward(d)
+
+
+def test_a_nan_stays_out_of_the_chunks_before_it():
+    for dtype, block in (("f32", 1), ("bf16", 64)):
+        d = inputs(1, 300, 2, 2, 64, 64, dtype)
+        y, _ = m3.linattn_chunked_fwd(d["q"], d["k"], d["v"], d["ld"], s0=d["s0"])
+        for name in "qkv":
+            bad = dict(d)
+            bad[name] = d[name].clone()
+            bad[name][:, 200] = math.nan
+            y2, _ = m3.linattn_chunked_fwd(bad["q"], bad["k"], bad["v"], d["ld"], s0=d["s0"])
+            first = 200 - 200 % block
+            assert torch.equal(y2[:, :first], y[:, :first]), name
+            assert bool(torch.isnan(y2[:, 200]).all()), name
+
+
 def test_lengths_outside_the_range_are_taken_into_it():
     d = inputs(3, 40, 2, 2, 64, 64, "bf16")
     d["lengths"] = torch.tensor([-5, 999, 40], dtype=torch.int32, device="cuda")
