@@ -385,7 +385,9 @@ size_t m3_linattn_workspace_bytes(int which, m3_linattn_dims d, m3_dtype dtype);
  *               1 / sqrt(biased variance + eps)
  *   u = (x - mean) rstd weight + bias
  *   y = act(u) without a gate, u act(gate) with one
- * channels <= 16384 and a multiple of ngroups; batch * ngroups < 2^31. */
+ * channels <= 16384 and a multiple of ngroups; batch * ngroups < 2^31.  With
+ * no rows (batch or seqlen 0) dweight and dbias are written as zeros and
+ * nothing else is. */
 typedef enum { M3_ACT_NONE = 0, M3_ACT_SILU = 1, M3_ACT_GELU = 2, M3_ACT_RELU = 3 } m3_act; /* GELU: the erf form */
 
 typedef struct {

@@ -3,9 +3,14 @@ each forward and its backward behind one torch.autograd.Function.
 
 Argument marshalling only: the forward calls m3_siso_chunked_fwd or
 m3_mimo_chunked_fwd, the backward calls m3_chunked_bwd (m3_linattn_* and
-m3_group_norm_* for the other two), and every gradient comes from the CUDA library (there is no other implementation behind these
-names).  The initial states and the final states take part in autograd too,
-so a sequence can be split into pieces whose states are chained.
+m3_group_norm_* for the other two), and every gradient comes from the CUDA
+library (there is no other implementation behind these names).  The initial
+states and the final states take part in autograd too, so a sequence can be
+split into pieces whose states are chained.
+
+A training step can be captured into a CUDA graph.  PyTorch ties a leaf's
+gradient to the stream of the graph that used it first: drop every eager
+graph of the same leaves (their losses) before the capture.
 """
 import torch
 from torch.autograd.function import once_differentiable
@@ -65,6 +70,13 @@ def mamba3_scan(x, dt, A, lam, theta, B, C, D, chunk=64, W_x=None, W_y=None, h0=
     return Mamba3Scan.apply(x, dt, A, lam, theta, B, C, D, W_x, W_y, h0, prevBx0, angle0, chunk)
 
 
+def _grad(t, dtype):
+    """An incoming gradient as the library takes it: a view that autograd cut
+    out of a larger one (by torch.cat, say) may start anywhere."""
+    t = t.to(dtype).contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class LinearAttention(torch.autograd.Function):
     """Returns (y, s_final); gradients of q, k, v and s0."""
 
@@ -85,9 +97,9 @@ class LinearAttention(torch.autograd.Function):
         q, k, v, log_decay, s0, lengths = ctx.saved_tensors
         need = dict(zip(("dq", "dk", "dv"), ctx.needs_input_grad[:3]), ds0=ctx.needs_input_grad[5])
         want = tuple(n for n, on in need.items() if on)
-        dy = torch.zeros_like(v, memory_format=torch.contiguous_format) if dy is None else dy.to(v.dtype).contiguous()
+        dy = torch.zeros_like(v, memory_format=torch.contiguous_format) if dy is None else _grad(dy, v.dtype)
         g = m3.linattn_chunked_bwd(q, k, v, log_decay, dy, scale=ctx.scale, s0=s0,
-                                   ds_final=None if ds is None else ds.contiguous(), lengths=lengths, want=want)
+                                   ds_final=None if ds is None else _grad(ds, torch.float32), lengths=lengths, want=want)
         return g.get("dq"), g.get("dk"), g.get("dv"), None, None, g.get("ds0"), None
 
 
@@ -113,8 +125,8 @@ class GroupNorm(torch.autograd.Function):
         x, weight, bias, gate, mean, rstd = ctx.saved_tensors
         n = ctx.needs_input_grad
         want = tuple(k for k, on in (("dx", n[0]), ("dweight", n[2]), ("dbias", n[3]), ("dgate", n[4])) if on)
-        g = m3.group_norm_bwd(x, dy.to(x.dtype).contiguous(), mean, rstd, ctx.groups, weight, bias, gate=gate,
-                              act=ctx.act, want=want)
+        g = m3.group_norm_bwd(x, _grad(dy, x.dtype), mean, rstd, ctx.groups, weight, bias, gate=gate, act=ctx.act,
+                              want=want)
         return g.get("dx"), None, g.get("dweight"), g.get("dbias"), g.get("dgate"), None, None
 
 

@@ -544,45 +544,33 @@ def _row_ptr(t):
     return t.data_ptr()
 
 
-class _Device:
-    """Makes a tensor's device the current one around a library call (the
-    library launches on the current device), and gives the stream: the
-    caller's, or that device's current one."""
-
-    def __init__(self, dev, stream):
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        self.dev, self.stream = dev, stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return (torch.cuda.current_stream(self.dev) if self.stream is None else self.stream).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
-
-
 # the current stream's handle without building a Stream object (3 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _run(fn, where, args, dev, stream, made=()):
-    """fn(*args, stream) on dev.  made: tensors that this call allocated, on
-    the current stream; the allocator has to know of the caller's stream before
-    it gives their memory to someone else."""
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-    if stream is None and _raw_stream is not None and dev.index == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(dev.index))
-    else:
-        with _Device(dev, stream) as s:
-            rc = fn(*args, s)
-    if rc != M3_OK:
-        raise M3Error(rc, where)
+def _run(fn, where, args, dev):
+    """fn(*args, stream) on dev, which the library's launches need as the
+    current device, and on its current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run(fn, where, args, dev)
+    _check(fn(*args, torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev.index)),
+           where)
+
+
+def _on(stream, t, fn, *args, **kw):
+    """fn on the caller's stream: as the current one, so that what the call
+    allocates has no work of another stream pending on its memory; the
+    caller's current stream is noted on the results, which it may read."""
+    if stream.device != t.device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
+    here = torch.cuda.current_stream(t.device)
+    with torch.cuda.stream(stream):
+        got = fn(*args, **kw)
+    for r in (got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,)):
+        if r is not None:
+            r.record_stream(here)
+    return got
 
 
 def _ld(where, name, t):
@@ -634,8 +622,8 @@ def _linattn_dims(w, q, k, v, seq, which=None):
         _expect(w, dev, "k", k, n, io)
         raise ValueError("%s: q is %s, k %s and v %s" % (w, tuple(qs), tuple(k.shape), tuple(vs)))
     H, G = vs[-2], qs[-2]
-    if G < 1 or H % G:
-        raise ValueError("%s: %d heads over %d groups of q and k" % (w, H, G))
+    if G < 1 or H % G or qs[-1] < 1:
+        raise ValueError("%s: %d heads over %d groups of q and k, %d wide" % (w, H, G, qs[-1]))
     d, need = _linattn_plan(vs[0], vs[1] if seq else 1, H, vs[-1], qs[-1], G, _ld(w, "q", q), _ld(w, "k", k),
                             _ld(w, "v", v), dt, which)
     return d, need, dev, dt
@@ -667,6 +655,8 @@ def linattn_chunked_fwd(q, k, v, log_decay, scale=None, s0=None, lengths=None, w
     out and their rows of y are zeros.  Returns y (Bt,T,H,dv) and s_final
     (Bt,H,dk,dv) fp32, the state for linattn_step_decode; ``out`` may hold
     both (s_final None when it is not wanted)."""
+    if stream is not None:
+        return _on(stream, v, linattn_chunked_fwd, q, k, v, log_decay, scale, s0, lengths, workspace, out)
     w, f = "m3_linattn_chunked_fwd", torch.float32
     d, need, dev, dt = _linattn_dims(w, q, k, v, True, M3_WS_LINATTN_FWD)
     ns = d.batch * d.nheads * d.dstate * d.headdim
@@ -684,14 +674,15 @@ def linattn_chunked_fwd(q, k, v, log_decay, scale=None, s0=None, lengths=None, w
     args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(y), _ptr(sf),
             _ptr(ws), nbytes)
-    _run(lib().m3_linattn_chunked_fwd, w, args, dev, stream, (None if workspace is not None else ws,
-                                                              *((y, sf) if out is None else ())))
+    _run(lib().m3_linattn_chunked_fwd, w, args, dev)
     return y, sf
 
 
 def linattn_step_decode(q_t, k_t, v_t, log_decay, s, scale=None, y_out=None, stream=None):
     """One token of every lane: q_t, k_t (Bt,G,dk), v_t (Bt,H,dv); the state s
     (Bt,H,dk,dv) fp32 is updated in place; returns y_t (Bt,H,dv)."""
+    if stream is not None:
+        return _on(stream, v_t, linattn_step_decode, q_t, k_t, v_t, log_decay, s, scale, y_out)
     w, f = "m3_linattn_step_decode", torch.float32
     d, _, dev, dt = _linattn_dims(w, q_t, k_t, v_t, False)
     _expect(w, dev, "log_decay", log_decay, d.nheads, f)
@@ -703,7 +694,7 @@ def linattn_step_decode(q_t, k_t, v_t, log_decay, s, scale=None, y_out=None, str
         _expect(w, dev, "y_t", y, v_t.numel(), v_t.dtype)
     args = (_row_ptr(q_t), _row_ptr(k_t), _row_ptr(v_t), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), d, _ptr(s), _ptr(y))
-    _run(lib().m3_linattn_step_decode, w, args, dev, stream, (y,) if y_out is None else ())
+    _run(lib().m3_linattn_step_decode, w, args, dev)
     return y
 
 
@@ -713,6 +704,9 @@ def linattn_chunked_bwd(q, k, v, log_decay, dy, scale=None, s0=None, ds_final=No
     ``want`` (by default dq, dk, dv, ds0), contiguous in their inputs' shapes
     and dtype (ds0 fp32).  dy (Bt,T,H,dv) contiguous; ds_final fp32 or None for
     zero.  ``out`` may hold preallocated tensors by name."""
+    if stream is not None:
+        return _on(stream, v, linattn_chunked_bwd, q, k, v, log_decay, dy, scale, s0, ds_final, lengths, want, out,
+                   workspace)
     w, f = "m3_linattn_chunked_bwd", torch.float32
     d, need, dev, dt = _linattn_dims(w, q, k, v, True, M3_WS_LINATTN_BWD)
     ns = d.batch * d.nheads * d.dstate * d.headdim
@@ -740,8 +734,7 @@ def linattn_chunked_bwd(q, k, v, log_decay, dy, scale=None, s0=None, ds_final=No
     args = (_row_ptr(q), _row_ptr(k), _row_ptr(v), dt, _ptr(log_decay),
             d.dstate ** -0.5 if scale is None else float(scale), _ptr(s0), _ptr(lengths), d, _ptr(dy), _ptr(ds_final),
             ctypes.byref(g), _ptr(ws), nbytes)
-    _run(lib().m3_linattn_chunked_bwd, w, args, dev, stream, (None if workspace is not None else ws,
-                                                              *(t for n, t in out.items() if n not in pre)))
+    _run(lib().m3_linattn_chunked_bwd, w, args, dev)
     return out
 
 
@@ -780,6 +773,8 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps
     head of each token pass (tokens, C) and groups = heads.  Returns y, mean
     and rstd (Bt, groups) fp32; ``out`` may hold the three (mean, rstd None
     when not wanted)."""
+    if stream is not None:
+        return _on(stream, x, group_norm_fwd, x, groups, weight, bias, gate, act, eps, workspace, out)
     w, f = "m3_group_norm_fwd", torch.float32
     d, need, dev, dt = _norm_dims(w, x, groups, weight, bias, gate, act, M3_WS_NORM_FWD)
     if out is None:
@@ -793,8 +788,7 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps
     ws, nbytes = _own_workspace(need, workspace, x)
     args = (_ptr(x), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], float(eps), d, _ptr(y), _ptr(mean),
             _ptr(rstd), _ptr(ws), nbytes)
-    _run(lib().m3_group_norm_fwd, w, args, dev, stream, (None if workspace is not None else ws,
-                                                         *((y, mean, rstd) if out is None else ())))
+    _run(lib().m3_group_norm_fwd, w, args, dev)
     return y, mean, rstd
 
 
@@ -803,6 +797,8 @@ def group_norm_bwd(x, dy, mean, rstd, groups, weight=None, bias=None, gate=None,
     """Backward of group_norm_fwd from its mean and rstd: a dict of the
     gradients named in ``want`` (by default dx, dweight, dbias, and dgate with
     a gate): dx, dgate in x's shape and dtype, dweight, dbias (C) fp32."""
+    if stream is not None:
+        return _on(stream, x, group_norm_bwd, x, dy, mean, rstd, groups, weight, bias, gate, act, want, out, workspace)
     w, f = "m3_group_norm_bwd", torch.float32
     d, need, dev, dt = _norm_dims(w, x, groups, weight, bias, gate, act, M3_WS_NORM_BWD)
     _expect(w, dev, "dy", dy, x.numel(), x.dtype)
@@ -828,6 +824,5 @@ def group_norm_bwd(x, dy, mean, rstd, groups, weight=None, bias=None, gate=None,
     args = (_ptr(x), _ptr(dy), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], _ptr(mean), _ptr(rstd), d,
             _ptr(out.get("dx")), _ptr(out.get("dweight")), _ptr(out.get("dbias")), _ptr(out.get("dgate")), _ptr(ws),
             nbytes)
-    _run(lib().m3_group_norm_bwd, w, args, dev, stream, (None if workspace is not None else ws,
-                                                         *(t for n, t in out.items() if n not in pre)))
+    _run(lib().m3_group_norm_bwd, w, args, dev)
     return out

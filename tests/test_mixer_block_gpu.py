@@ -211,3 +211,61 @@ def test_injected_launch_failures_raise_and_enqueue_nothing():
     assert bool((y == -7).all()) and bool((s == -7).all())
     m3.linattn_chunked_fwd(q, k, v, x["ld"], out=(y, s))
     assert not bool((y == -7).all())
+
+
+def test_results_on_another_stream_take_no_memory_with_work_pending():
+    """A block of memory that the current stream has freed but is still to
+    write goes to nobody on another stream."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn(2, 4096, 4, 64, generator=g, device="cuda").bfloat16() for _ in range(3))
+    ld = torch.full((4,), -0.05, device="cuda")
+    x = torch.randn(2, 4096, 256, generator=g, device="cuda").bfloat16()
+    w = torch.randn(256, generator=g, device="cuda")
+    ref, _ = m3.linattn_chunked_fwd(q, k, v, ld)
+    gref = m3.linattn_chunked_bwd(q, k, v, ld, v)
+    nref, mean, rstd = m3.group_norm_fwd(x, 4, w)
+    bref = m3.group_norm_bwd(x, x, mean, rstd, 4, w)
+    state = torch.zeros(2, 4, 64, 64, device="cuda")
+    sref = m3.linattn_step_decode(q[:, 0], k[:, 0], v[:, 0], ld, state.clone())
+    side = torch.cuda.Stream()
+    calls = [
+        lambda: (m3.linattn_chunked_fwd(q, k, v, ld, stream=side)[0], ref),
+        lambda: (m3.linattn_chunked_bwd(q, k, v, ld, v, stream=side)["dk"], gref["dk"]),
+        lambda: (m3.group_norm_fwd(x, 4, w, stream=side)[0], nref),
+        lambda: (m3.group_norm_bwd(x, x, mean, rstd, 4, w, stream=side)["dx"], bref["dx"]),
+        lambda: (m3.linattn_step_decode(q[:, 0], k[:, 0], v[:, 0], ld, state, stream=side), sref),
+    ]
+    for call in calls:
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(20_000_000)                        # ~10 ms of the current stream
+        for _ in range(8):
+            late = [torch.empty_like(t).fill_(7) for t in (ref, sref, gref["dk"], nref)]
+            del late
+        got, want = call()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_incoming_gradients_that_start_anywhere():
+    """torch.cat hands back slices of one gradient: contiguous, but not on 16
+    bytes."""
+    for dtype in (torch.float32, torch.bfloat16):
+        g = torch.Generator(device="cuda").manual_seed(6)
+        q, k, v = (torch.randn(1, 33, 2, 24, generator=g, device="cuda").to(dtype).requires_grad_() for _ in range(3))
+        ld = torch.full((2,), -0.1, device="cuda")
+        w = torch.randn(48, generator=g, device="cuda").requires_grad_()
+        first = torch.zeros(3, device="cuda", dtype=dtype, requires_grad=True)
+        up = torch.randn(3 + 33 * 48, generator=g, device="cuda").to(dtype)
+
+        def grads(cat):
+            y, s = linear_attention(q, k, v, ld)
+            z = group_norm(y.reshape(33, 48), 2, w)
+            for out in (y, z):
+                flat = out.reshape(-1)
+                loss = (torch.cat([first, flat]) * up).sum() if cat else (flat * up[3:].clone()).sum()
+                up_s = torch.ones(s.numel() + 1, device="cuda")
+                loss = loss.float() + ((torch.cat([first[:1].float(), s.reshape(-1)]) * up_s).sum() if cat else s.sum())
+                yield torch.autograd.grad(loss, (q, k, v) if out is y else (q, k, v, w), retain_graph=True)
+
+        for a, b in zip(grads(True), grads(False)):
+            assert all(torch.equal(x, z) for x, z in zip(a, b))
