@@ -247,7 +247,7 @@ struct HeadSum {
     const float *in[2];
     void *out[2];
     int64_t n;                                            // vectors of an output
-    int rep, d;
+    int rep, d, wide;                                     // columns of a row, and of a row of `in`
 };
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) k_head_sum(HeadSum a) {
@@ -257,12 +257,12 @@ __global__ void __launch_bounds__(256) k_head_sum(HeadSum a) {
     const int w = a.d / VEC;                              // vectors of a row
     const int64_t rg = a.n < (int64_t)1 << 31 ? (unsigned)i / (unsigned)w : i / w;
     const int e = (int)(i - rg * w) * VEC;
-    const float *p = a.in[blockIdx.y] + rg * a.rep * a.d + e;
+    const float *p = a.in[blockIdx.y] + rg * a.rep * a.wide + e;
     float s[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; k++) s[k] = 0.f;
 #pragma unroll 4
-    for (int r = 0; r < a.rep; r++, p += a.d) {
+    for (int r = 0; r < a.rep; r++, p += a.wide) {
         if (VEC == 4) {
             const float4 v = *reinterpret_cast<const float4 *>(p);
             s[0] += v.x; s[VEC - 3] += v.y; s[VEC - 2] += v.z; s[VEC - 1] += v.w;
@@ -413,7 +413,7 @@ cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_head_sum(const float *const in[2], void *const out[2], int count, m3_dtype dt, int64_t rows, int64_t H,
-                            int64_t G, int64_t d, cudaStream_t s) {
+                            int64_t G, int64_t d, int64_t wide, cudaStream_t s) {
     const bool v4 = d % 4 == 0;
     HeadSum a;
     for (int i = 0; i < 2; i++) {
@@ -423,6 +423,7 @@ cudaError_t launch_head_sum(const float *const in[2], void *const out[2], int co
     a.n = rows * G * d / (v4 ? 4 : 1);
     a.rep = (int)(H / G);
     a.d = (int)d;
+    a.wide = (int)wide;
     if (a.n == 0) return cudaSuccess;
     const dim3 grid((unsigned)((a.n + 255) / 256), count);
     if (dt == M3_BF16)

@@ -462,8 +462,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                                : (seg == 0 ? g.m0 + lane * elems : slots + (size_t)(seg - 1) * elems);
             const bool tr = seg == 0 && g.m_trans;
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                M[e] = pair(src && inside(e, 0) ? src[at(e, 0, tr)] : 0.f, src && inside(e, 1) ? src[at(e, 1, tr)] : 0.f);
+            for (int e = 0; e < 8; e++) M[e] = 0ull;
+            if (src) {
+                // all sixteen loads go out before one is looked at: those outside
+                // the state read its last element
+                const size_t last = elems - 1;
+                float x[16];
+#pragma unroll
+                for (int e = 0; e < 16; e++) x[e] = src[inside(e >> 1, e & 1) ? at(e >> 1, e & 1, tr) : last];
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    M[e] = pair(inside(e, 0) ? x[2 * e] : 0.f, inside(e, 1) ? x[2 * e + 1] : 0.f);
+            }
         }
         const int mr = 16 * q + (l32 & 15), mc = l32 >> 4;
         uint32_t mo[2];
@@ -539,12 +549,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             for (int p = 0; p < 16; p++) M[p] = 0ull;
             const bool tr = seg == 0 && g.m_trans;
             if (src && (tr || !pieces)) {
-                if (mine) {
+                const size_t last = elems - 1;          // as in the 64-wide variant
+                float x[32];
 #pragma unroll
-                    for (int p = 0; p < 32; p += 2)
-                        M[p / 2] = pair(p0 + c0 + p < g.dcr ? src[at(p, tr)] : 0.f,
-                                        p0 + c0 + p + 1 < g.dcr ? src[at(p + 1, tr)] : 0.f);
-                }
+                for (int p = 0; p < 32; p++) x[p] = src[mine && p0 + c0 + p < g.dcr ? at(p, tr) : last];
+#pragma unroll
+                for (int p = 0; p < 32; p += 2)
+                    M[p / 2] = pair(mine && p0 + c0 + p < g.dcr ? x[p] : 0.f, mine && p0 + c0 + p + 1 < g.dcr ? x[p + 1] : 0.f);
             } else if (src) {
 #pragma unroll 4
                 for (int r = wr; r < 32; r += 4) {
@@ -644,11 +655,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
 #pragma unroll
         for (int i = 0; i < 4; i++) yo[i] = ybase + mr * 128 + (((2 * i + mc) ^ (mr & 7)) << 4);
         const float si = g.scale_i;
-        // y goes out by TMA, or straight from the registers: in fp32, and where
-        // its rows are no whole 16-byte pieces (then also in single elements,
-        // where they are no whole pairs)
-        const bool direct = g.y_f32 || g.dcr != g.dc, f32 = g.y_f32, even = g.dcr % 2 == 0;
-        const int64_t y0 = ((b * g.T + t_beg) * g.H + h) * g.dcr + p0 + cq;
+        // y in bf16 goes by way of shared memory: from there by TMA, or by its
+        // elements where its rows are no whole 16-byte pieces; y in fp32 (rows
+        // of dc) straight from the registers
+        const bool f32 = g.y_f32, tma = !f32 && g.dcr == g.dc;
+        float *yf = static_cast<float *>(g.y) + ((b * g.T + t_beg) * g.H + h) * g.dc + p0 + cq;
+        __nv_bfloat16 *yh = static_cast<__nv_bfloat16 *>(g.y) + ((b * g.T + t_beg) * g.H + h) * g.dcr + p0;
         for (int c = 0; c < nch; c++) {
             const int pb = c & 1, L = chunk_n(c), t = chunk_t(c);
             if (!wait(B_YFULL + pb, c >> 1, 116)) break;
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             const float fa = ra < L ? pw[rev ? L - 1 - ra : ra + 1] * si : 0.f;
             const float fb = rb < L ? pw[rev ? L - 1 - rb : rb + 1] * si : 0.f;
             const f32x2 fa2 = pair(fa, fa), fb2 = pair(fb, fb);
-            if (!direct) {
+            if (!f32) {
                 if (l32 == 0) tma_store_wait_read();    // the rows of the chunk before are on their way
                 __syncwarp();
             }
@@ -675,34 +687,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     for (int e = 0; e < 8; e++)
                         if (((e & 1) ? rb : ra) >= L) o[e] = 0ull;
                 }
-                if (!direct) {
+                if (!f32) {
                     stmatrix4(yo[2 * hf], round2(o[0]), round2(o[1]), round2(o[2]), round2(o[3]));
                     stmatrix4(yo[2 * hf + 1], round2(o[4]), round2(o[5]), round2(o[6]), round2(o[7]));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
-                        const int row = (e & 1) ? rb : ra, col = 32 * hf + 8 * (e >> 1), left = g.dcr - (p0 + col + cq);
-                        if (left <= 0 || t_beg + t + row >= g.T) continue;
-                        const int64_t at = y0 + (int64_t)(t + row) * g.H * g.dcr + col;
-                        float a, b2;
-                        unpair(o[e], a, b2);
-                        if (f32) {
-                            float *y = static_cast<float *>(g.y) + at;
-                            if (even) {
-                                *reinterpret_cast<f32x2 *>(y) = o[e];
-                            } else {
-                                y[0] = a;
-                                if (left > 1) y[1] = b2;
-                            }
-                        } else {
-                            __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(g.y) + at;
-                            if (even) {
-                                *reinterpret_cast<uint32_t *>(y) = pack_bf16(a, b2);
-                            } else {
-                                y[0] = __float2bfloat16_rn(a);
-                                if (left > 1) y[1] = __float2bfloat16_rn(b2);
-                            }
-                        }
+                        const int row = (e & 1) ? rb : ra, col = 32 * hf + 8 * (e >> 1);
+                        // dc is a multiple of 8: a pair is inside or outside
+                        if (p0 + col + cq < g.dc && t_beg + t + row < g.T)
+                            *reinterpret_cast<f32x2 *>(yf + (int64_t)(t + row) * g.H * g.dc + col) = o[e];
                     }
                 }
             }
@@ -711,19 +705,30 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             __syncwarp();
             if (l32 == 0) {
                 mbar_arrive(bar(B_YEMPTY + pb));
-                if (!direct && t_beg + t + 16 * q < g.T)
+                if (tma && t_beg + t + 16 * q < g.T)
                     tma_store4(&P.my[pi], p0, (int)h, (int)t_beg + t + 16 * q, (int)b, ybase);
             }
             __syncwarp();
+            if (!f32 && !tma) {
+#pragma unroll 1
+                for (int r = 0; r < 16 && t_beg + t + 16 * q + r < g.T; r++) {
+                    const __nv_bfloat16 *in = reinterpret_cast<const __nv_bfloat16 *>(sm + OFF_Y + (16 * q + r) * 128);
+                    __nv_bfloat16 *out = yh + (int64_t)(t + 16 * q + r) * g.H * g.dcr;
+                    for (int p = l32; p < DC && p0 + p < g.dcr; p += 32)
+                        out[p] = in[((((p >> 3) ^ (r & 7)) << 3) | (p & 7))];
+                }
+                __syncwarp();
+            }
         }
         // rows behind the sequence in the segment's chunks that were not walked: zeros
         const int64_t e = t_beg + g.seg_len < g.T ? t_beg + g.seg_len : g.T;
-        const int cols = g.dcr - p0 < DC ? g.dcr - p0 : DC;
+        const int w = f32 ? g.dc : g.dcr, cols = w - p0 < DC ? w - p0 : DC, es = f32 ? 4 : 2;
         for (int64_t t = t_beg + (int64_t)nch * Q + wy; t < e; t += 4) {
-            const int64_t row = ((b * g.T + t) * g.H + h) * g.dcr + p0;
-            for (int p = l32; p < cols; p += 32) {
-                if (f32) static_cast<float *>(g.y)[row + p] = 0.f;
-                else static_cast<__nv_bfloat16 *>(g.y)[row + p] = __float2bfloat16_rn(0.f);
+            uint8_t *row = static_cast<uint8_t *>(g.y) + (((b * g.T + t) * g.H + h) * w + p0) * es;
+            if (f32 || tma) {
+                for (int v = l32; v < cols * es / 16; v += 32) reinterpret_cast<uint4 *>(row)[v] = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                for (int p = l32; p < cols; p += 32) reinterpret_cast<uint16_t *>(row)[p] = 0;
             }
         }
         if (l32 == 0) tma_store_wait_all();

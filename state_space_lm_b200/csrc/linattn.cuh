@@ -33,7 +33,7 @@ struct MixArgs {
     float *m_out;                // state after the walk, or NULL
     int m_trans;                 // m0, m_out hold the state transposed, (dcr, dar) instead of (dar, dcr)
     void *y;                     // (Bt, T, H, dcr), or NULL when only m_out is wanted
-    int y_f32;                   // y in fp32 (else the input type)
+    int y_f32;                   // y in fp32, rows of dc elements (else the input type, rows of dcr)
     int64_t Bt, T, H;
     int reverse;
     float scale_p, scale_i, scale_w;
@@ -109,9 +109,10 @@ struct PadArgs {
     int count;
 };
 cudaError_t launch_pad_rows(const PadArgs &a, cudaStream_t s);
-// sums one or two fp32 (Bt, T, H, d) tensors over the heads of each of G groups
+// sums one or two fp32 (Bt, T, H, wide) tensors over the heads of each of G
+// groups; d of the wide columns are real
 cudaError_t launch_head_sum(const float *const in[2], void *const out[2], int count, m3_dtype dt, int64_t rows, int64_t H,
-                            int64_t G, int64_t d, cudaStream_t s);
+                            int64_t G, int64_t d, int64_t wide, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinStepArgs &a, m3_dtype dt, cudaStream_t s);
 
 }  // namespace m3

@@ -568,9 +568,9 @@ PadArgs pad_rows(const m3_linattn_dims &d, const LinGeo &o, const LinPads &pd, c
     if (dy) add(*dy, pd.dy, d.nheads * d.headdim, d.nheads, d.headdim, pd.dv);
     return a;
 }
-// bytes of one gradient of shared heads, per head in fp32
-size_t head_bytes(const m3_linattn_dims &d, const LinGeo &o) {
-    return o.G == d.nheads ? 0 : align256((size_t)d.batch * d.seqlen * d.nheads * d.dstate * sizeof(float));
+// bytes of one gradient of shared heads, per head in fp32, in padded rows
+size_t head_bytes(const m3_linattn_dims &d, const LinGeo &o, const LinPads &pd) {
+    return o.G == d.nheads ? 0 : align256((size_t)d.batch * d.seqlen * d.nheads * pd.dk * sizeof(float));
 }
 inline bool tma_aligned(const void *q, const void *k, const void *v) { return aligned16(q) && aligned16(k) && aligned16(v); }
 }  // namespace
@@ -590,7 +590,7 @@ size_t m3_linattn_workspace_bytes(int which, m3_linattn_dims d, m3_dtype dtype) 
         plan_mixes(p, dtype, aligned);
         if (p.bytes > most) most = p.bytes;
     }
-    return most + (bwd ? 2 * head_bytes(d, o) + pd.bytes : pd.on ? pd.dy : 0);
+    return most + (bwd ? 2 * head_bytes(d, o, pd) + pd.bytes : pd.on ? pd.dy : 0);
 }
 
 m3_status m3_linattn_chunked_fwd(const void *q, const void *k, const void *v, m3_dtype dtype, const float *log_decay,
@@ -671,7 +671,7 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
     const LinPads pd = pads_of(d, o, dtype);
     LinPlan p = bwd_mixes(d, o, pd, dtype);
     plan_mixes(p, dtype, pd.on || tma_aligned(q, k, v));
-    const size_t hb = head_bytes(d, o);
+    const size_t hb = head_bytes(d, o, pd);
     const bool shared = hb > 0;
     char *heads = static_cast<char *>(workspace) + p.bytes;
     PadArgs pads{};
@@ -713,7 +713,7 @@ m3_status m3_linattn_chunked_bwd(const void *q, const void *k, const void *v, m3
         cudaError_t e = launch_pad_rows(pads, s);
         if (e == cudaSuccess) e = launch_mixes(p, dtype, workspace, s);
         if (e == cudaSuccess && ns > 0)
-            e = launch_head_sum(sum_in, sum_out, ns, dtype, d.batch * d.seqlen, d.nheads, o.G, d.dstate, s);
+            e = launch_head_sum(sum_in, sum_out, ns, dtype, d.batch * d.seqlen, d.nheads, o.G, d.dstate, pd.dk, s);
         return e;
     });
 }
