@@ -180,8 +180,10 @@ __global__ void __launch_bounds__(ST) k_mix_simt(MixArgs g) {
     if (!SO && col && g.y) {
         // rows behind the sequence, inside this segment: zeros
         const int64_t e = t0 + g.seg_len < g.T ? t0 + g.seg_len : g.T;
-        for (int64_t t = t0 + n + w; t < e; t += 8) {
-            const int64_t o = ((row0 + t) * g.H + h) * g.dc + pc;
+        const int64_t step = 8 * g.H * g.dc;
+        int64_t o = ((row0 + t0 + n + w) * g.H + h) * g.dc + pc;
+#pragma unroll 4
+        for (int64_t t = t0 + n + w; t < e; t += 8, o += step) {
             if (g.y_f32) stf(static_cast<float *>(g.y), o, 0.f);
             else stf(static_cast<T *>(g.y), o, 0.f);
         }

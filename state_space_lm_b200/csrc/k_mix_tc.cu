@@ -710,25 +710,57 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             }
             __syncwarp();
             if (!f32 && !tma) {
-#pragma unroll 1
-                for (int r = 0; r < 16 && t_beg + t + 16 * q + r < g.T; r++) {
-                    const __nv_bfloat16 *in = reinterpret_cast<const __nv_bfloat16 *>(sm + OFF_Y + (16 * q + r) * 128);
-                    __nv_bfloat16 *out = yh + (int64_t)(t + 16 * q + r) * g.H * g.dcr;
-                    for (int p = l32; p < DC && p0 + p < g.dcr; p += 32)
-                        out[p] = in[((((p >> 3) ^ (r & 7)) << 3) | (p & 7))];
+                // row by row, in pairs where a row is whole pairs
+                const int64_t left = g.T - (t_beg + t + 16 * q), step = (int64_t)g.H * g.dcr;
+                const int rows = left < 16 ? (int)left : 16, cols = g.dcr - p0;
+                __nv_bfloat16 *out = yh + (t + 16 * q) * step;
+                const uint8_t *in = sm + OFF_Y + 16 * q * 128;
+                auto piece = [&](int r, int p) { return in + r * 128 + (((p >> 3) ^ (r & 7)) << 4) + 2 * (p & 7); };
+                if (g.dcr % 2 == 0) {
+#pragma unroll 4
+                    for (int r = 0; r < rows; r++)
+                        if (2 * l32 < cols)
+                            *reinterpret_cast<uint32_t *>(out + r * step + 2 * l32) =
+                                *reinterpret_cast<const uint32_t *>(piece(r, 2 * l32));
+                } else {
+#pragma unroll 2
+                    for (int r = 0; r < rows; r++) {
+                        if (l32 < cols) out[r * step + l32] = *reinterpret_cast<const __nv_bfloat16 *>(piece(r, l32));
+                        if (l32 + 32 < cols)
+                            out[r * step + l32 + 32] = *reinterpret_cast<const __nv_bfloat16 *>(piece(r, l32 + 32));
+                    }
                 }
                 __syncwarp();
             }
         }
-        // rows behind the sequence in the segment's chunks that were not walked: zeros
-        const int64_t e = t_beg + g.seg_len < g.T ? t_beg + g.seg_len : g.T;
-        const int w = f32 ? g.dc : g.dcr, cols = w - p0 < DC ? w - p0 : DC, es = f32 ? 4 : 2;
-        for (int64_t t = t_beg + (int64_t)nch * Q + wy; t < e; t += 4) {
-            uint8_t *row = static_cast<uint8_t *>(g.y) + (((b * g.T + t) * g.H + h) * w + p0) * es;
-            if (f32 || tma) {
-                for (int v = l32; v < cols * es / 16; v += 32) reinterpret_cast<uint4 *>(row)[v] = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                for (int p = l32; p < cols; p += 32) reinterpret_cast<uint16_t *>(row)[p] = 0;
+        // rows behind the sequence in the segment's chunks that were not walked:
+        // zeros, 16 rows a TMA store (8 x 2048 tokens, 16 heads, 100 tokens each:
+        // 70 us with one row a warp and store)
+        const int64_t z0 = t_beg + (int64_t)nch * Q, e = t_beg + g.seg_len < g.T ? t_beg + g.seg_len : g.T;
+        if (z0 < e && tma) {
+            if (l32 == 0) tma_store_wait_read();
+            __syncwarp();
+            for (int v = l32; v < 128; v += 32)
+                *reinterpret_cast<uint4 *>(sm + OFF_Y + 16 * q * 128 + 16 * v) = make_uint4(0u, 0u, 0u, 0u);
+            fence_async_smem();
+            __syncwarp();
+            if (l32 == 0)
+                for (int64_t t = z0 + 16 * q; t < e; t += 64) tma_store4(&P.my[pi], p0, (int)h, (int)t, (int)b, ybase);
+        } else if (f32) {
+            const int pieces = (g.dc - p0 < DC ? g.dc - p0 : DC) / 4, pk = l32 & 15;
+            float *row = static_cast<float *>(g.y) + ((b * g.T + z0 + 2 * wy + (l32 >> 4)) * g.H + h) * g.dc + p0 + 4 * pk;
+            const int64_t step = 8 * g.H * g.dc;
+#pragma unroll 4
+            for (int64_t t = z0 + 2 * wy + (l32 >> 4); t < e; t += 8, row += step)
+                if (pk < pieces) *reinterpret_cast<float4 *>(row) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if (!tma) {
+            uint16_t *row = static_cast<uint16_t *>(g.y) + ((b * g.T + z0 + wy) * g.H + h) * g.dcr + p0 + l32;
+            const int left = g.dcr - p0 - l32;
+            const int64_t step = 4 * g.H * g.dcr;
+#pragma unroll 4
+            for (int64_t t = z0 + wy; t < e; t += 4, row += step) {
+                if (left > 0) row[0] = 0;
+                if (left > 32) row[32] = 0;
             }
         }
         if (l32 == 0) tma_store_wait_all();
