@@ -106,6 +106,7 @@ struct PadArgs {
     void *dst[4];                // (rows, heads, (d + 7) / 8 * 8), contiguous, 16-byte aligned
     int64_t ld[4], n[4];         // n: 8-column pieces of dst
     int heads[4], d[4];
+    int vec[4];                  // elements of a load, as rows and base allow (launch_pad_rows sets it)
     int count;
 };
 cudaError_t launch_pad_rows(const PadArgs &a, cudaStream_t s);
