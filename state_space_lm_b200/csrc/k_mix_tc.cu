@@ -29,6 +29,14 @@
 // A split time axis takes two passes: B and C alone for every segment's own
 // state, the combine of linattn.cuh, then all segments at once.
 //
+// Measured: 8 x 2048 tokens, 16 heads of 128 x 64, 45 us for 206 MB (69 % of the
+// copy rate), on 128 of the 148 SMs; the backward's dq and dk 143 us, dv 45.
+// Bound by the shared memory pipe: a chunk takes 2225 cycles, and the tensor
+// core's operands, the epilogues and TMA need about 2290 cycles of it between
+// them.  One persistent CTA to an SM instead of one to a lane was slower at
+// long sequences (220 us for the backward, 195 here) and faster at hundreds of
+// single chunks (512 x 64 tokens: 288 us, 338 here).
+//
 // The problems of a call (three in the backward) share one launch.  Every
 // wait is bounded: past ~1 s the kernel records the site, stops issuing work,
 // drains what it has in flight and returns.
@@ -655,12 +663,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
 #pragma unroll
         for (int i = 0; i < 4; i++) yo[i] = ybase + mr * 128 + (((2 * i + mc) ^ (mr & 7)) << 4);
         const float si = g.scale_i;
-        // y in bf16 goes by way of shared memory: from there by TMA, or by its
-        // elements where its rows are no whole 16-byte pieces; y in fp32 (rows
-        // of dc) straight from the registers
-        const bool f32 = g.y_f32, tma = !f32 && g.dcr == g.dc;
-        float *yf = static_cast<float *>(g.y) + ((b * g.T + t_beg) * g.H + h) * g.dc + p0 + cq;
+        // y goes by way of shared memory: from there by TMA, 64 columns of bf16
+        // or 32 of fp32 (whose stores from registers, 32 bytes of a row each, took
+        // 254 us where these take 170: 8 x 2048 tokens, 16 heads over 4 groups, dq
+        // and dk), or by its elements where bf16 rows are no whole 16-byte pieces
+        const bool f32 = g.y_f32, tma = f32 || g.dcr == g.dc;
         __nv_bfloat16 *yh = static_cast<__nv_bfloat16 *>(g.y) + ((b * g.T + t_beg) * g.H + h) * g.dcr + p0;
+        auto store = [&](int col, int64_t t) {          // the staged rows, as rows t of y
+            if (l32 == 0 && p0 + col < g.dc && t < g.T) tma_store4(&P.my[pi], p0 + col, (int)h, (int)t, (int)b, ybase);
+        };
         for (int c = 0; c < nch; c++) {
             const int pb = c & 1, L = chunk_n(c), t = chunk_t(c);
             if (!wait(B_YFULL + pb, c >> 1, 116)) break;
@@ -668,10 +679,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             const float fa = ra < L ? pw[rev ? L - 1 - ra : ra + 1] * si : 0.f;
             const float fb = rb < L ? pw[rev ? L - 1 - rb : rb + 1] * si : 0.f;
             const f32x2 fa2 = pair(fa, fa), fb2 = pair(fb, fb);
-            if (!f32) {
-                if (l32 == 0) tma_store_wait_read();    // the rows of the chunk before are on their way
-                __syncwarp();
-            }
 #pragma unroll
             for (int hf = 0; hf < 2; hf++) {
                 float y2[16], y3[16];
@@ -687,29 +694,31 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                     for (int e = 0; e < 8; e++)
                         if (((e & 1) ? rb : ra) >= L) o[e] = 0ull;
                 }
+                if (f32 || hf == 0) {                   // what was staged before is on its way
+                    if (l32 == 0) tma_store_wait_read();
+                    __syncwarp();
+                }
                 if (!f32) {
                     stmatrix4(yo[2 * hf], round2(o[0]), round2(o[1]), round2(o[2]), round2(o[3]));
                     stmatrix4(yo[2 * hf + 1], round2(o[4]), round2(o[5]), round2(o[6]), round2(o[7]));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
-                        const int row = (e & 1) ? rb : ra, col = 32 * hf + 8 * (e >> 1);
-                        // dc is a multiple of 8: a pair is inside or outside
-                        if (p0 + col + cq < g.dc && t_beg + t + row < g.T)
-                            *reinterpret_cast<f32x2 *>(yf + (int64_t)(t + row) * g.H * g.dc + col) = o[e];
+                        const int r = (l32 >> 2) + 8 * (e & 1), k = 2 * (e >> 1) + ((l32 >> 1) & 1);
+                        *reinterpret_cast<f32x2 *>(sm + OFF_Y + (16 * q + r) * 128 + ((k ^ (r & 7)) << 4) + 8 * (l32 & 1)) = o[e];
                     }
+                    fence_async_smem();
+                    __syncwarp();
+                    store(32 * hf, t_beg + t + 16 * q);
                 }
             }
             tc_fence_before();
             fence_async_smem();
             __syncwarp();
-            if (l32 == 0) {
-                mbar_arrive(bar(B_YEMPTY + pb));
-                if (tma && t_beg + t + 16 * q < g.T)
-                    tma_store4(&P.my[pi], p0, (int)h, (int)t_beg + t + 16 * q, (int)b, ybase);
-            }
+            if (l32 == 0) mbar_arrive(bar(B_YEMPTY + pb));
+            if (!f32 && tma) store(0, t_beg + t + 16 * q);
             __syncwarp();
-            if (!f32 && !tma) {
+            if (!tma) {
                 // row by row, in pairs where a row is whole pairs
                 const int64_t left = g.T - (t_beg + t + 16 * q), step = (int64_t)g.H * g.dcr;
                 const int rows = left < 16 ? (int)left : 16, cols = g.dcr - p0;
@@ -734,7 +743,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             }
         }
         // rows behind the sequence in the segment's chunks that were not walked:
-        // zeros, 16 rows a TMA store (8 x 2048 tokens, 16 heads, 100 tokens each:
+        // zeros, 16 rows a store (8 x 2048 tokens, 16 heads, 100 tokens each:
         // 70 us with one row a warp and store)
         const int64_t z0 = t_beg + (int64_t)nch * Q, e = t_beg + g.seg_len < g.T ? t_beg + g.seg_len : g.T;
         if (z0 < e && tma) {
@@ -744,16 +753,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 *reinterpret_cast<uint4 *>(sm + OFF_Y + 16 * q * 128 + 16 * v) = make_uint4(0u, 0u, 0u, 0u);
             fence_async_smem();
             __syncwarp();
-            if (l32 == 0)
-                for (int64_t t = z0 + 16 * q; t < e; t += 64) tma_store4(&P.my[pi], p0, (int)h, (int)t, (int)b, ybase);
-        } else if (f32) {
-            const int pieces = (g.dc - p0 < DC ? g.dc - p0 : DC) / 4, pk = l32 & 15;
-            float *row = static_cast<float *>(g.y) + ((b * g.T + z0 + 2 * wy + (l32 >> 4)) * g.H + h) * g.dc + p0 + 4 * pk;
-            const int64_t step = 8 * g.H * g.dc;
-#pragma unroll 4
-            for (int64_t t = z0 + 2 * wy + (l32 >> 4); t < e; t += 8, row += step)
-                if (pk < pieces) *reinterpret_cast<float4 *>(row) = make_float4(0.f, 0.f, 0.f, 0.f);
-        } else if (!tma) {
+            for (int64_t t = z0 + 16 * q; t < e; t += 64) {
+                store(0, t);
+                if (f32) store(32, t);
+            }
+        } else {
             uint16_t *row = static_cast<uint16_t *>(g.y) + ((b * g.T + z0 + wy) * g.H + h) * g.dcr + p0 + l32;
             const int left = g.dcr - p0 - l32;
             const int64_t step = 4 * g.H * g.dcr;
@@ -797,17 +801,18 @@ static EncodeFn encode_fn() {
     return fn;
 }
 
-// bf16 rows (Bt, T, heads, d) with ld elements from token to token: boxes of
-// 64 columns and `rows` tokens, zeros outside
+// bf16 (or fp32) rows (Bt, T, heads, d) with ld elements from token to token:
+// boxes of 128 bytes of `rows` tokens, zeros outside
 static bool rows_map(CUtensorMap *m, const void *base, int64_t d, int64_t heads, int64_t T, int64_t Bt, int64_t ld,
-                     uint32_t rows) {
+                     uint32_t rows, bool f32 = false) {
+    const int64_t size = f32 ? 4 : 2;
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)Bt};
-    const cuuint64_t strides[3] = {(cuuint64_t)(d * 2), (cuuint64_t)(ld * 2), (cuuint64_t)(ld * T * 2)};
-    const cuuint32_t box[4] = {64, 1, rows, 1}, es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t strides[3] = {(cuuint64_t)(d * size), (cuuint64_t)(ld * size), (cuuint64_t)(ld * T * size)};
+    const cuuint32_t box[4] = {(cuuint32_t)(128 / size), 1, rows, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims,
+              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -823,7 +828,7 @@ bool mix_tc_sizes(const MixArgs &g, m3_dtype dt) {
     if (g.T <= 16 && g.Bt * g.H <= 256) return false;
     if (g.Bt * g.H > (int64_t)1 << 28) return false;      // three problems of two column tiles share a 1-D grid
     // a TMA stride is a multiple of 16 bytes below 2^40
-    for (int64_t ld : {g.lda, g.ldb, g.ldc})
+    for (int64_t ld : {g.lda, g.ldb, g.ldc, 2 * g.H * g.dc})
         if (ld % 8 || ld > ((int64_t)1 << 38) / g.T) return false;
     return true;
 }
@@ -927,7 +932,8 @@ cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
             if (!rows_map(&P.ma[k], a.a, a.da, a.H / a.ra, a.T, a.Bt, a.lda, Q) ||
                 !rows_map(&P.mb[k], a.b, a.da, a.H / a.rb, a.T, a.Bt, a.ldb, Q) ||
                 !rows_map(&P.mc[k], a.c, a.dc, a.H / a.rc, a.T, a.Bt, a.ldc, Q) ||
-                (a.y && !a.y_f32 && a.dcr == a.dc && !rows_map(&P.my[k], a.y, a.dc, a.H, a.T, a.Bt, a.H * a.dc, 16)))
+                (a.y && (a.y_f32 || a.dcr == a.dc) &&
+                 !rows_map(&P.my[k], a.y, a.dc, a.H, a.T, a.Bt, a.H * a.dc, 16, a.y_f32)))
                 return cudaErrorInvalidValue;
             P.g[k] = a;
             split |= a.nseg > 1;
