@@ -4,12 +4,13 @@
 // that one's programmatic dependents: their set-up passes while the kernel
 // before them drains (group norm over sequences, backward, 8 x 2048 x 1024: 51
 // to 47 us).  The passes of the mixes are not: a CTA of theirs holds an SM, and
-// one that waits there was slower.  A kernel calls pdl_trigger() at its start, and pdl_wait() before it
-// reads what the kernels before it in the call wrote (it returns when those
-// have finished, with their memory visible).  The call's first kernel is
-// launched as usual, after everything earlier on the stream; so the call's own
-// inputs may be read before pdl_wait().  Every block of a dependent waits
-// before it ends: then a kernel that has finished says that all before it have.
+// one that waits there was slower.  A kernel calls pdl_trigger() at its start,
+// and pdl_wait() before it reads what the kernels before it in the call wrote
+// (it returns when those have finished, with their memory visible).  The call's
+// first kernel is launched as usual, after everything earlier on the stream; so
+// the call's own inputs may be read before pdl_wait().  Every block of a
+// dependent waits before it ends: then a kernel that has finished says that all
+// before it have.
 #pragma once
 #include "m3_internal.cuh"
 
