@@ -166,6 +166,30 @@ def test_a_nan_stays_out_of_the_chunks_before_it():
             assert bool(torch.isnan(y2[:, 200]).all()), name
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_growing_decays(dtype):
+    d = inputs(2, 200, 3, 3, 64, 48, dtype)
+    d["ld"] = torch.tensor([0.02, 0.001, 0.1], device="cuda")    # up to e^20 over the sequence
+    check_forward(d)
+    check_backward(d)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_tensor_as_q_k_v_and_dy(dtype):
+    d = inputs(2, 150, 3, 3, 64, 64, dtype)
+    d["q"] = d["k"] = d["dy"] = d["v"]
+    check_forward(d)
+    check_backward(d)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_most_heads(dtype):
+    d = inputs(1, 20, 4096, 64, 8, 8, dtype)
+    check_forward(d)
+    check_backward(d)
+    m3.linattn_step_decode(d["q"][:, 0], d["k"][:, 0], d["v"][:, 0], d["ld"], d["s0"])
+
+
 def test_lengths_outside_the_range_are_taken_into_it():
     d = inputs(3, 40, 2, 2, 64, 64, "bf16")
     d["lengths"] = torch.tensor([-5, 999, 40], dtype=torch.int32, device="cuda")

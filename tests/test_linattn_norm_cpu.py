@@ -3,6 +3,7 @@ library's own refusals (no call here passes validation, or it enqueues
 nothing), and the autograd wrappers' plumbing with a 64-bit stand-in for the
 library."""
 import ctypes
+import types
 
 import pytest
 import torch
@@ -138,6 +139,16 @@ def test_binding_checks_linattn():
         m3.linattn_chunked_bwd(q, q, v, ld, dy, out={"ds0": S.bfloat16()})
     with pytest.raises(ValueError, match=": s has"):
         m3.linattn_step_decode(q[:, 0], q[:, 0], v[:, 0], ld, S[:1])
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    for call in (lambda: m3.linattn_chunked_fwd(q, q, v, ld, stream=other),
+                 lambda: m3.linattn_chunked_bwd(q, q, v, ld, dy, stream=other),
+                 lambda: m3.linattn_step_decode(q[:, 0], q[:, 0], v[:, 0], ld, S, stream=other),
+                 lambda: m3.group_norm_fwd(dy, 4, stream=other),
+                 lambda: m3.group_norm_bwd(dy, dy, z(2, 4), z(2, 4), 4, stream=other)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
+    with pytest.raises(ValueError, match="0 wide"):
+        m3.linattn_chunked_fwd(z(2, 6, 2, 0), z(2, 6, 2, 0), v, ld)
     # what the binding takes as it is: slices of a fused projection, one token of a longer tensor
     flat = z(2, 6, 100)
     a, b, c = flat[..., :16].unflatten(-1, (2, 8)), flat[..., 16:32].unflatten(-1, (2, 8)), flat[..., 36:100].unflatten(-1, (4, 16))
