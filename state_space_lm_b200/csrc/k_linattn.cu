@@ -20,14 +20,14 @@ namespace {
 // block.  This is the path of fp32 inputs, whose products the tensor cores
 // would round, and of sizes that TMA cannot address.  Bound by the chain of a
 // lane's blocks at small sizes (3 x 333 tokens, 5 heads of 37 x 29, cut into
-// segments: 24 us), by arithmetic and shared-memory reads at large ones (8 x 2048,
-// 16 heads of 128 x 64: 850 us forward).
+// segments: 23 us), by arithmetic and shared-memory reads at large ones (8 x 2048,
+// 16 heads of 128 x 64: 712 us forward).
 constexpr int SC = 16, SP = 32, ST = 256;
 
 template <int RS>
 struct SimtSmem {
     static constexpr int DA = 8 * RS, LDA = DA + 4;     // row padding: conflict-free 16-byte reads down a column
-    float a[SC][LDA], b[SC][LDA], c[SC][SP], p[SC][SC + 1], part[8][SC][SP];
+    float a[SC][LDA], b[SC][LDA], c[SC][SP], p[SC][SC + 4], part[8][SC][SP], sp[8][SC][SC + 4];
     float pw[SC + 1], pm1[SC + 1];
 };
 
@@ -103,20 +103,26 @@ __global__ void __launch_bounds__(ST) k_mix_simt(MixArgs g) {
         if (j0 + SC < n) fetch(j0 + SC);
         if (!SO) {
             {
-                const int j = tid >> 4, i = tid & 15;
-                if (i <= j) {
-                    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll 4
-                    for (int k = 0; k < Sm::DA; k += 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(&sm.a[j][k]);
-                        const float4 z = *reinterpret_cast<const float4 *>(&sm.b[i][k]);
-                        s0 = fmaf(x.x, z.x, s0);
-                        s1 = fmaf(x.y, z.y, s1);
-                        s2 = fmaf(x.z, z.z, s2);
-                        s3 = fmaf(x.w, z.w, s3);
+                // scores over this warp's rows of the state: a lane takes one row of
+                // a against 8 of b, so that most reads are broadcasts
+                const int j = l >> 1, i0 = (l & 1) * 8;
+                float acc[8];
+#pragma unroll
+                for (int u = 0; u < 8; u++) acc[u] = 0.f;
+#pragma unroll
+                for (int k = 0; k < RS; k += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.a[j][w * RS + k]);
+#pragma unroll
+                    for (int u = 0; u < 8; u++) {
+                        const float4 z = *reinterpret_cast<const float4 *>(&sm.b[i0 + u][w * RS + k]);
+                        acc[u] = fmaf(x.x, z.x, acc[u]);
+                        acc[u] = fmaf(x.y, z.y, acc[u]);
+                        acc[u] = fmaf(x.z, z.z, acc[u]);
+                        acc[u] = fmaf(x.w, z.w, acc[u]);
                     }
-                    sm.p[j][i] = ((s0 + s1) + (s2 + s3)) * (sm.pw[j - i] * g.scale_p);
                 }
+                *reinterpret_cast<float4 *>(&sm.sp[w][j][i0]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                *reinterpret_cast<float4 *>(&sm.sp[w][j][i0 + 4]) = make_float4(acc[4], acc[5], acc[6], acc[7]);
             }
 #pragma unroll 4
             for (int j = 0; j < SC; j++) {
@@ -154,15 +160,32 @@ __global__ void __launch_bounds__(ST) k_mix_simt(MixArgs g) {
         }
         if (!SO) {
             __syncthreads();
+            {
+                const int j = tid >> 4, i = tid & 15;
+                float t = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; k++) t += sm.sp[k][j][i];
+                sm.p[j][i] = t * (sm.pw[max(0, j - i)] * g.scale_p);
+            }
+            __syncthreads();
+            // rows j = w and w + 8 of this thread's column
+            float inter[2] = {0.f, 0.f}, intra[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                inter[0] += sm.part[k][w][l];
+                inter[1] += sm.part[k][w + 8][l];
+            }
+#pragma unroll
+            for (int i = 0; i < SC; i++) {                // later rows are left out, not multiplied by zero
+                const float c = sm.c[i][l];
+                if (i <= w) intra[0] = fmaf(sm.p[w][i], c, intra[0]);
+                if (i <= w + 8) intra[1] = fmaf(sm.p[w + 8][i], c, intra[1]);
+            }
 #pragma unroll
             for (int u = 0; u < 2; u++) {
                 const int j = w + 8 * u;
                 if (j < L && col && g.y) {
-                    float inter = 0.f, intra = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; k++) inter += sm.part[k][j][l];
-                    for (int i = 0; i <= j; i++) intra = fmaf(sm.p[j][i], sm.c[i][l], intra);
-                    const float y = fmaf(inter, sm.pw[g.reverse ? j : j + 1] * g.scale_i, intra);
+                    const float y = fmaf(inter[u], sm.pw[g.reverse ? j : j + 1] * g.scale_i, intra[u]);
                     const int64_t t = row0 + (g.reverse ? t0 + n - 1 - (j0 + j) : t0 + j0 + j);
                     const int64_t o = (t * g.H + h) * g.dc + pc;
                     if (g.y_f32) stf(static_cast<float *>(g.y), o, y);
@@ -415,26 +438,38 @@ cudaError_t launch_mix_simt_d(const MixArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-// Split the time axis when the lanes' column tiles leave SMs idle: enough
-// segments for about four CTAs per SM, at least 32 tokens each (a segment
-// costs a state written and read, and its tokens' b and c twice), at most 64
-// segments and 64 MB of states.  (3 x 333 tokens, 5 heads of 37 x 29, fp32:
-// 64 us in one piece of each lane, 31 us in five.)
+// Split the time axis where it pays: the second pass repeats 0.4 of the first
+// one's work (without answers), but lanes that leave SMs idle fill them.  Costs
+// are counted in blocks of 16 tokens, plus 2 to a CTA and 3 to the launches
+// between; m CTAs on an SM take 1 + 0.4 (m - 1) of one's time, up to the number
+// that its registers hold.  At most 64 segments and 64 MB of states.
+// Measured against one piece of each lane: 3 x 333 tokens, 5 heads of 37 x 29:
+// 53 us, 24 in seven; 2 x 1000, 4 of 128 x 128: 252 us, 70 in nine (one wave), 95
+// in eleven (two); 8 x 2048, 16 of 128 x 64: 712 us, 850 in two.
 void mix_simt_plan(MixArgs &a) {
     a.nseg = 1;
     a.seg_len = a.T > 0 ? a.T : 1;
-    const int64_t lanes = a.Bt * a.H, ctas = lanes * ((a.dc + SP - 1) / SP);
+    const int64_t lanes = a.Bt * a.H, ctas = lanes * ((a.dc + SP - 1) / SP), nb = (a.T + SC - 1) / SC;
     if (lanes == 0 || ctas >= 296 || a.T < 96) return;
-    int64_t ns = 592 / ctas;
-    if (ns > a.T / 32) ns = a.T / 32;
-    if (ns > 64) ns = 64;
+    const int most_cta = a.da <= 32 ? 4 : a.da <= 64 ? 3 : a.da <= 128 ? 2 : 1;
+    auto cost = [&](int64_t n, double len) {
+        const int64_t wave = 148 * most_cta, rest = n % wave;
+        double c = (double)(n / wave) * (1 + 0.4 * (most_cta - 1));
+        if (rest > 0) c += 1 + 0.4 * (double)((rest + 147) / 148 - 1);
+        return c * (len + 2);
+    };
     const int64_t most = ((int64_t)64 << 20) / (lanes * a.da * a.dc * 4) + 1;
-    if (ns > most) ns = most;
-    if (ns < 2) return;
-    int64_t len = (a.T + ns - 1) / ns;
-    len = (len + SC - 1) / SC * SC;
-    a.nseg = (int)((a.T + len - 1) / len);
-    a.seg_len = len;
+    double best = cost(ctas, (double)nb);
+    for (int64_t ns = 2; ns <= 64 && ns <= most; ns++) {
+        const int64_t len = (nb + ns - 1) / ns, k = (nb + len - 1) / len;
+        if (len < 2) break;
+        const double c = cost(ctas * k, (double)len) + cost(ctas * (k - 1), 0.4 * (double)len) + 3;
+        if (k > 1 && c < best) {
+            best = c;
+            a.nseg = (int)k;
+            a.seg_len = len * SC;
+        }
+    }
 }
 
 cudaError_t launch_mix_simt(const MixArgs &a, m3_dtype dt, cudaStream_t s) {
