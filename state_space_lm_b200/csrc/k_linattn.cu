@@ -1,6 +1,8 @@
 // k_linattn.cu -- linear attention with a decay for each head: the fp32
 // kernel for every size and type, the combine of a split time axis, the sum
 // of per-head gradients over shared heads, and the single-token step.
+#include <algorithm>
+
 #include "launch.cuh"
 #include "linattn.cuh"
 
@@ -20,8 +22,8 @@ namespace {
 // block.  This is the path of fp32 inputs, whose products the tensor cores
 // would round, and of sizes that TMA cannot address.  Bound by the chain of a
 // lane's blocks at small sizes (3 x 333 tokens, 5 heads of 37 x 29, cut into
-// segments: 23 us), by arithmetic and shared-memory reads at large ones (8 x 2048,
-// 16 heads of 128 x 64: 712 us forward).
+// segments: 24 us), by arithmetic and shared-memory reads at large ones (8 x 2048,
+// 16 heads of 128 x 64: 673 us forward, 2214 backward).
 constexpr int SC = 16, SP = 32, ST = 256;
 
 template <int RS>
@@ -31,9 +33,19 @@ struct SimtSmem {
     float pw[SC + 1], pm1[SC + 1];
 };
 
-template <typename T, int RS, bool SO>
-__global__ void __launch_bounds__(ST) k_mix_simt(MixArgs g) {
+// The mixes of a launch (blockIdx.z): the backward's three, or those of them
+// that have the same width.  A single one has a variant of its own, whose
+// arguments stand at fixed places (3 % of the forward).
+template <int NB>
+struct MixBatch {
+    MixArgs g[NB];
+};
+
+template <typename T, int RS, bool SO, int NB>
+__global__ void __launch_bounds__(ST, RS <= 4 ? 4 : RS <= 8 ? 3 : RS <= 16 ? 2 : 1) k_mix_simt(const __grid_constant__ MixBatch<NB> P) {
     using Sm = SimtSmem<RS>;
+    const MixArgs &g = P.g[NB == 1 ? 0 : blockIdx.z];
+    if ((int)blockIdx.y * SP >= g.dc) return;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
@@ -221,8 +233,9 @@ __global__ void __launch_bounds__(ST) k_mix_simt(MixArgs g) {
 //   M_(j+1) = g^n_j M_j + own_j.
 // One thread per state element; bound by the slots' bytes, read and written
 // once each.
-__global__ void __launch_bounds__(256) k_mix_combine(MixArgs g) {
+__global__ void __launch_bounds__(256) k_mix_combine(const __grid_constant__ MixBatch<3> P) {
     __shared__ float dm1[256];
+    const MixArgs &g = P.g[blockIdx.z];
     const int64_t lane = blockIdx.x, bi = lane / g.H, h = lane % g.H;
     const int64_t len = lane_length(g.lengths, bi, g.T);
     const double lg = (double)g.log_decay[h];
@@ -405,35 +418,47 @@ __global__ void __launch_bounds__(256) k_lin_step(LinStepArgs a) {
     }
 }
 
-template <typename T, int RS>
-cudaError_t launch_mix_simt_t(const MixArgs &a, cudaStream_t s) {
+template <typename T, int RS, int NB>
+cudaError_t launch_mix_simt_t(const MixArgs *m, int n, cudaStream_t s) {
     constexpr int smem = (int)sizeof(SimtSmem<RS>);
-    const int64_t lanes = a.Bt * a.H;
-    const unsigned tiles = (unsigned)((a.dc + SP - 1) / SP);
+    const int64_t lanes = m[0].Bt * m[0].H;
+    const int nseg = m[0].nseg;
+    unsigned tiles = 1;
+    MixBatch<NB> b;
+    for (int i = 0; i < n; i++) {
+        b.g[i] = m[i];
+        tiles = std::max(tiles, (unsigned)((m[i].dc + SP - 1) / SP));
+    }
     cudaError_t e;
-    if (a.nseg > 1) {
-        if ((e = cudaFuncSetAttribute(k_mix_simt<T, RS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
+    if (nseg > 1) {
+        if ((e = cudaFuncSetAttribute(k_mix_simt<T, RS, true, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
             cudaSuccess)
             return e;
-        k_mix_simt<T, RS, true><<<dim3((unsigned)(lanes * (a.nseg - 1)), tiles), ST, smem, s>>>(a);
+        k_mix_simt<T, RS, true, NB><<<dim3((unsigned)(lanes * (nseg - 1)), tiles, n), ST, smem, s>>>(b);
         count_launch();
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if ((e = launch_mix_combine(a, s)) != cudaSuccess) return e;
+        if ((e = launch_mix_combine(m, n, s)) != cudaSuccess) return e;
     }
-    if ((e = cudaFuncSetAttribute(k_mix_simt<T, RS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
+    if ((e = cudaFuncSetAttribute(k_mix_simt<T, RS, false, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
         cudaSuccess)
         return e;
-    k_mix_simt<T, RS, false><<<dim3((unsigned)(lanes * a.nseg), tiles), ST, smem, s>>>(a);
+    k_mix_simt<T, RS, false, NB><<<dim3((unsigned)(lanes * nseg), tiles, n), ST, smem, s>>>(b);
     count_launch();
     return cudaGetLastError();
 }
 
+template <typename T, int NB>
+cudaError_t launch_mix_simt_d(const MixArgs *m, int n, cudaStream_t s) {
+    switch (m[0].wide) {
+        case 32: return launch_mix_simt_t<T, 4, NB>(m, n, s);
+        case 64: return launch_mix_simt_t<T, 8, NB>(m, n, s);
+        case 128: return launch_mix_simt_t<T, 16, NB>(m, n, s);
+        default: return launch_mix_simt_t<T, 32, NB>(m, n, s);
+    }
+}
 template <typename T>
-cudaError_t launch_mix_simt_d(const MixArgs &a, cudaStream_t s) {
-    if (a.da <= 32) return launch_mix_simt_t<T, 4>(a, s);
-    if (a.da <= 64) return launch_mix_simt_t<T, 8>(a, s);
-    if (a.da <= 128) return launch_mix_simt_t<T, 16>(a, s);
-    return launch_mix_simt_t<T, 32>(a, s);
+cudaError_t launch_mix_simt_n(const MixArgs *m, int n, cudaStream_t s) {
+    return n == 1 ? launch_mix_simt_d<T, 1>(m, n, s) : launch_mix_simt_d<T, 3>(m, n, s);
 }
 
 }  // namespace
@@ -446,19 +471,24 @@ cudaError_t launch_mix_simt_d(const MixArgs &a, cudaStream_t s) {
 // Measured against one piece of each lane: 3 x 333 tokens, 5 heads of 37 x 29:
 // 53 us, 24 in seven; 2 x 1000, 4 of 128 x 128: 252 us, 70 in nine (one wave), 95
 // in eleven (two); 8 x 2048, 16 of 128 x 64: 712 us, 850 in two.
-void mix_simt_plan(MixArgs &a) {
-    a.nseg = 1;
-    a.seg_len = a.T > 0 ? a.T : 1;
-    const int64_t lanes = a.Bt * a.H, ctas = lanes * ((a.dc + SP - 1) / SP), nb = (a.T + SC - 1) / SC;
-    if (lanes == 0 || ctas >= 296 || a.T < 96) return;
-    const int most_cta = a.da <= 32 ? 4 : a.da <= 64 ? 3 : a.da <= 128 ? 2 : 1;
-    auto cost = [&](int64_t n, double len) {
-        const int64_t wave = 148 * most_cta, rest = n % wave;
-        double c = (double)(n / wave) * (1 + 0.4 * (most_cta - 1));
-        if (rest > 0) c += 1 + 0.4 * (double)((rest + 147) / 148 - 1);
-        return c * (len + 2);
+static void plan_group(MixArgs *m, int n, int wide) {
+    int64_t ctas = 0;
+    const int64_t lanes = m[0].Bt * m[0].H, T = m[0].T, nb = (T + SC - 1) / SC;
+    for (int i = 0; i < n; i++)
+        if (m[i].wide == wide) {
+            m[i].nseg = 1;
+            m[i].seg_len = T > 0 ? T : 1;
+            ctas += lanes * ((m[i].dc + SP - 1) / SP);
+        }
+    if (ctas == 0 || ctas >= 296 || T < 96) return;
+    const int most_cta = wide <= 32 ? 4 : wide <= 64 ? 3 : wide <= 128 ? 2 : 1;
+    auto cost = [&](int64_t c, double len) {
+        const int64_t wave = 148 * most_cta, rest = c % wave;
+        double t = (double)(c / wave) * (1 + 0.4 * (most_cta - 1));
+        if (rest > 0) t += 1 + 0.4 * (double)((rest + 147) / 148 - 1);
+        return t * (len + 2);
     };
-    const int64_t most = ((int64_t)64 << 20) / (lanes * a.da * a.dc * 4) + 1;
+    const int64_t most = ((int64_t)64 << 20) / (lanes * m[0].da * m[0].dc * 4) + 1;
     double best = cost(ctas, (double)nb);
     for (int64_t ns = 2; ns <= 64 && ns <= most; ns++) {
         const int64_t len = (nb + ns - 1) / ns, k = (nb + len - 1) / len;
@@ -466,18 +496,53 @@ void mix_simt_plan(MixArgs &a) {
         const double c = cost(ctas * k, (double)len) + cost(ctas * (k - 1), 0.4 * (double)len) + 3;
         if (k > 1 && c < best) {
             best = c;
-            a.nseg = (int)k;
-            a.seg_len = len * SC;
+            for (int i = 0; i < n; i++)
+                if (m[i].wide == wide) {
+                    m[i].nseg = (int)k;
+                    m[i].seg_len = len * SC;
+                }
         }
     }
 }
 
-cudaError_t launch_mix_simt(const MixArgs &a, m3_dtype dt, cudaStream_t s) {
-    return dt == M3_BF16 ? launch_mix_simt_d<__nv_bfloat16>(a, s) : launch_mix_simt_d<float>(a, s);
+// Mixes of one width share their launches; all of a call do, at the widest
+// one's, where together they are fewer CTAs than SMs (the backward of 3 x 333
+// tokens, 5 heads of 37 x 29: 73 us one by one, 47 us together).
+void mix_simt_plan(MixArgs *m, int n) {
+    int widest = 32;
+    int64_t ctas = 0;
+    for (int i = 0; i < n; i++) {
+        m[i].wide = m[i].da <= 32 ? 32 : m[i].da <= 64 ? 64 : m[i].da <= 128 ? 128 : 256;
+        widest = std::max(widest, m[i].wide);
+        ctas += m[i].Bt * m[i].H * ((m[i].dc + SP - 1) / SP);
+    }
+    if (ctas <= 148)
+        for (int i = 0; i < n; i++) m[i].wide = widest;
+    for (int wide : {32, 64, 128, 256}) plan_group(m, n, wide);
 }
 
-cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s) {
-    k_mix_combine<<<dim3((unsigned)(a.Bt * a.H), (unsigned)((a.dar * a.dcr + 255) / 256)), 256, 0, s>>>(a);
+cudaError_t launch_mix_simt(const MixArgs *m, int n, m3_dtype dt, cudaStream_t s) {
+    for (int wide : {32, 64, 128, 256}) {
+        MixArgs g[3];
+        int k = 0;
+        for (int i = 0; i < n; i++)
+            if (m[i].wide == wide) g[k++] = m[i];
+        if (k == 0) continue;
+        const cudaError_t e = dt == M3_BF16 ? launch_mix_simt_n<__nv_bfloat16>(g, k, s) : launch_mix_simt_n<float>(g, k, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+
+cudaError_t launch_mix_combine(const MixArgs *m, int n, cudaStream_t s) {
+    MixBatch<3> b;
+    int k = 0;
+    for (int i = 0; i < n; i++)
+        if (m[i].nseg > 1) b.g[k++] = m[i];
+    if (k == 0) return cudaSuccess;
+    const MixArgs &a = b.g[0];                            // the others' states have as many elements
+    k_mix_combine<<<dim3((unsigned)(a.Bt * a.H), (unsigned)((a.dar * a.dcr + 255) / 256), k), 256, 0, s>>>(b);
     count_launch();
     return cudaGetLastError();
 }

@@ -941,8 +941,7 @@ cudaError_t launch_mix_tc(const MixArgs *g, int n, cudaStream_t s) {
         if (P.n == 0) continue;
         if (split) {
             if ((e = launch_pass<true>(P, kd, s)) != cudaSuccess) return e;
-            for (int i = 0; i < P.n; i++)
-                if (P.g[i].nseg > 1 && (e = launch_mix_combine(P.g[i], s)) != cudaSuccess) return e;
+            if ((e = launch_mix_combine(P.g, P.n, s)) != cudaSuccess) return e;
         }
         if ((e = launch_pass<false>(P, kd, s)) != cudaSuccess) return e;
     }

@@ -39,6 +39,7 @@ struct MixArgs {
     float scale_p, scale_i, scale_w;
     int nseg;                    // segments of the time axis, in walking order
     int64_t seg_len;             // tokens of a segment
+    int wide;                    // fp32 kernel: the variant, rows of a and b up to 32, 64, 128 or 256
     float *ws;                   // (nseg - 1) states of dar * dcr floats for each lane
 };
 
@@ -88,8 +89,8 @@ __device__ __forceinline__ void decay_pow_f32(float lg, int n, float &p, float &
 
 // segment plan (nseg, seg_len) and launch of the fp32 kernel: any sizes
 // within the limits
-void mix_simt_plan(MixArgs &a);
-cudaError_t launch_mix_simt(const MixArgs &a, m3_dtype dt, cudaStream_t s);
+void mix_simt_plan(MixArgs *m, int n);
+cudaError_t launch_mix_simt(const MixArgs *m, int n, m3_dtype dt, cudaStream_t s);
 // The tensor-core kernel: bf16, widths at most 128, widths and row strides
 // multiples of 8, 16-byte aligned bases.  Up to three problems of one batch share
 // their launches.
@@ -98,7 +99,7 @@ void mix_tc_plan(MixArgs *a, int n);
 cudaError_t launch_mix_tc(const MixArgs *a, int n, cudaStream_t s);
 int mix_tc_error_and_clear(cudaStream_t s);
 // chains the segments' states between the two passes
-cudaError_t launch_mix_combine(const MixArgs &a, cudaStream_t s);
+cudaError_t launch_mix_combine(const MixArgs *m, int n, cudaStream_t s);
 // Rows whose width or stride TMA cannot address, copied into rows padded with
 // zeros to a multiple of 8 columns: up to four tensors in one launch.
 struct PadArgs {

@@ -451,17 +451,17 @@ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 struct LinPlan {
     MixArgs m[3];
     int n;
-    bool tc;                   // all of them on the tensor cores, in shared launches; else one by one
+    bool tc;                   // all of them on the tensor cores (else none)
     size_t states[3], bytes;   // offsets of their segment states, and the end of these
 };
 void plan_mixes(LinPlan &p, m3_dtype dtype, bool aligned) {
     p.tc = aligned;
     for (int i = 0; i < p.n; i++) p.tc = p.tc && mix_tc_sizes(p.m[i], dtype);
     if (p.tc) mix_tc_plan(p.m, p.n);
+    else mix_simt_plan(p.m, p.n);
     p.bytes = 0;
     for (int i = 0; i < p.n; i++) {
         MixArgs &m = p.m[i];
-        if (!p.tc) mix_simt_plan(m);
         p.states[i] = p.bytes;
         p.bytes += align256((size_t)(m.Bt * m.H) * (size_t)(m.nseg - 1) * m.dar * m.dcr * sizeof(float));
     }
@@ -470,11 +470,7 @@ cudaError_t launch_mixes(LinPlan &p, m3_dtype dtype, void *workspace, cudaStream
     for (int i = 0; i < p.n; i++)
         p.m[i].ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.states[i]);
     if (p.tc) return launch_mix_tc(p.m, p.n, s);
-    for (int i = 0; i < p.n; i++) {
-        const cudaError_t e = launch_mix_simt(p.m[i], dtype, s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    return launch_mix_simt(p.m, p.n, dtype, s);
 }
 
 // bf16 rows that TMA cannot address, for their width or their stride, are
