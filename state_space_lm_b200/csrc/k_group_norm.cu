@@ -523,6 +523,13 @@ __device__ __forceinline__ SeqGeo seq_geo(const GnArgs &a, int vec, int rows, in
     return s;
 }
 
+// A sum of squares that rounding took below zero; a NaN stays one (fmaxf would
+// turn it into 0, and the variance of a group with an infinity into eps).
+__device__ __forceinline__ float not_below_0(float v) { return v < 0.f ? 0.f : v; }
+// What differences are taken from: with an infinity there, the mean would be
+// inf - inf and not the infinity that it is.
+__device__ __forceinline__ float origin(float v) { return isfinite(v) ? v : 0.f; }
+
 // Per (sequence, chunk, group): the count is known, (mean, M2) are written.  A
 // thread sums a vector of channels over its tokens as differences from its
 // first value (so a large mean cancels nothing); the threads' (n, mean, M2)
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_stats(GnArgs a, int rows, int
             const T *p = x + (int64_t)(s.t0 + s.ph) * a.C + v * VEC;
             const int64_t step = s.np * a.C;
             float sum[VEC], q[VEC];
-            K = ldf(p, 0);
+            K = origin(ldf(p, 0));
 #pragma unroll
             for (int e = 0; e < VEC; e++) sum[e] = q[e] = 0.f;
 #pragma unroll 8
@@ -561,7 +568,7 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_stats(GnArgs a, int rows, int
             }
             const float m = S / (float)(n * VEC);
             K += m;
-            Q = fmaxf(Q - S * m, 0.f);
+            Q = not_below_0(Q - S * m);
         }
         vstat[s.ph * s.nvec + v] = make_float2(K, Q);
     }
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_apply(GnArgs a, int rows, int
             const float2 *p = reinterpret_cast<const float2 *>(a.ws) + (int64_t)s.bi * nch * a.G + g;
             float K = 0.f, s1 = 0.f, s2 = 0.f;
             if (g < a.G) {
-                K = p[0].x;
+                K = origin(p[0].x);
 #pragma unroll 8
                 for (int c = w; c < nch; c += 8) {
                     const float2 q = p[c * (int)a.G];
@@ -665,7 +672,7 @@ __global__ void __launch_bounds__(SQT, 2) k_gn_seq_apply(GnArgs a, int rows, int
                     s1 += sh[i][l].x;
                     s2 += sh[i][l].y;
                 }
-                const float dm = s1 / n, m = K + dm, rstd = rsqrtf(fmaxf(s2 - s1 * dm, 0.f) / n + a.eps);
+                const float dm = s1 / n, m = K + dm, rstd = rsqrtf(not_below_0(s2 - s1 * dm) / n + a.eps);
                 gstat[g] = make_float2(m, rstd);
                 if (s.ch == 0 && a.mean) a.mean[(int64_t)s.bi * a.G + g] = m;
                 if (s.ch == 0 && a.rstd) a.rstd[(int64_t)s.bi * a.G + g] = rstd;
