@@ -14,7 +14,7 @@ namespace {
 // the tokens in blocks of 16.  With M the state entering a block, j the place
 // in it and L its tokens:
 //   y_j = scale_i g^(j+1) M^T a_j + sum_{i <= j} P_ji c_i,  P_ji = scale_p g^(j-i) (a_j . b_i)
-//   M  <- M + M (g^L - 1) + sum_i b_i (scale_w g^(L-1-i) c_i)^T
+//   M  <- M g^L + sum_i b_i (scale_w g^(L-1-i) c_i)^T     (M g^L as in decay_of)
 // (walking backwards g^j and g^(L-i)).  A thread holds one column and RS rows
 // of M in registers (warp = row slice, lane = column), so a and b rows are
 // read from shared memory as broadcasts and the block's own part of M is
@@ -166,9 +166,9 @@ __global__ void __launch_bounds__(ST, RS <= 4 ? 4 : RS <= 8 ? 3 : RS <= 16 ? 2 :
                     own[i + 3] = fmaf(x.w, cw, own[i + 3]);
                 }
             }
-            const float dm1 = sm.pm1[L];
+            const Decay d = decay_of(sm.pw[L], sm.pm1[L]);
 #pragma unroll
-            for (int i = 0; i < RS; i++) M[i] = fmaf(M[i], dm1, M[i]) + own[i];
+            for (int i = 0; i < RS; i++) M[i] = fmaf(M[i], d.keep, fmaf(M[i], d.f, own[i]));
         }
         if (!SO) {
             __syncthreads();
@@ -234,13 +234,13 @@ __global__ void __launch_bounds__(ST, RS <= 4 ? 4 : RS <= 8 ? 3 : RS <= 16 ? 2 :
 // One thread per state element; bound by the slots' bytes, read and written
 // once each.
 __global__ void __launch_bounds__(256) k_mix_combine(const __grid_constant__ MixBatch<3> P) {
-    __shared__ float dm1[256];
+    __shared__ Decay dec[256];
     const MixArgs &g = P.g[blockIdx.z];
     const int64_t lane = blockIdx.x, bi = lane / g.H, h = lane % g.H;
     const int64_t len = lane_length(g.lengths, bi, g.T);
     const double lg = (double)g.log_decay[h];
     for (int j = threadIdx.x; j < g.nseg - 1; j += 256)
-        dm1[j] = decay_pow_m1(lg, seg_tokens(j, g.nseg, g.seg_len, g.reverse, len));
+        dec[j] = decay_pow_f64(lg, seg_tokens(j, g.nseg, g.seg_len, g.reverse, len));
     __syncthreads();
     const size_t elems = (size_t)g.dar * g.dcr, i = (size_t)blockIdx.y * 256 + threadIdx.x;
     if (i >= elems) return;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(256) k_mix_combine(const __grid_constant__ Mix
     }
     float *sl = g.ws + (size_t)lane * (g.nseg - 1) * elems + i;
     for (int j = 0; j < g.nseg - 1; j++) {
-        M = fmaf(M, dm1[j], M) + sl[j * elems];
+        M = fmaf(M, dec[j].keep, fmaf(M, dec[j].f, sl[j * elems]));
         sl[j * elems] = M;
     }
 }

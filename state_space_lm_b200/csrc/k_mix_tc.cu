@@ -10,7 +10,7 @@
 //   D3 = A M                the past's answer          M=64  N=64 K=da
 //   D4 = B^T Cw             own chunk's state          M=128 N=3x64 K=64
 //   y_j = D2_j + scale_i g^(j+1) D3_j                  (backwards g^(L-1-j))
-//   M  <- M + M (g^L - 1) + D4,  Cw_i = scale_w g^(L-1-i) c_i   (backwards g^(i+1))
+//   M  <- M g^L + D4 (as in decay_of),  Cw_i = scale_w g^(L-1-i) c_i   (backwards g^(i+1))
 // The decay is a constant of the lane, so every weight is a table of the 65
 // powers g^0 .. g^64: the 64 x 64 mask lives in the score warps' registers.
 //
@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         if (!SO && nch > 0) publish(0);
         for (int c = 0; c < nch; c++) {
             const int pb = c & 1;
-            const float d1 = pm1[chunk_n(c)];
-            const f32x2 dm1 = pair(d1, d1);
+            const Decay d = decay_of(pw[chunk_n(c)], pm1[chunk_n(c)]);
+            const f32x2 keep = pair(d.keep, d.keep), df = pair(d.f, d.f);
             if (!wait(B_DFULL, c, 114)) break;
             tc_fence_after();
             float hi[16], mid[16], lo[16];
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
             for (int e = 0; e < 8; e++) {
                 const f32x2 s = add2(add2(pair(lo[2 * e], lo[2 * e + 1]), pair(mid[2 * e], mid[2 * e + 1])),
                                      pair(hi[2 * e], hi[2 * e + 1]));
-                M[e] = add2(fma2(M[e], dm1, M[e]), s);
+                M[e] = fma2(M[e], keep, fma2(M[e], df, s));
             }
             tc_fence_before();
             arrive(B_DEMPTY);
@@ -596,8 +596,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
         if (!SO && nch > 0) publish(0);
         for (int c = 0; c < nch; c++) {
             const int pb = c & 1;
-            const float d1 = pm1[chunk_n(c)];
-            const f32x2 dm1 = pair(d1, d1);
+            const Decay d = decay_of(pw[chunk_n(c)], pm1[chunk_n(c)]);
+            const f32x2 keep = pair(d.keep, d.keep), df = pair(d.f, d.f);
             if (!wait(B_DFULL, c, 114)) break;
             tc_fence_after();
 #pragma unroll
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 for (int u = 0; u < 4; u++) {
                     const f32x2 s = add2(add2(pair(lo[2 * u], lo[2 * u + 1]), pair(mid[2 * u], mid[2 * u + 1])),
                                          pair(hi[2 * u], hi[2 * u + 1]));
-                    M[4 * k + u] = add2(fma2(M[4 * k + u], dm1, M[4 * k + u]), s);
+                    M[4 * k + u] = fma2(M[4 * k + u], keep, fma2(M[4 * k + u], df, s));
                 }
             }
             tc_fence_before();

@@ -69,11 +69,20 @@ __device__ __forceinline__ int64_t lane_length(const int32_t *lengths, int64_t b
     const int64_t n = lengths[b];
     return n < 0 ? 0 : (n > T ? T : n);
 }
-// g^n - 1 for whole n >= 0, from 64 bits.  A state multiplied by g^n must not
-// inherit the rounding of a g^n near 1: it is updated as M + M (g^n - 1).  g^0
-// is 1 for a decay of zero too (log_decay = -inf).
-__device__ __forceinline__ float decay_pow_m1(double lg, int64_t n) {
-    return n == 0 ? 0.f : (float)expm1(lg * (double)n);
+// How a state M is multiplied by p = g^n: as keep M + M f.  For p >= 1/2, M + M
+// (p - 1), so that it does not inherit the rounding of a p near 1 from chunk to
+// chunk.  Below, M p: p - 1 rounds at 2^-25 whatever p is, which is all there is
+// of a small p.  g^0 is 1 for a decay of zero too (log_decay = -inf).
+struct Decay {
+    float keep, f;
+};
+__device__ __forceinline__ Decay decay_of(float p, float pm1) {
+    return p < 0.5f ? Decay{0.f, p} : Decay{1.f, pm1};
+}
+// from 64 bits, for any whole n >= 0
+__device__ __forceinline__ Decay decay_pow_f64(double lg, int64_t n) {
+    const double x = lg * (double)n, m = n == 0 ? 0. : expm1(x);
+    return m < -0.5 ? Decay{0.f, (float)exp(x)} : Decay{1.f, (float)m};
 }
 
 // g^n and g^n - 1 from fp32 arithmetic for n <= 64, within a few roundings: the

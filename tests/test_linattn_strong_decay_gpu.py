@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from lin_reference import U, forward64, within
+from lin_reference import U, backward64, forward64, mix_bound, within
 from state_space_lm_b200 import m3
 
 pytestmark = pytest.mark.gpu
@@ -56,3 +56,59 @@ def test_no_memory_is_none():
     S = s0.clone()
     m3.linattn_step_decode(q[:, 0], k[:, 0], v[:, 0], ld, S)
     assert torch.equal(S, k[:, 0, :, :, None] * v[:, 0, :, None, :])
+
+
+# What 32 bits hold of a vanishing state: below this nothing is asked (the
+# smallest normal number, times 2^16 for the bf16 pieces of weighted rows)
+FLOOR = 2.0 ** -110
+
+
+def on_tensor_cores(q, v):
+    return q.dtype == torch.bfloat16 and q.shape[-1] <= 128 and v.shape[-1] <= 128
+
+
+def chain_bound(ref, mass, T):
+    """A state in fp32: a chunk's own sum (3 x 64, as in state_bound), and for
+    each chunk of 16 tokens at least: its power (expf to 2 units in the last
+    place, two more roundings; or expm1f and one), the product and the sum."""
+    return (3 * 64 + 16 + 8 * (T / 16 + 1)) * F32 * mass + F32 * ref.abs() + FLOOR
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [16, 64, 65, 200, 1100])
+@pytest.mark.parametrize("dk,dv", [(128, 64), (64, 96), (37, 29)])
+@pytest.mark.parametrize("first", [0, 10])
+def test_a_state_decays_through_tokens_that_add_nothing(first, dk, dv, T, dtype):
+    """Keys and queries (the adjoint's keys) are zero behind the first 10 tokens
+    or from the start: s_final = g^T s0 + ..., ds0 = g^T ds + ... to their own
+    digits, and so are the answers and gradients that read them."""
+    q, k, v, _, s0 = inputs(2, T, 7, dk, dv, dtype, 1.0)
+    ld = torch.tensor([-math.inf, -5.0, -0.3, -0.25, -0.05, -1e-3, 0.0], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dy = torch.randn(v.shape, generator=g, device="cuda").to(v.dtype)
+    ds = torch.randn(s0.shape, generator=g, device="cuda")
+    k[:, first:] = 0
+    sc, tc = dk ** -0.5, on_tensor_cores(q, v)
+    y, sf = m3.linattn_chunked_fwd(q, k, v, ld, s0=s0)
+    ry, rs = forward64(q, k, v, ld, sc, s0)
+    ay, as_ = forward64(q, k, v, ld, sc, s0, absolute=True)
+    within(sf, rs, chain_bound(rs, as_, T), "s_final")
+    within(y, ry, mix_bound(ry, ay, v.dtype, 4 * T, dk, tc) + FLOOR, "y")
+    q2 = q.clone()
+    q2[:, :T - first] = 0
+    got = m3.linattn_chunked_bwd(q2, k, v, ld, dy, s0=s0, ds_final=ds)
+    ref = backward64(q2, k, v, ld, sc, dy, s0, ds)
+    mass = backward64(q2, k, v, ld, sc, dy, s0, ds, absolute=True)
+    within(got["ds0"], ref[3], chain_bound(ref[3], mass[3], T), "ds0")
+    for name, r, a, da in zip(("dq", "dk", "dv"), ref, mass, (dv, dv, dk)):
+        within(got[name], r, mix_bound(r, a, v.dtype, 4 * T, da, tc) + FLOOR, name)
+    assert m3.device_error() == m3.M3_OK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_large_old_state_behind_a_strong_decay(dtype):
+    """The new tokens keep their digits beside what 100 tokens leave of 1e8."""
+    q, k, v, ld, s0 = inputs(2, 100, len(DECAYS), 64, 64, dtype, 1e8)
+    _, sf = m3.linattn_chunked_fwd(q, k, v, ld, s0=s0)
+    rs = forward64(q, k, v, ld, 0.125, s0)[1]
+    within(sf, rs, chain_bound(rs, forward64(q, k, v, ld, 0.125, s0, absolute=True)[1], 100), "s_final")
