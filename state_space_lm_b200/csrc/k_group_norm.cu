@@ -1017,22 +1017,29 @@ int seq_phases(int64_t C, int vec) {
     return nvec < SQT ? (int)(SQT / nvec) : 1;
 }
 
+// Dynamic shared memory of the forward over sequences: 8 bytes a vector of
+// channels, or a group (16384 of them at most).  A launch gets 48 KB, its static
+// part included, without asking; above 40 KB the kernel is allowed the most that
+// any call needs, always the same, so that no call takes away from another.
+constexpr int SEQ_SMEM = 16384 * (int)sizeof(float2);
+template <typename... P>
+cudaError_t allow_smem(void (*kernel)(P...), int bytes) {
+    return bytes <= 40 * 1024 ? cudaSuccess
+                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SEQ_SMEM);
+}
+
 template <typename T, int VEC>
 cudaError_t seq_fwd(const GnArgs &a, const Plan &p, cudaStream_t s) {
     const unsigned blocks = (unsigned)(a.Bt * p.nch);
     const int smem = (int)(seq_phases(a.C, VEC) * (a.C / VEC) * sizeof(float2));
     cudaError_t e;
-    if (smem > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(k_gn_seq_stats<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-        return e;
+    if ((e = allow_smem(k_gn_seq_stats<T, VEC>, smem)) != cudaSuccess) return e;
     k_gn_seq_stats<T, VEC><<<blocks, SQT, smem, s>>>(a, (int)p.rows, (int)p.nch);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int gsm = (int)(a.G * sizeof(float2));          // above 48 KB only without vectors (G > 6144)
-#define GN_CALL(K)                                                                                               \
-    if (gsm > 48 * 1024 &&                                                                                       \
-        (e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, gsm)) != cudaSuccess)          \
-        return e;                                                                                                \
+    const int gsm = (int)(a.G * sizeof(float2));
+#define GN_CALL(K)                                              \
+    if ((e = allow_smem(K, gsm)) != cudaSuccess) return e;      \
     e = launch_after(K, dim3(blocks), SQT, gsm, s, a, (int)p.rows, (int)p.nch)
     GN_ACTS(GN_CALL, k_gn_seq_apply, T, VEC, )
 #undef GN_CALL
