@@ -378,3 +378,15 @@ def test_long_sequences_over_few_lanes(dtype):
     d["lengths"] = torch.tensor([T, 3333], dtype=torch.int32, device="cuda")
     check_forward(d)
     check_backward(d)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_step_of_the_most_heads(dtype):
+    d = inputs(2, 1, 4096, 64, 8, 8, dtype)
+    S = d["s0"].clone()
+    y = m3.linattn_step_decode(d["q"][:, 0], d["k"][:, 0], d["v"][:, 0], d["ld"], S)
+    ry, rs = forward64(d["q"], d["k"], d["v"], d["ld"], 8 ** -0.5, d["s0"])
+    ay, as_ = forward64(d["q"], d["k"], d["v"], d["ld"], 8 ** -0.5, d["s0"], absolute=True)
+    # g or g - 1 (4 half steps), a product and two sums; y: those, and a sum over 8 rows
+    within(S, rs, 8 * U[torch.float32] * as_, "s")
+    within(y[:, None], ry, (8 + 12) * U[torch.float32] * ay + 1.01 * U[y.dtype] * ry.abs(), "y_t")
