@@ -77,6 +77,12 @@ def _grad(t, dtype):
     return t.clone() if t.data_ptr() % 16 else t
 
 
+def _shaped(g, t):
+    """A gradient (or None) in its input's own shape: the library asks for
+    element counts, so a gate may be (B, T, C) beside rows (B T, C)."""
+    return None if g is None else g.view(t.shape)
+
+
 class LinearAttention(torch.autograd.Function):
     """Returns (y, s_final); gradients of q, k, v and s0."""
 
@@ -100,7 +106,7 @@ class LinearAttention(torch.autograd.Function):
         dy = torch.zeros_like(v, memory_format=torch.contiguous_format) if dy is None else _grad(dy, v.dtype)
         g = m3.linattn_chunked_bwd(q, k, v, log_decay, dy, scale=ctx.scale, s0=s0,
                                    ds_final=None if ds is None else _grad(ds, torch.float32), lengths=lengths, want=want)
-        return g.get("dq"), g.get("dk"), g.get("dv"), None, None, g.get("ds0"), None
+        return g.get("dq"), g.get("dk"), g.get("dv"), None, None, _shaped(g.get("ds0"), s0), None
 
 
 def linear_attention(q, k, v, log_decay, scale=None, s0=None, lengths=None):
@@ -127,7 +133,8 @@ class GroupNorm(torch.autograd.Function):
         want = tuple(k for k, on in (("dx", n[0]), ("dweight", n[2]), ("dbias", n[3]), ("dgate", n[4])) if on)
         g = m3.group_norm_bwd(x, _grad(dy, x.dtype), mean, rstd, ctx.groups, weight, bias, gate=gate, act=ctx.act,
                               want=want)
-        return g.get("dx"), None, g.get("dweight"), g.get("dbias"), g.get("dgate"), None, None
+        return (g.get("dx"), None, _shaped(g.get("dweight"), weight), _shaped(g.get("dbias"), bias),
+                _shaped(g.get("dgate"), gate), None, None)
 
 
 def group_norm(x, groups, weight=None, bias=None, gate=None, act="none", eps=1e-5):
