@@ -771,8 +771,8 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps
     x and gate (Bt,...,C) bf16 or fp32, contiguous; weight, bias (C) fp32 or
     None; act "none", "silu", "gelu" (erf) or "relu".  For the norm of each
     head of each token pass (tokens, C) and groups = heads.  Returns y, mean
-    and rstd (Bt, groups) fp32; ``out`` may hold the three (mean, rstd None
-    when not wanted)."""
+    and rstd (Bt, groups) fp32, NaN where a sequence has no positions; ``out``
+    may hold the three (mean, rstd None when not wanted)."""
     if stream is not None:
         return _on(stream, x, group_norm_fwd, x, groups, weight, bias, gate, act, eps, workspace, out)
     w, f = "m3_group_norm_fwd", torch.float32
@@ -789,6 +789,10 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, act="none", eps
     args = (_ptr(x), dt, _ptr(weight), _ptr(bias), _ptr(gate), ACTIVATIONS[act], float(eps), d, _ptr(y), _ptr(mean),
             _ptr(rstd), _ptr(ws), nbytes)
     _run(lib().m3_group_norm_fwd, w, args, dev)
+    if d.seqlen == 0:                                     # the library writes nothing then
+        for t in (mean, rstd):
+            if t is not None:
+                t.fill_(float("nan"))
     return y, mean, rstd
 
 

@@ -74,3 +74,15 @@ def test_what_an_infinity_or_a_nan_reaches(shape, groups, bad, dtype):
             assert torch.equal(g["dbias"][~cols], g0["dbias"][~cols])
             if z is not None:
                 assert torch.equal(g["dgate"].isnan(), hit) and torch.equal(g["dgate"][~hit], g0["dgate"][~hit])
+
+
+def test_statistics_of_no_positions():
+    """The mean of nothing is NaN, not what the memory held."""
+    held = torch.ones(2, 2, 4, device="cuda")
+    del held
+    x = torch.empty(2, 0, 64, device="cuda")
+    y, mean, rstd = m3.group_norm_fwd(x, 4)
+    assert y.shape == x.shape and bool(mean.isnan().all()) and bool(rstd.isnan().all())
+    out = [torch.empty_like(x), torch.ones(2, 4, device="cuda"), None]
+    m3.group_norm_fwd(x, 4, out=out)
+    assert bool(out[1].isnan().all())
