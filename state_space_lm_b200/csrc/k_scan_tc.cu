@@ -53,10 +53,11 @@
 // returns.
 #include <cuda.h>
 
-#include "m3_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace m3 {
 namespace tc {
+using namespace ptx;
 
 template <bool V> struct BoolC { static constexpr bool value = V; };
 
@@ -160,101 +161,26 @@ struct TcArgs {
 constexpr int SLOT_G = 0, SLOT_PHIL = N * P, SLOT_PHIN = N * P + NP2, SLOT_E = N * P + N;
 constexpr int SLOT_FLOATS = N * P + N + 4;
 
-// ---- PTX wrappers ---------------------------------------------------------
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(bar),
-                 "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+// ---- PTX wrappers beside those of tc_ptx.cuh ------------------------------
+// One probe that may suspend the thread for up to 10 ms (the drains at the end;
+// every other wait polls without the hint: measured on the default, MIMO and
+// long workloads, the hinted form woke waiting warps later, 2-5 % slower calls).
+__device__ __forceinline__ bool mbar_try_hint(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(10000000u)   // suspend up to 10 ms instead of spinning
+        : "r"(bar), "r"(parity), "r"(10000000u)
         : "memory");
     return ok != 0;
 }
-
-__device__ __forceinline__ bool mbar_try_spin(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-constexpr long long WAIT_LIMIT_CYCLES = 2000000000LL;  // ~1 s at 1.9 GHz
-
-// Bounded wait without the suspend hint (for the single MMA-issuing thread).
-// The first probe is inline; the polling loop is one out-of-line copy shared
-// by every call site, which keeps the hot loops of the kernel small.
-__device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
-                                           int site, bool spin) {
-    const long long t0 = clock64();
-    while (true) {
-        if (spin ? mbar_try_spin(bar, parity) : mbar_try(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (clock64() - t0 > WAIT_LIMIT_CYCLES) {
-            *abort_flag = 1;
-            atomicCAS(err, 0, site);
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool wait_bar_spin(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
-                                              int site) {
-    return mbar_try_spin(bar, parity) || wait_bar_slow(bar, parity, abort_flag, err, site, true);
-}
-// Bounded waits taken by every lane of a converged warp, with one warp-wide
-// outcome.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
-                                          int site);
-__device__ __forceinline__ bool warp_wait_spin(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
-                                               int site) {
-    const bool ok = wait_bar_spin(bar, parity, abort_flag, err, site);
-    return __all_sync(0xffffffffu, ok);
-}
-
-// Bounded wait on an mbarrier phase.  Returns false when the kernel is
-// aborting (this wait timed out, or another thread's did).  Every role polls
-// without the suspend-time hint: measured on the default, MIMO and long
-// workloads, the hinted form woke waiting warps later (2-5 % slower calls).
+// Bounded wait of one thread on an mbarrier phase.  Returns false when the kernel
+// is aborting (this wait timed out, or another thread's did).
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
                                          int site) {
-    return mbar_try_spin(bar, parity) || wait_bar_slow(bar, parity, abort_flag, err, site, true);
-}
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
-                                          int site) {
-    const bool ok = wait_bar(bar, parity, abort_flag, err, site);
-    return __all_sync(0xffffffffu, ok);
+    return mbar_try(bar, parity) || wait_slow(bar, parity, abort_flag, err, site);
 }
 
-// One lane of a converged warp (elect.sync): the lane that issues a UMMA, a
-// commit or a TMA copy, while the whole warp computes the (warp-uniform)
-// operands.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t pred;
-    asm volatile(
-        "{\n .reg .b32 rx;\n .reg .pred px;\n elect.sync rx|px, 0xffffffff;\n selp.b32 %0, 1, 0, px;\n}"
-        : "=r"(pred));
-    return pred != 0;
-}
-
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void named_bar(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 // Named barrier that also ORs a predicate over the participating threads, so
 // that every thread of a group takes the same decision.
@@ -268,20 +194,6 @@ __device__ __forceinline__ bool named_bar_or(int id, int n, bool pred) {
     return r != 0;
 }
 
-__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                          uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_store4(const CUtensorMap *map, int c0, int c1, int c2, int c3, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
 __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
                                           uint32_t bar) {
     asm volatile(
@@ -295,40 +207,6 @@ __device__ __forceinline__ void tma_prefetch5(const CUtensorMap *map, int c0, in
                  "r"(c1), "r"(c2), "r"(c3), "r"(c4)
                  : "memory");
 }
-// Pull a box of the tensor into L2 ahead of its load (no shared memory, no barrier).
-__device__ __forceinline__ void tma_prefetch4(const CUtensorMap *map, int c0, int c1, int c2, int c3) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(c0), "r"(c1),
-                 "r"(c2), "r"(c3)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// UMMA shared-memory descriptor, 128B swizzle, sm_100 version bits.
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-// Instruction descriptor: kind::f16, bf16 x bf16 -> fp32, dense.
-__host__ __device__ constexpr uint32_t idesc(int M, int Nn, int a_mn, int b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(Nn >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ void umma(uint32_t dtmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(
-            dtmem),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
 // 16 consecutive fp32 columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
     uint32_t r[16];
@@ -341,22 +219,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
 #pragma unroll
     for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
-// 32 fp32 columns of 16 TMEM lanes (the rows of an M=64 accumulator in this
-// warp's lane quarter), spread over the 32 threads: thread t gets, for each
-// group i of 8 columns, v[4i], v[4i+1] = (lane t/4, columns 8i + 2(t%4) + 0, 1)
-// and v[4i+2], v[4i+3] = (lane t/4 + 8, the same columns).
-__device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr, float *v) {
-    uint32_t r[16];
-    __syncwarp();
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
-}
-// The same for 16 columns (two groups of 8).
+// tmem_ld16x256b_x4 for 16 columns (two groups of 8).
 __device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t taddr, float *v) {
     uint32_t r[8];
     __syncwarp();
@@ -365,15 +228,6 @@ __device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t taddr, float *v) {
                  : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-    __syncwarp();
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&v);
 }
 __device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
     __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162 *>(&u);
@@ -544,12 +398,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             // never leave loads in flight into shared memory at exit
             for (int c = (issued > L::NXR ? issued - L::NXR : 0); c < issued; c++) {
                 const long long t0 = clock64();
-                while (!mbar_try(bar(B_XFULL + c % L::NXR), (c / L::NXR) & 1) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+                while (!mbar_try_hint(bar(B_XFULL + c % L::NXR), (c / L::NXR) & 1) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
                 }
             }
             for (int c = (issued > NB ? issued - NB : 0); c < issued; c++) {
                 const long long t0 = clock64();
-                while (!mbar_try(bar(B_BFULL + c % NB), (c / NB) & 1) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+                while (!mbar_try_hint(bar(B_BFULL + c % NB), (c / NB) & 1) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
                 }
             }
         }
@@ -968,10 +822,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint64_t d_bb_mn = d_bb_mn0 + ob * STEP_BC, d_xw = d_xw0 + ob * STEP_XP;
                 const uint64_t dx = (R == 1) ? d_x0 + (uint64_t)sx * STEP_X : d_xr0 + ob * STEP_XP;
                 const uint64_t dg = d_gb0 + ((c + 1) & 1) * STEP_GB;   // state after chunk c-1
-                if (!warp_wait_spin(bar(B_OPSREADY + ob), (c >> 1) & 1, abort_flag, a.err, 10)) break;
+                if (!warp_wait(bar(B_OPSREADY + ob), (c >> 1) & 1, abort_flag, a.err, 10)) break;
                 if (SO) {
                     // state-only pass: the chunk-state UMMA alone
-                    if (!warp_wait_spin(bar(B_STTAKEN), c & 1, abort_flag, a.err, 12)) break;
+                    if (!warp_wait(bar(B_STTAKEN), c & 1, abort_flag, a.err, 12)) break;
                     tc_fence_after();
                     if (elect_one()) {
                         for (int kk = 0; kk < Q / 16; kk++)
@@ -982,7 +836,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     continue;
                 }
-                if (c > 0 && !warp_wait_spin(bar(B_STAKEN), (c - 1) & 1, abort_flag, a.err, 11)) break;
+                if (c > 0 && !warp_wait(bar(B_STAKEN), (c - 1) & 1, abort_flag, a.err, 11)) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll 1
@@ -991,7 +845,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     umma_commit(bar(B_SFULL));
                 }
                 __syncwarp();
-                if (!warp_wait_spin(bar(B_STTAKEN), c & 1, abort_flag, a.err, 12)) break;
+                if (!warp_wait(bar(B_STTAKEN), c & 1, abort_flag, a.err, 12)) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll 1
@@ -1001,7 +855,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
                 // D3 buffer c & 1 was last read by the outputs of chunk c - 2
-                if (c > 1 && !warp_wait_spin(bar(B_YTAKEN + (c & 1)), ((c >> 1) - 1) & 1, abort_flag, a.err, 13))
+                if (c > 1 && !warp_wait(bar(B_YTAKEN + (c & 1)), ((c >> 1) - 1) & 1, abort_flag, a.err, 13))
                     break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -1014,7 +868,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (R == 1) umma_commit(bar(B_OPSFREE + ob));
                 }
                 __syncwarp();
-                if (!warp_wait_spin(bar(B_SPFULL), c & 1, abort_flag, a.err, 14)) break;
+                if (!warp_wait(bar(B_SPFULL), c & 1, abort_flag, a.err, 14)) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll 1
@@ -1030,7 +884,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (elect_one()) umma_commit(bar(B_DRAIN));
             __syncwarp();
             const long long t0 = clock64();
-            while (!mbar_try(bar(B_DRAIN), 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+            while (!mbar_try_hint(bar(B_DRAIN), 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
             }
             __syncwarp();
         }

@@ -1,5 +1,5 @@
 // tc_ptx.cuh -- PTX wrappers of the tensor-core kernels: mbarriers and their
-// bounded waits, TMA, tcgen05.  (k_scan_tc.cu has its own.)
+// bounded waits, TMA, tcgen05.
 #pragma once
 #include <cuda.h>
 
@@ -35,7 +35,7 @@ constexpr long long WAIT_LIMIT_CYCLES = 2000000000LL;   // ~1 s at 1.9 GHz
 // Bounded wait on an mbarrier phase: false when the kernel is giving up (this
 // wait ran out, or another one did).  The first probe is inline; the polling
 // loop is one out-of-line copy.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err, int site) {
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err, int site) {
     const long long t0 = clock64();
     while (true) {
         if (mbar_try(bar, parity)) return true;
