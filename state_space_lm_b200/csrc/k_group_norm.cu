@@ -11,6 +11,7 @@
 // them; the second read of x comes from L2 while the tensors fit there.
 #include "group_norm.cuh"
 #include "launch.cuh"
+#include "tc_ptx.cuh"
 
 namespace m3 {
 namespace {
@@ -59,10 +60,7 @@ __device__ __forceinline__ float act_only(float u, int act) {
 
 // fma of two values in one instruction (register pairs)
 __device__ __forceinline__ void fma_pair(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
-    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
-        : "=f"(d0), "=f"(d1)
-        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+    ptx::unpair(ptx::fma2(ptx::pair(a0, a1), ptx::pair(b0, b1), ptx::pair(c0, c1)), d0, d1);
 }
 // o = a * b + c over VEC values; b and c may be one value each
 template <int VEC>
