@@ -385,13 +385,13 @@ __global__ void __launch_bounds__(256) k_lin_step(LinStepArgs a) {
         ks[tid] = ldf(k, tid);
     }
     if (tid < dv) vs[tid] = ldf(v, tid);
-    // S + (S (g - 1) + k v) for g >= 1/2, S g + k v below: the first does not
-    // inherit the rounding of a g near 1, token after token; but it rounds at the
-    // size of the old S, which is too much for the small state that a strong
-    // decay leaves (none of the old one at log_decay = -inf)
-    const float lg = a.log_decay[h], g = expf(lg);
-    const bool strong = g < 0.5f;
-    const float f = strong ? g : expm1f(lg);
+    // S keep + (S f + k v): S + (S (g - 1) + k v) for g >= 1/2, S g + k v below.  The
+    // first does not inherit the rounding of a g near 1, token after token; but it
+    // rounds at the size of the old S, which is too much for the small state that
+    // a strong decay leaves (none of the old one at log_decay = -inf)
+    const float lg = a.log_decay[h];
+    const bool strong = lg < -0.69314718f;
+    const float keep = strong ? 0.f : 1.f, f = strong ? expf(lg) : expm1f(lg);
 #pragma unroll
     for (int e = 0; e < VEC; e++) acc[e] = 0.f;
     __syncthreads();
@@ -405,8 +405,7 @@ __global__ void __launch_bounds__(256) k_lin_step(LinStepArgs a) {
                     const float kr = ks[r], qr = qs[r];
 #pragma unroll
                     for (int e = 0; e < VEC; e++) {
-                        const float n = fmaf(x[u][e], f, kr * vs[VEC * c + e]);
-                        x[u][e] = strong ? n : x[u][e] + n;
+                        x[u][e] = fmaf(x[u][e], keep, fmaf(x[u][e], f, kr * vs[VEC * c + e]));
                         acc[e] = fmaf(qr, x[u][e], acc[e]);
                     }
                     if (VEC == 4) *reinterpret_cast<float4 *>(S + r * dv) = *reinterpret_cast<float4 *>(x[u]);
