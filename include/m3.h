@@ -325,8 +325,18 @@ size_t m3_workspace_bytes(int which, m3_dims d, m3_dtype dtype);
  * bf16 inputs with dstate and headdim <= 128 run on the tensor cores (widths or
  * row strides that are no multiples of 8 by way of padded copies in the
  * workspace; other bases than 16-byte aligned ones do not, nor do few sequences
- * of up to 16 tokens); everything else runs in fp32 arithmetic.  A
- * non-finite q, k or v reaches the rows that depend on it, and may reach
+ * of up to 16 tokens); everything else, and the step, runs in fp32 arithmetic.
+ *
+ * Roundings.  In fp32 arithmetic an answer or gradient is an fp32 sum, rounded
+ * once to its type.  On the tensor cores every term of y, dq, dk and dv meets one
+ * rounding to bf16 more (2^-8 of the term) before its fp32 sum: that of the
+ * decayed score (scale g^(t-s) a_t . b_s), or of the copy of the state that the
+ * row is multiplied with, which holds s0 or ds_final too.  Where terms cancel,
+ * the error is that of the terms, not of the result.  The carried state,
+ * s_final and ds0 are fp32 on either path: what is added to them is not rounded
+ * to bf16.
+ *
+ * A non-finite q, k or v reaches the rows that depend on it, and may reach
  * earlier rows of its own 64-token chunk; one behind a sequence's length
  * reaches nothing. */
 typedef struct {
@@ -352,8 +362,9 @@ m3_status m3_linattn_step_decode(const void *q_t, const void *k_t, const void *v
                                  void *y_t, void *stream);
 
 /* Gradients, contiguous, in the shapes and the dtype of their inputs (ds0 in
- * fp32), each rounded once from an fp32 sum; NULL = not wanted.  log_decay is
- * a constant: it has no gradient. */
+ * fp32), with the roundings above; NULL = not wanted.  Those of shared heads are
+ * kept in fp32 for each head until they are summed.  log_decay is a constant:
+ * it has no gradient. */
 typedef struct {
     void *dq, *dk, *dv;
     float *ds0;
@@ -387,7 +398,8 @@ size_t m3_linattn_workspace_bytes(int which, m3_linattn_dims d, m3_dtype dtype);
  *   y = act(u) without a gate, u act(gate) with one
  * channels <= 16384 and a multiple of ngroups; batch * ngroups < 2^31.  With
  * no rows (batch or seqlen 0) dweight and dbias are written as zeros and
- * nothing else is. */
+ * nothing else is.  An infinity or a NaN makes rstd, and so all of its group's y
+ * and dx, NaN; other groups do not see it. */
 typedef enum { M3_ACT_NONE = 0, M3_ACT_SILU = 1, M3_ACT_GELU = 2, M3_ACT_RELU = 3 } m3_act; /* GELU: the erf form */
 
 typedef struct {

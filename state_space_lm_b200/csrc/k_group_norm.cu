@@ -902,7 +902,8 @@ struct Plan {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Row plan: groups of one token that a block can hold in registers (4096
-// bf16, 8192 fp32 channels, 2048 without vectors).  Otherwise the seq plan.
+// bf16, 8192 fp32 channels, 2048 without vectors; the backward of more than 4096
+// fp32 channels spills up to 520 bytes a thread).  Otherwise the seq plan.
 // Vectors of 16 bytes where the group is a whole number of them (every base
 // address is 16-byte aligned), else single elements.
 Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd) {
@@ -931,8 +932,10 @@ Plan plan_of(int64_t Bt, int64_t L, int64_t C, int64_t G, m3_dtype dt, bool bwd)
             p.blocks = (unsigned)blocks;
             return p;
         }
-        // backward: the CTAs that are resident at once, at least two rows a
-        // team; always enough teams for one of each group
+        // backward: at most two CTAs for each SM, at least two rows a team; always
+        // enough teams for one of each group.  Two are resident at once up to 128
+        // registers a thread; a lane that holds 16 bf16 or from 16 fp32 channels
+        // takes 148 to 255, one CTA to an SM, and the blocks come in two turns
         blocks = (blocks + 1) / 2;
         if (blocks > 148 * 2) blocks = 148 * 2;
         if (blocks < need) blocks = need;

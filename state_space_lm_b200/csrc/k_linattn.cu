@@ -23,7 +23,7 @@ namespace {
 // would round, and of sizes that TMA cannot address.  Bound by the chain of a
 // lane's blocks at small sizes (3 x 333 tokens, 5 heads of 37 x 29, cut into
 // segments: 24 us), by arithmetic and shared-memory reads at large ones (8 x 2048,
-// 16 heads of 128 x 64: 673 us forward, 2214 backward).
+// 16 heads of 128 x 64: 680 us forward, 2227 backward).
 constexpr int SC = 16, SP = 32, ST = 256;
 
 template <int RS>
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(256) k_head_sum(HeadSum a) {
 // contiguous; the y sums over rows meet in shared memory.  The first rows of
 // the state are on their way before anything else is read (a lane of 128 x 64
 // then has its whole 32 KB in flight).  Bound by the state's bytes: 512 x 16
-// lanes of 128 x 64 in 87 us, 95 % of the copy rate.
+// lanes of 128 x 64 in 86 to 87 us, 95 % of the copy rate.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) k_lin_step(LinStepArgs a) {
     __shared__ float qs[256], ks[256], vs[256];

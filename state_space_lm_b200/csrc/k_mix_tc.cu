@@ -29,13 +29,17 @@
 // A split time axis takes two passes: B and C alone for every segment's own
 // state, the combine of linattn.cuh, then all segments at once.
 //
-// Measured: 8 x 2048 tokens, 16 heads of 128 x 64, 45 us for 206 MB (69 % of the
-// copy rate), on 128 of the 148 SMs; the backward's dq and dk 143 us, dv 45.
-// Bound by the shared memory pipe: a chunk takes 2225 cycles, and the tensor
-// core's operands, the epilogues and TMA need about 2290 cycles of it between
-// them.  One persistent CTA to an SM instead of one to a lane was slower at
-// long sequences (220 us for the backward, 195 here) and faster at hundreds of
-// single chunks (512 x 64 tokens: 288 us, 338 here).
+// Measured: 8 x 2048 tokens, 16 heads of 128 x 64, 43 to 45 us with the clock for
+// 206 MB (69 % of the copy rate), on 128 of the 148 SMs; the backward's dq and dk
+// 128 to 141 us, dv 42 to 46.  No unit is at its limit there: of an SM's active
+// cycles (about 2300 a chunk) the issue slots are busy for 57 %, tensor memory for
+// 50, the tensor pipe for 44, the LSU's data pipe for 42; DRAM is at 49 %.  What is
+// left are the hand-overs between the roles, each a chain of waits, fences and
+// latencies: 1.2 of a scheduler's 6 warps are ready at a time.  (768 threads leave
+// 80 registers a thread; the wide variant spills 12 bytes.)  One persistent CTA to
+// an SM instead of one to a lane was slower at long sequences (220 us for the
+// backward, 195 here) and faster at hundreds of single chunks (512 x 64 tokens: 288
+// us, 338 here).
 //
 // The problems of a call (three in the backward) share one launch.  Every
 // wait is bounded: past ~1 s the kernel records the site, stops issuing work,
@@ -280,8 +284,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_mix_tc(const __grid_constant__ B
                 if (elect_one()) {
                     const uint64_t db = d_mn0 + st * ST + AB, dw = d_cw0 + pb * (3 * TT);
                     // the three pieces side by side in N = 192: B is read once,
-                    // not three times (shared-memory bandwidth is the limit of
-                    // the loop), and the state warps add them up
+                    // not three times, and the state warps add them up (forward
+                    // 51 -> 50 us)
 #pragma unroll
                     for (int kk = 0; kk < 4; kk++) umma(tmem + COL_D, db + kk * MN, dw + kk * MN, id_st, kk > 0);
                     umma_commit(bar(B_DFULL));
@@ -818,11 +822,12 @@ static bool rows_map(CUtensorMap *m, const void *base, int64_t d, int64_t heads,
 
 }  // namespace mixtc
 
-// Up to 256 lanes of up to 16 tokens are one block each of the fp32 kernel, which
-// takes about as long and has no operand rounding.  128 x 64 states, 16 tokens
-// there against 17 here, forward and backward: 16 lanes 6.9 and 16.5 us against
-// 7.0 and 13.2, 256 lanes 17.6 and 48.8 against 14.3 and 54.1; 1024 lanes'
-// forward is 61 us there against 49 here (with the calls' host time).
+// Up to 256 lanes of up to 16 tokens are one block each of the fp32 kernel, for
+// its exactness: a few tokens behind a prompt are then as exact as single steps.  It
+// costs little: 128 x 64 states, 16 tokens there against 17 here, forward and
+// backward, replayed with a cold L2: 16 lanes 12.3 and 18.5 us against 10.3 and
+// 20.5, 256 lanes 22.5 and 59.4 against 18.4 and 60.  With 1024 lanes it would be
+// a fifth more (forward 61 us there, 49 here).
 bool mix_tc_sizes(const MixArgs &g, m3_dtype dt) {
     if (dt != M3_BF16 || g.da > mixtc::DA || g.dc > mixtc::DA || g.da % 8 || g.dc % 8 || g.T < 1) return false;
     if (g.T <= 16 && g.Bt * g.H <= 256) return false;

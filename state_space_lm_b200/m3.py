@@ -654,7 +654,9 @@ def linattn_chunked_fwd(q, k, v, log_decay, scale=None, s0=None, lengths=None, w
     int32 on the device or None: tokens behind a sequence's length are left
     out and their rows of y are zeros.  Returns y (Bt,T,H,dv) and s_final
     (Bt,H,dk,dv) fp32, the state for linattn_step_decode; ``out`` may hold
-    both (s_final None when it is not wanted)."""
+    both (s_final None when it is not wanted; like every output they must not
+    overlap an input).  bf16 on the tensor cores: each term of y meets one
+    rounding to bf16 before its fp32 sum; s_final does not (include/m3.h)."""
     if stream is not None:
         return _on(stream, v, linattn_chunked_fwd, q, k, v, log_decay, scale, s0, lengths, workspace, out)
     w, f = "m3_linattn_chunked_fwd", torch.float32
