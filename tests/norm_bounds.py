@@ -16,9 +16,15 @@ from lin_reference import U
 F32 = U[torch.float32]
 
 
-def roundings(B, L, D):
+def roundings(x, L, groups):
+    B, C = x.shape[0], x.shape[-1]
+    D = C // groups
+    wide = 8 if x.dtype == torch.bfloat16 else 4
+    vec = C // (wide if D % wide == 0 else 1)
+    phases = max(1, 256 // vec)                             # threads that share a vector's tokens
     nch = max(1, min(296 // max(B, 1), -(-L // 4)))         # chunks of a sequence
-    return 32 + 5 + 8 + 32 + 2 * -(-L // nch) + nch / 8 + D / 32 + 16
+    tokens = -(-(-(-L // nch)) // phases)                   # of a thread
+    return 32 + 5 + 8 + phases + 2 * tokens + nch / 8 + D / 32 + 16
 
 
 def act_parts(act, v):
@@ -46,15 +52,18 @@ def forward(x, groups, w, b, gate, act, eps=1e-5):
     io, C, B = x.dtype, x.shape[-1], x.shape[0]
     xg = x.double().reshape(B, -1, groups, C // groups)
     L = xg.shape[1]
-    R = roundings(B, L, C // groups)
+    R = roundings(x, L, groups)
     over = lambda t: t[:, None, :, None]                   # noqa: E731
     mean = xg.mean((1, 3))
     d = xg - over(mean)
     var = d.square().mean((1, 3))
     rstd = (var + eps) ** -0.5
     far = d.abs().amax((1, 3))
-    # one token: the values themselves are summed; more: differences from one of them
-    e_mean = R * F32 * (xg.abs().mean((1, 3)) if L == 1 else d.abs().mean((1, 3)) + far) + F32 * mean.abs()
+    # one token: the values themselves are summed; more: differences from one of
+    # them, which is added again by the thread, the phases' merge, the vectors'
+    # merge and the chunks' merge: four roundings of the mean's own size
+    e_mean = (R * F32 * xg.abs().mean((1, 3)) + F32 * mean.abs() if L == 1
+              else R * F32 * (d.abs().mean((1, 3)) + far) + 4 * F32 * mean.abs())
     # squares of differences from the computed mean, or from a value, far^2 from it
     e_var = R * F32 * (var if L == 1 else 2 * (var + far ** 2)) + e_mean ** 2 + 2 * e_mean * F32 * far
     e_rstd = rstd * (0.5 * e_var / (var + eps) + 4 * F32)
@@ -84,7 +93,7 @@ def backward(x, dy, mean, rstd, groups, w, b, gate, act, leave_out=()):
     D = C // groups
     xg = x.double().reshape(B, -1, groups, D)
     L = xg.shape[1]
-    R = roundings(B, L, D)
+    R = roundings(x, L, groups)
     over = lambda t: t.double()[:, None, :, None]          # noqa: E731
     group = lambda t: t.reshape(B, L, groups, D)           # noqa: E731
     xh = ((xg - over(mean)) * over(rstd)).reshape(x.shape)

@@ -69,6 +69,16 @@ def test_a_large_mean():
             check(shape, groups, "f32", False, act, shift=4096.0)
 
 
+# phases of a vector that share its tokens: 256, 85 and 64 of them; hundreds of
+# sequences, one chunk each
+@pytest.mark.parametrize("shape,groups", [((300, 1000, 4), 1), ((2, 3000, 4), 1), ((3, 3000, 8), 2), ((1, 3000, 3), 3), ((308, 6, 3), 3),
+                                          ((928, 3, 3), 3), ((310, 3, 8), 8), ((40, 900, 16), 1)],
+                         ids=lambda s: "x".join(map(str, s)) if isinstance(s, tuple) else str(s))
+def test_the_mean_of_means(shape, groups):
+    for shift in (100.0, 4096.0, -4096.0):
+        check(shape, groups, "f32", False, "none", shift=shift)
+
+
 def test_no_weight_and_no_bias():
     for shape in ((50, 64), (2, 30, 64)):
         check(shape, 4, "f32", False, "gelu", affine=False)
